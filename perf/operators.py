@@ -10,11 +10,13 @@ torch operations (32-bit), with ``own`` true through this package's binding.
 Kinds of case:
   quantize  f32 or bfloat16 [M, K] -> E4M3 codes and one f32 scale per block of
             128 columns of a row (block_rows 1) or per 128 x 128 tile (128).
-  product   y[m, n] = sum_b as[m, b] ws[n / 128, b] sum_{k in b} a[m, k] w[n, k].
+  product   y[m, n] = sum_b as[m, b] ws[n / 128, b] sum_{k in b} a[m, k] w[n, k],
+            y in bfloat16 (the type the next layer's quantizer reads).
   route     logits [T, E] -> the top_k experts of each token, their softmax
             weights, and the slots (t, j) sorted by expert.
   grouped   y[r] = a[r / share] @ dequant(W[expert of r])^T for the slots r of
-            each expert, the weights Q4_0, Q8_0 or E4M3 with 128 x 128 scales.
+            each expert, the weights Q4_0 or Q8_0 (y in f32), or E4M3 with
+            128 x 128 scales (y in bfloat16).
 """
 import math
 
@@ -88,7 +90,7 @@ def work(case):
     if c["kind"] == "product":
         M, N, K = c["M"], c["N"], c["K"]
         kb = -(-K // 128)
-        return {"bytes": M * K + 4 * M * kb + N * K + 4 * -(-N // 128) * kb + 4 * M * N, "flops": 2 * M * N * K}
+        return {"bytes": M * K + 4 * M * kb + N * K + 4 * -(-N // 128) * kb + 2 * M * N, "flops": 2 * M * N * K}
     if c["kind"] == "route":
         S = c["T"] * c["top_k"]
         return {"bytes": 4 * c["T"] * c["E"] + 12 * S + 4 * (c["E"] + 1), "flops": 4 * c["T"] * c["E"]}
@@ -96,10 +98,10 @@ def work(case):
     hit = min(c["E"], S)     # experts with a row, at most: each one's weights are read once
     if c["fmt"] == "f8":
         kb = -(-K // 128)
-        per_w, per_a = N * K + 4 * -(-N // 128) * kb, K + 4 * kb
+        per_w, per_a, out = N * K + 4 * -(-N // 128) * kb, K + 4 * kb, 2
     else:
-        per_w, per_a = N * (K // 32) * BLOCK_BYTES[c["fmt"]], K * (4 if c["act"] == "f32" else 2)
-    return {"bytes": hit * per_w + S // c["share"] * per_a + 4 * S * N + 4 * (S + c["E"] + 1), "flops": 2 * S * N * K}
+        per_w, per_a, out = N * (K // 32) * BLOCK_BYTES[c["fmt"]], K * (4 if c["act"] == "f32" else 2), 4
+    return {"bytes": hit * per_w + S // c["share"] * per_a + out * S * N + 4 * (S + c["E"] + 1), "flops": 2 * S * N * K}
 
 
 # ---------------------------------------------------------------------------
@@ -188,7 +190,7 @@ def prepare(case, seed):
     elif c["kind"] == "product":
         st["a"], st["a_s"] = _quantize(_activations(g, c["M"], c["K"], dev), 1)
         st["w"], st["w_s"] = _quantize(0.02 * torch.randn(c["N"], c["K"], generator=g, device=dev), 128)
-        st["y"] = torch.empty(c["M"], c["N"], device=dev)
+        st["y"] = torch.empty(c["M"], c["N"], dtype=torch.bfloat16, device=dev)
     elif c["kind"] == "route":
         # Router outputs are often computed in bfloat16: equal logits occur.
         st["logits"] = _logits(g, c["T"], c["E"], 0.5, dev).to(torch.bfloat16).float()
@@ -214,7 +216,7 @@ def prepare(case, seed):
             st["w"] = torch.empty(E, N, K // 32, BLOCK_BYTES[c["fmt"]], dtype=torch.uint8, device=dev)
             for e in range(E):
                 st["w"][e] = _gguf(0.02 * torch.randn(N, K, generator=g, device=dev), c["fmt"])
-        st["y"] = torch.empty(S, N, device=dev)
+        st["y"] = torch.empty(S, N, dtype=torch.bfloat16 if c["fmt"] == "f8" else torch.float32, device=dev)
     return st
 
 
@@ -231,7 +233,7 @@ def run(state):
         M, N, K = c["M"], c["N"], c["K"]
         a = st["a"].float() * _spread(st["a_s"], 1, M, K, torch.float32)
         w = st["w"].float() * _spread(st["w_s"], 128, N, K, torch.float32)
-        return a @ w.t()
+        return (a @ w.t()).to(torch.bfloat16)
     if c["kind"] == "route":
         x = st["logits"]
         top, ids = torch.sort(x, dim=1, descending=True, stable=True)
@@ -260,8 +262,8 @@ def _grouped(st, c):
         w = _ungguf(st["w"][hit], c["fmt"], torch.float32)
     x = a[rows // c["share"]].transpose(1, 2).contiguous()
     out = torch.bmm(w, x).transpose(1, 2)
-    y = torch.empty(order.numel(), N, device=off.device)
-    y[rows[there]] = out[there]
+    y = torch.empty(order.numel(), N, dtype=st["y"].dtype, device=off.device)
+    y[rows[there]] = out[there].to(y.dtype)
     return y
 
 
