@@ -40,6 +40,11 @@ EXPORTS = ("q4_abi_version", "q4_status_string", "q4_dequant", "q4_gemv", "q4_ge
            "q8_gemv_prepared", "q4_gemv_q8a", "q8_gemv_q8a", "q4_gemm_q8a",
            "q4_gemm_q8a_workspace_bytes", "q8_gemm_q8a", "q8_gemm_q8a_workspace_bytes")
 
+#: Every symbol include/f8.h declares.
+F8_EXPORTS = ("f8_quantize", "f8_quantize_bf16", "f8_dequant", "f8_gemm", "f8_gemv")
+F8_BLOCK = 128
+F8_MAX_K = 4194304
+
 
 class Q4Error(RuntimeError):
     def __init__(self, status: int, entry: str):
@@ -96,6 +101,11 @@ def _load_library():
     for name in ("q8_quantize", "q4_quantize"):
         getattr(lib, name).restype = i32
         getattr(lib, name).argtypes = [P, sz, P, sz, P]
+    for name in F8_EXPORTS:
+        getattr(lib, name).restype = i32
+    lib.f8_quantize.argtypes = lib.f8_quantize_bf16.argtypes = [P, i32, i32, i32, P, sz, P, sz, P]
+    lib.f8_dequant.argtypes = [P, sz, P, sz, i32, i32, i32, P, sz, P]
+    lib.f8_gemm.argtypes = lib.f8_gemv.argtypes = [P, P, P, sz, P, P, i32, i32, i32, P]
     return lib
 
 
@@ -429,6 +439,55 @@ def q4_quantize(x, out_q, n_elems=None, out_bytes=None, stream=None) -> None:
     n = int(x.numel()) if n_elems is None else int(n_elems)
     ob = _nbytes(out_q) if out_bytes is None else int(out_bytes)
     _check(lib.q4_quantize(_addr(x), n, _addr(out_q), ob, _stream(stream)), "q4_quantize")
+
+
+def _f8_quantize(entry, x, q, s, M, K, block_rows, q_bytes, s_elems, stream) -> None:
+    qb = _nbytes(q) if q_bytes is None else int(q_bytes)
+    se = int(s.numel()) if s_elems is None else int(s_elems)
+    _check(getattr(lib, entry)(_addr(x), int(M), int(K), int(block_rows), _addr(q), qb, _addr(s),
+                               se, _stream(stream)), entry)
+
+
+def f8_quantize(x, q, s, M: int, K: int, block_rows: int = 1, q_bytes=None, s_elems=None,
+                stream=None) -> None:
+    """f32 ``x`` [M, K] -> E4M3 codes ``q`` [M, K] (uint8 or float8_e4m3fn) and f32
+    scales ``s``, one per 128 columns of a row (``block_rows=1``, activations)
+    or per 128 x 128 tile (``block_rows=128``, weights)."""
+    _f8_quantize("f8_quantize", x, q, s, M, K, block_rows, q_bytes, s_elems, stream)
+
+
+def f8_quantize_bf16(x, q, s, M: int, K: int, block_rows: int = 1, q_bytes=None, s_elems=None,
+                     stream=None) -> None:
+    """As f8_quantize with ``x`` a [M, K] bfloat16 tensor (or its address)."""
+    _f8_quantize("f8_quantize_bf16", x, q, s, M, K, block_rows, q_bytes, s_elems, stream)
+
+
+def f8_dequant(q, s, out, M: int, K: int, block_rows: int = 1, q_bytes=None, s_elems=None,
+               out_elems=None, stream=None) -> None:
+    """E4M3 codes and scales -> f32 ``out`` [M, K]."""
+    qb = _nbytes(q) if q_bytes is None else int(q_bytes)
+    se = int(s.numel()) if s_elems is None else int(s_elems)
+    oe = int(out.numel()) if out_elems is None else int(out_elems)
+    _check(lib.f8_dequant(_addr(q), qb, _addr(s), se, int(M), int(K), int(block_rows), _addr(out),
+                          oe, _stream(stream)), "f8_dequant")
+
+
+def _f8_product(entry, a, a_s, w, w_s, y, M, N, K, w_bytes, stream) -> None:
+    wb = _nbytes(w) if w_bytes is None else int(w_bytes)
+    _check(getattr(lib, entry)(_addr(a), _addr(a_s), _addr(w), wb, _addr(w_s), _addr(y), int(M),
+                               int(N), int(K), _stream(stream)), entry)
+
+
+def f8_gemm(a, a_s, w, w_s, y, M: int, N: int, K: int, w_bytes=None, stream=None) -> None:
+    """y[M, N] (bfloat16) = a @ w^T for any M, both in E4M3 with a scale for each
+    block of 128: ``a`` [M, K] with ``a_s`` [M, ceil(K/128)], ``w`` [N, K] with
+    ``w_s`` [ceil(N/128), ceil(K/128)]."""
+    _f8_product("f8_gemm", a, a_s, w, w_s, y, M, N, K, w_bytes, stream)
+
+
+def f8_gemv(a, a_s, w, w_s, y, M: int, N: int, K: int, w_bytes=None, stream=None) -> None:
+    """f8_gemm for 1 <= M <= 8 rows."""
+    _f8_product("f8_gemv", a, a_s, w, w_s, y, M, N, K, w_bytes, stream)
 
 
 def raw_status(entry: str, *args) -> int:

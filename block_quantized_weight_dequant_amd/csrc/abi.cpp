@@ -1,6 +1,8 @@
-// The exported C ABI (include/q4.h): validate every argument, then enqueue the
-// kernel on the caller's stream. Only the functions declared in q4.h are
-// exported from the shared library (it is built with hidden visibility).
+// The exported C ABI (include/q4.h, include/f8.h): validate every argument,
+// then enqueue the kernel on the caller's stream. Only the functions declared
+// there are exported from the shared library (it is built with hidden
+// visibility).
+#include "f8.h"
 #include "q4.h"
 
 #include "launch.h"
@@ -395,4 +397,61 @@ Q4_EXPORT int q8_gemm_q8a(const void *a_q, size_t a_bytes, const void *w_q, size
 {
     return gemm_q8a(q4k::WeightFormat::kQ8_0, 34, a_q, a_bytes, w_q, w_bytes, y, M, N, K,
                     workspace, workspace_bytes, stream);
+}
+
+Q4_EXPORT int f8_quantize(const float *x, int M, int K, int block_rows, void *q, size_t q_bytes,
+                          float *s, size_t s_elems, void *stream)
+{
+    bool empty = false;
+    int st = q4v::check_f8_codec(x, 4, M, K, block_rows, q, q_bytes, s, s_elems, false, &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    return launched(q4k::launch_f8_quantize(x, static_cast<uint8_t *>(q), s, M, K, block_rows,
+                                            as_stream(stream)));
+}
+
+Q4_EXPORT int f8_quantize_bf16(const uint16_t *x, int M, int K, int block_rows, void *q,
+                               size_t q_bytes, float *s, size_t s_elems, void *stream)
+{
+    bool empty = false;
+    int st = q4v::check_f8_codec(x, 2, M, K, block_rows, q, q_bytes, s, s_elems, false, &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    return launched(q4k::launch_f8_quantize_bf16(x, static_cast<uint8_t *>(q), s, M, K, block_rows,
+                                                 as_stream(stream)));
+}
+
+Q4_EXPORT int f8_dequant(const void *q, size_t q_bytes, const float *s, size_t s_elems, int M,
+                         int K, int block_rows, float *out, size_t out_elems, void *stream)
+{
+    bool empty = false;
+    int st = q4v::check_f8_codec(out, 4, M, K, block_rows, q, q_bytes, s, s_elems, true, &empty);
+    if (st != Q4_ERR_SHAPE && out_elems != q_bytes)   // q_bytes is M K, or the size error is its own
+        return Q4_ERR_SIZE;
+    if (st != Q4_OK || empty)
+        return st;
+    return launched(q4k::launch_f8_dequant(static_cast<const uint8_t *>(q), s, out, M, K,
+                                           block_rows, as_stream(stream)));
+}
+
+static int f8_product(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,
+                      const float *w_s, uint16_t *y, int M, int N, int K, int max_rows, void *stream)
+{
+    bool empty = false;
+    int st = q4v::check_f8_product(a, a_s, w, w_bytes, w_s, y, M, N, K, max_rows, &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    return launched(q4k::launch_f8_gemm(a, a_s, w, w_s, y, M, N, K, as_stream(stream)));
+}
+
+Q4_EXPORT int f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,
+                      const float *w_s, uint16_t *y, int M, int N, int K, void *stream)
+{
+    return f8_product(a, a_s, w, w_bytes, w_s, y, M, N, K, 0, stream);
+}
+
+Q4_EXPORT int f8_gemv(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,
+                      const float *w_s, uint16_t *y, int M, int N, int K, void *stream)
+{
+    return f8_product(a, a_s, w, w_bytes, w_s, y, M, N, K, Q4_GEMV_MAX_ROWS, stream);
 }

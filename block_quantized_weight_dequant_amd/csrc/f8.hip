@@ -1,0 +1,750 @@
+// E4M3 (8-bit floating point, 4 exponent and 3 fraction bits, no infinities,
+// largest value 448) with one f32 scale for each block of 128: the quantizers,
+// the decode, and the product y = (a_s a) @ (w_s w)^T, also grouped by expert.
+//
+// Layout: activations are codes [M, K] with scales [M, ceil(K / 128)] (one per
+// 128 columns of a row), weights codes [N, K] with scales [ceil(N / 128),
+// ceil(K / 128)] (one per 128 x 128 tile), all row-major; a row's last block
+// may be short.
+#include "device_common.h"
+#include "groups.h"
+#include "launch.h"
+
+namespace q4k {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kE4M3Max = 448.0f;
+
+// ---------------------------------------------------------------------------
+// Quantize. Per block: s = max|x| / 448 in f32, code = the E4M3 value nearest
+// to x / s (ties to even), the quotient rounded once to f32 and clamped to
+// +-448 (it can pass that only where s is subnormal); s == 0 stores zeros.
+// Bound by the bytes of x: 16 lanes share a block of a row, eight elements
+// each, so a wavefront reads four blocks (2 KB of f32) and writes 512 bytes
+// of codes in whole lines, and the maximum crosses 16 lanes in four DPP moves.
+
+__device__ __forceinline__ float f32_of(float v) { return v; }
+__device__ __forceinline__ float f32_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+template <class T>
+struct Eight {
+    float v[8];
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (sizeof(T) == 4) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = a[i], v[4 + i] = b[i];
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void clear_if(bool c)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c ? 0.0f : v[i];
+    }
+    __device__ __forceinline__ float amax() const
+    {
+        float m = fabsf(v[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            m = fmaxf(m, fabsf(v[i]));
+        return m;
+    }
+    __device__ __forceinline__ u32x2 codes(float s) const
+    {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = s == 0.0f ? 0.0f : fminf(fmaxf(v[i] / s, -kE4M3Max), kE4M3Max);
+        u32x2 r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int x = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
+            r[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], x, true);
+        }
+        return r;
+    }
+};
+
+// Largest over each 16 lanes, in every one of them.
+__device__ __forceinline__ float max16(float v)
+{
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));    // quad_perm 1,0,3,2
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));    // quad_perm 2,3,0,1
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));   // row_half_mirror
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));   // row_mirror
+    return v;
+}
+
+// One scale per 128 columns of a row. 16 R blocks per 256-thread workgroup.
+template <class T, int R>
+__global__ __launch_bounds__(256) void k_f8_quantize_rows(const T *__restrict__ x,
+                                                         uint8_t *__restrict__ q,
+                                                         float *__restrict__ s, int K, unsigned Kb,
+                                                         unsigned n_blocks)
+{
+    const unsigned tid = threadIdx.x, p = tid & 15;
+    const unsigned b0 = blockIdx.x * (16u * R) + (tid >> 4);
+    Eight<T> v[R];
+    size_t at[R];
+    bool in[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        // Unconditional loads, from a valid place where the lane has none: a
+        // load under a branch would be waited for before the next one.
+        const unsigned b = min(b0 + 16 * r, n_blocks - 1);
+        const unsigned row = b / Kb, col = (b - row * Kb) * 128 + 8 * p;
+        in[r] = col < (unsigned)K;
+        at[r] = (size_t)row * (size_t)K + (in[r] ? col : 0u);
+        v[r].load(x + at[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        v[r].clear_if(!in[r]);
+        const float sc = max16(v[r].amax()) / kE4M3Max;
+        const unsigned b = b0 + 16 * r;
+        if (b < n_blocks) {
+            if (in[r])
+                *reinterpret_cast<u32x2 *>(q + at[r]) = v[r].codes(sc);
+            if (p == 0)
+                s[b] = sc;
+        }
+    }
+}
+
+// One scale per 128 x 128 tile: a workgroup holds the tile in registers
+// (eight rows of eight elements a thread) between its maximum and its codes,
+// so x is read once.
+template <class T>
+__global__ __launch_bounds__(256) void k_f8_quantize_tiles(const T *__restrict__ x,
+                                                          uint8_t *__restrict__ q,
+                                                          float *__restrict__ s, int M, int K,
+                                                          int Kb)
+{
+    __shared__ float wave_max[4];
+    const int tid = threadIdx.x;
+    const int rb = blockIdx.x / Kb, kb = blockIdx.x - rb * Kb;
+    const int col = kb * 128 + 8 * (tid & 15);
+    const bool col_in = col < K;
+    const T *src = x + (col_in ? col : 0);
+    const int row0 = rb * 128 + (tid >> 4);
+    Eight<T> v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i].load(src + (size_t)min(row0 + 16 * i, M - 1) * (size_t)K);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i].clear_if(!col_in || row0 + 16 * i >= M);
+        m = fmaxf(m, v[i].amax());
+    }
+    m = max16(m);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    if ((tid & 63) == 0)
+        wave_max[tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+    const float sc = m / kE4M3Max;
+    if (tid == 0)
+        s[blockIdx.x] = sc;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = row0 + 16 * i;
+        if (col_in && row < M)
+            *reinterpret_cast<u32x2 *>(q + (size_t)row * (size_t)K + col) = v[i].codes(sc);
+    }
+}
+
+template <class T>
+static hipError_t launch_quantize_t(const T *x, uint8_t *q, float *s, int M, int K, int block_rows,
+                                    hipStream_t st)
+{
+    const unsigned Kb = (unsigned)(K + 127) / 128;
+    if (block_rows == 1) {
+        const unsigned nb = (unsigned)M * Kb;   // < 2^31, checked
+        // Four blocks a thread group where that still leaves four workgroups
+        // for each compute unit; otherwise one, for the spread.
+        if (nb >= 64u * 1024u)
+            return launch_kernel(k_f8_quantize_rows<T, 4>, dim3((nb + 63) / 64), dim3(256), 0, st,
+                                 x, q, s, K, Kb, nb);
+        return launch_kernel(k_f8_quantize_rows<T, 1>, dim3((nb + 15) / 16), dim3(256), 0, st, x,
+                             q, s, K, Kb, nb);
+    }
+    const unsigned Mb = (unsigned)(((long long)M + 127) / 128);
+    return launch_kernel(k_f8_quantize_tiles<T>, dim3(Mb * Kb), dim3(256), 0, st, x, q, s, M, K,
+                         (int)Kb);
+}
+
+hipError_t launch_f8_quantize(const float *x, uint8_t *q, float *s, int M, int K, int block_rows,
+                              hipStream_t st)
+{
+    return launch_quantize_t<float>(x, q, s, M, K, block_rows, st);
+}
+
+hipError_t launch_f8_quantize_bf16(const uint16_t *x, uint8_t *q, float *s, int M, int K,
+                                   int block_rows, hipStream_t st)
+{
+    return launch_quantize_t<uint16_t>(x, q, s, M, K, block_rows, st);
+}
+
+// ---------------------------------------------------------------------------
+// Decode: out = code * s, one rounding. A thread takes 16 codes.
+__global__ __launch_bounds__(256) void k_f8_dequant(const uint8_t *__restrict__ q,
+                                                   const float *__restrict__ s,
+                                                   float *__restrict__ out, int K, int Kb,
+                                                   int block_rows, size_t n16)
+{
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n16)
+        return;
+    const size_t e = i * 16, row = e / (size_t)K;
+    const int col = (int)(e - row * (size_t)K);   // K % 32 == 0: 16 codes never straddle rows
+    const float sc = s[(row / (size_t)block_rows) * (size_t)Kb + (size_t)(col >> 7)];
+    const u32x4 c = reinterpret_cast<const u32x4 *>(q)[i];
+    f32x4 *o = reinterpret_cast<f32x4 *>(out + e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], true);
+        o[j] = (f32x4){lo[0] * sc, lo[1] * sc, hi[0] * sc, hi[1] * sc};
+    }
+}
+
+hipError_t launch_f8_dequant(const uint8_t *q, const float *s, float *out, int M, int K,
+                             int block_rows, hipStream_t st)
+{
+    const size_t n16 = (size_t)M * (size_t)K / 16, grid = (n16 + 255) / 256;
+    if (grid > 0x7fffffffu)
+        return hipErrorInvalidValue;
+    return launch_kernel(k_f8_dequant, dim3((unsigned)grid), dim3(256), 0, st, q, s, out, K,
+                         (K + 127) / 128, block_rows, n16);
+}
+
+// ---------------------------------------------------------------------------
+// The product. v_mfma_f32_16x16x128_f8f6f4 contracts one whole block of 128
+// codes, so per 16 x 16 tile and block one matrix instruction gives the sum
+// over the block and one f32 FMA per element adds it, times a_s w_s, to the
+// accumulator. The weights are the A operand and the activations the B
+// operand: a lane's four results are then four columns of y of one row, one
+// activation scale serves a lane's whole tile column, and they are stored
+// together.
+//
+// Rounding: the instruction forms each run of eight products (the bytes a
+// lane's dword pair holds) against the largest of the eight, and drops what is
+// below 2^-13 of that one's power of two (measured on the card with one large
+// and one small product at every distance); the runs are added in f32. Every
+// other 8-bit matrix instruction of the card does the same. On N(0, 1) codes
+// that is 1.3e-5 of the result's norm, a hundredth of y's rounding to
+// bfloat16 (1.7e-3), and the reason y is bfloat16: an f32 result would claim
+// bits that the products do not have. (Widening the codes to binary16 first
+// would keep them, at half the matrix rate and eight conversions an operand.)
+// Blocks are added in f32 in K order.
+//
+// The K order within a block does not matter as long as both operands agree:
+// lane group g = lane / 16 takes bytes [16 g, 16 g + 16) and [64 + 16 g, 80 +
+// 16 g) of its row's block, so every 16-byte load is aligned.
+
+struct F8Product {
+    const uint8_t *a;
+    const float *a_s;
+    const uint8_t *w;
+    const float *w_s;
+    uint16_t *y;
+    int M, N, K, Kb, Nb;
+};
+
+__device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
+{
+    return (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+__device__ __forceinline__ f32x4 mfma_block(i32x8 w, i32x8 a)
+{
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// Columns n .. n + 3 of one row of y.
+__device__ __forceinline__ void store4(uint16_t *__restrict__ row, int n, int N, f32x4 v)
+{
+    const bf16x4 b = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    if ((N & 3) == 0) {
+        if (n < N)
+            *reinterpret_cast<bf16x4 *>(row + n) = b;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (n + q < N)
+                reinterpret_cast<__bf16 *>(row)[n + q] = b[q];
+    }
+}
+
+// Few rows: bound by the weights' bytes. A workgroup takes 16 weight rows and
+// up to 16 R activation rows; its eight wavefronts take the blocks of K in
+// turn, U at a time with all their loads in flight, straight into registers
+// (nothing is shared between wavefronts but the activations, which L1 and L2
+// serve), and add their partial tiles through LDS.
+constexpr int kSkinnyWaves = 8;
+
+template <int R, int U>
+__device__ __forceinline__ void skinny_tile(const F8Product &p, const uint8_t *__restrict__ w,
+                                            const float *__restrict__ w_s, int n0,
+                                            const int (&row)[R], const int (&arow)[R], f32x4 *red)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, g = lane >> 4;
+    const uint8_t *wp = w + (size_t)min(n0 + li, p.N - 1) * (size_t)p.K + 16 * g;
+    const float *wsp = w_s + (size_t)(n0 >> 7) * (size_t)p.Kb;
+    const uint8_t *ap[R];
+    const float *asp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        ap[r] = p.a + (size_t)arow[r] * (size_t)p.K + 16 * g;
+        asp[r] = p.a_s + (size_t)arow[r] * (size_t)p.Kb;
+    }
+    f32x4 acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        acc[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    const int full = p.K >> 7;   // whole blocks
+    auto run = [&](int kb, int n) __attribute__((always_inline)) {
+        u32x4 wl[U][2], al[U][R][2];
+        float ws[U], as[U][R];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = min(kb + u * kSkinnyWaves, full - 1);
+            wl[u][0] = *reinterpret_cast<const u32x4 *>(wp + (size_t)k * 128);
+            wl[u][1] = *reinterpret_cast<const u32x4 *>(wp + (size_t)k * 128 + 64);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = min(kb + u * kSkinnyWaves, full - 1);
+            ws[u] = u < n ? wsp[k] : 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                al[u][r][0] = *reinterpret_cast<const u32x4 *>(ap[r] + (size_t)k * 128);
+                al[u][r][1] = *reinterpret_cast<const u32x4 *>(ap[r] + (size_t)k * 128 + 64);
+                as[u][r] = asp[r][k];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u >= n)
+                break;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const f32x4 c = mfma_block(join(wl[u][0], wl[u][1]), join(al[u][r][0], al[u][r][1]));
+                const float s = as[u][r] * ws[u];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[r][q] = fmaf(s, c[q], acc[r][q]);
+            }
+        }
+    };
+    int kb = wave;
+    for (; kb + (U - 1) * kSkinnyWaves < full; kb += U * kSkinnyWaves)
+        run(kb, U);
+    if (kb < full)
+        run(kb, (full - kb + kSkinnyWaves - 1) / kSkinnyWaves);
+    if (full < p.Kb && wave == full % kSkinnyWaves) {
+        // The short last block: pieces past K are zero in both operands.
+        const int k0 = full * 128;
+        const bool in0 = k0 + 16 * g < p.K, in1 = k0 + 64 + 16 * g < p.K;
+        const u32x4 w0 = in0 ? *reinterpret_cast<const u32x4 *>(wp + k0) : zero;
+        const u32x4 w1 = in1 ? *reinterpret_cast<const u32x4 *>(wp + k0 + 64) : zero;
+        const float ws = wsp[full];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const u32x4 a0 = in0 ? *reinterpret_cast<const u32x4 *>(ap[r] + k0) : zero;
+            const u32x4 a1 = in1 ? *reinterpret_cast<const u32x4 *>(ap[r] + k0 + 64) : zero;
+            const f32x4 c = mfma_block(join(w0, w1), join(a0, a1));
+            const float s = asp[r][full] * ws;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[r][q] = fmaf(s, c[q], acc[r][q]);
+        }
+    }
+    // Partial tiles, [r][wave][lane]; wavefront r mod 8 adds tile r's eight in
+    // wavefront order.
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        red[(r * kSkinnyWaves + wave) * 64 + lane] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r % kSkinnyWaves != wave || row[r] < 0)
+            continue;
+        f32x4 v = red[r * kSkinnyWaves * 64 + lane];
+#pragma unroll
+        for (int s = 1; s < kSkinnyWaves; ++s)
+            v += red[(r * kSkinnyWaves + s) * 64 + lane];
+        store4(p.y + (size_t)row[r] * (size_t)p.N, n0 + 4 * g, p.N, v);
+    }
+}
+
+template <int R>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void k_f8_skinny(F8Product p)
+{
+    __shared__ f32x4 red[R * kSkinnyWaves * 64];
+    const int li = threadIdx.x & 15, m0 = blockIdx.y * (16 * R);
+    int row[R], arow[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int m = m0 + 16 * r + li;
+        row[r] = m < p.M ? m : -1;
+        arow[r] = min(m, p.M - 1);
+    }
+    constexpr int U = R == 1 ? 4 : R == 2 ? 4 : R == 4 ? 2 : 1;
+    skinny_tile<R, U>(p, p.w, p.w_s, blockIdx.x * 16, row, arow, red);
+}
+
+// The same over groups: workgroup (x, e) takes 16 weight rows of group e
+// through the group's rows, 16 R at a time.
+template <int R>
+__device__ __forceinline__ void skinny_rows(const F8Product &p, const Groups &gr,
+                                            const uint8_t *w, const float *w_s, int lo, int hi,
+                                            f32x4 *red)
+{
+    const int li = threadIdx.x & 15;
+    int row[R], arow[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int at = lo + 16 * r + li;
+        row[r] = at < hi ? group_row(gr, at) : -1;
+        arow[r] = max(row[r], 0) / gr.share;
+    }
+    constexpr int U = R == 1 ? 4 : 2;
+    skinny_tile<R, U>(p, w, w_s, blockIdx.x * 16, row, arow, red);
+}
+
+__global__ __launch_bounds__(64 * kSkinnyWaves) void k_f8_skinny_grouped(F8Product p, Groups gr)
+{
+    __shared__ f32x4 red[4 * kSkinnyWaves * 64];
+    const int e = blockIdx.y;
+    int lo, hi;
+    group_bounds(gr, e, lo, hi);
+    const uint8_t *w = p.w + (size_t)e * (size_t)p.N * (size_t)p.K;
+    const float *w_s = p.w_s + (size_t)e * (size_t)p.Nb * (size_t)p.Kb;
+    while (lo < hi) {
+        if (hi - lo <= 16) {
+            skinny_rows<1>(p, gr, w, w_s, lo, hi, red);
+            return;
+        }
+        if (hi - lo <= 32) {
+            skinny_rows<2>(p, gr, w, w_s, lo, hi, red);
+            return;
+        }
+        skinny_rows<4>(p, gr, w, w_s, lo, hi, red);
+        lo += 64;
+        __syncthreads();   // red is read before the next rows write it
+    }
+}
+
+// Many rows: bound by the matrix instructions. A workgroup of eight wavefronts
+// computes BN x BM of y^T. Per step of 128 KG of K it stages both operands and
+// the activation scales in LDS by direct loads, one stage ahead; 16-byte
+// pieces of a row's 128 bytes are stored at piece ^ (row % 8), so that the 8
+// rows that an LDS read serves at a time lie in different banks (the lanes'
+// global addresses carry the permutation; the LDS side of a direct load is
+// contiguous).
+//   WN x WM wavefronts of TN x TM tiles each, KG groups of them: with KG = 2
+//   the second group takes the odd blocks of K and the two tiles are added
+//   through LDS at the end, so that a small tile still has two wavefronts a
+//   SIMD and one's FMAs run beside the other's matrix instructions.
+template <int WN_, int WM_, int TN_, int TM_, int KG_>
+struct TileShape {
+    static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, KG = KG_;
+    static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
+    static constexpr int kThreads = 64 * WN * WM * KG;
+    static constexpr int kWLoads = BN * 8 * KG / kThreads, kALoads = BM * 8 * KG / kThreads;
+    static constexpr int kSWaves = BM * KG / 64;   // wavefronts that load scales
+    static_assert(BN * 8 * KG % kThreads == 0 && BM * 8 * KG % kThreads == 0 && BM * KG % 64 == 0, "whole loads");
+    static_assert(kSWaves <= kThreads / 64, "one scale load a wavefront");
+    static_assert(TN * 16 <= 128 && 128 % (TN * 16) == 0, "a wavefront's columns share a weight scale");
+};
+
+template <class S>
+struct TileLds {
+    u32x4 w[2][S::KG * S::BN * 8];
+    u32x4 a[2][S::KG * S::BM * 8];
+    float s[2][S::KG * S::BM];
+    int row[S::BM];
+};
+
+constexpr uint32_t kOutOfRange = 0x80000000u;   // past every resource below (each spans at most 2^31 bytes)
+constexpr int kRawBuffer = 0x00020000;          // resource word 3: raw, 32-bit data format
+
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Direct-to-LDS loads of 16 and of 4 bytes a lane: lane l's bytes go to dst +
+// 16 l (4 l).
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, base, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 4, off, base, 0, 0);
+}
+
+template <class S, bool GROUPED>
+__global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, int tiles_m,
+                                                          int tiles_n)
+{
+    __shared__ TileLds<S> lds;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int mt, nt, rows;
+    const uint8_t *w = p.w;
+    const float *w_s = p.w_s;
+    if constexpr (GROUPED) {
+        const GroupTile g = find_group_tile(gr, xcd_runs(blockIdx.x), S::BM, tiles_n);
+        if (g.e < 0)
+            return;
+        mt = g.mt, nt = g.nt;
+        const int lo = g.lo + mt * S::BM;
+        rows = min(S::BM, g.hi - lo);
+        w += (size_t)g.e * (size_t)p.N * (size_t)p.K;
+        w_s += (size_t)g.e * (size_t)p.Nb * (size_t)p.Kb;
+        if (tid < S::BM)
+            lds.row[tid] = tid < rows ? group_row(gr, lo + tid) : -1;
+        __syncthreads();
+    } else {
+        // XCD x (workgroup index mod 8) takes a contiguous run of the tiles,
+        // row tiles fastest: its L2 holds few weight columns at a time.
+        const int T = tiles_m * tiles_n, per = (T + 7) / 8;
+        const int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+        if ((int)(blockIdx.x >> 3) >= per || t >= T)
+            return;
+        nt = t / tiles_m, mt = t - nt * tiles_m;
+        rows = min(S::BM, p.M - mt * S::BM);
+    }
+    const int n0 = nt * S::BN, m0 = mt * S::BM;
+    const int li = lane & 15, g = lane >> 4;
+    const int kg = wave / (S::WN * S::WM), wn = wave % S::WN, wm = (wave / S::WN) % S::WM;
+
+    // Resources: this tile's weight rows; its activation rows and scales, or
+    // (grouped) all of them.
+    const int wrows = min(S::BN, p.N - n0);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w + (size_t)n0 * (size_t)p.K), (short)0, (int)((uint32_t)wrows * (uint32_t)p.K), kRawBuffer);
+    const size_t am0 = GROUPED ? 0 : (size_t)m0;
+    const uint32_t arows = GROUPED ? (uint32_t)((gr.M - 1) / gr.share + 1) : (uint32_t)rows;
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(p.a + am0 * (size_t)p.K), (short)0, (int)(arows * (uint32_t)p.K), kRawBuffer);
+    const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(p.a_s + am0 * (size_t)p.Kb), (short)0, (int)(arows * (uint32_t)p.Kb * 4u), kRawBuffer);
+
+    // Activation row of the tile's row r, or -1.
+    auto a_row = [&](int r) __attribute__((always_inline)) {
+        if constexpr (GROUPED) {
+            const int x = lds.row[r];
+            return x < 0 ? -1 : x / gr.share;
+        } else {
+            return r < rows ? r : -1;
+        }
+    };
+    uint32_t wo[S::kWLoads], ao[S::kALoads], so = kOutOfRange;
+    // K offset of each load's piece, for the last step.
+    int wk[S::kWLoads], ak[S::kALoads], sk = 0;
+#pragma unroll
+    for (int j = 0; j < S::kWLoads; ++j) {
+        const int c = j * S::kThreads + tid, r = c / 8 % S::BN;
+        wk[j] = c / (8 * S::BN) * 128 + ((c ^ r) & 7) * 16;
+        wo[j] = r < wrows ? (uint32_t)r * (uint32_t)p.K + (uint32_t)wk[j] : kOutOfRange;
+    }
+#pragma unroll
+    for (int j = 0; j < S::kALoads; ++j) {
+        const int c = j * S::kThreads + tid, r = c / 8 % S::BM, x = a_row(r);
+        ak[j] = c / (8 * S::BM) * 128 + ((c ^ r) & 7) * 16;
+        ao[j] = x >= 0 ? (uint32_t)x * (uint32_t)p.K + (uint32_t)ak[j] : kOutOfRange;
+    }
+    if (wave < S::kSWaves) {
+        const int x = a_row(tid % S::BM);
+        sk = tid / S::BM;
+        so = x >= 0 ? ((uint32_t)x * (uint32_t)p.Kb + (uint32_t)sk) * 4u : kOutOfRange;
+    }
+    constexpr int kStepK = 128 * S::KG;
+    const int steps = (p.K + kStepK - 1) / kStepK;
+    auto issue = [&](int step) __attribute__((always_inline)) {
+        const int st = step & 1, k0 = step * kStepK;
+        if (k0 + kStepK <= p.K) {
+#pragma unroll
+            for (int j = 0; j < S::kWLoads; ++j)
+                load16_to_lds(wr, lds.w[st] + j * S::kThreads + wave * 64, wo[j], k0);
+#pragma unroll
+            for (int j = 0; j < S::kALoads; ++j)
+                load16_to_lds(ar, lds.a[st] + j * S::kThreads + wave * 64, ao[j], k0);
+            if (wave < S::kSWaves)
+                load4_to_lds(sr, lds.s[st] + wave * 64, so, step * (S::KG * 4));
+        } else {   // pieces past K read as zero
+#pragma unroll
+            for (int j = 0; j < S::kWLoads; ++j)
+                load16_to_lds(wr, lds.w[st] + j * S::kThreads + wave * 64,
+                              k0 + wk[j] < p.K ? wo[j] : kOutOfRange, k0);
+#pragma unroll
+            for (int j = 0; j < S::kALoads; ++j)
+                load16_to_lds(ar, lds.a[st] + j * S::kThreads + wave * 64,
+                              k0 + ak[j] < p.K ? ao[j] : kOutOfRange, k0);
+            if (wave < S::kSWaves)
+                load4_to_lds(sr, lds.s[st] + wave * 64, step * S::KG + sk < p.Kb ? so : kOutOfRange, step * (S::KG * 4));
+        }
+    };
+
+    f32x4 acc[S::TN][S::TM];
+#pragma unroll
+    for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j)
+            acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    const int nb = min((n0 + wn * (S::TN * 16)) >> 7, p.Nb - 1);
+    const float *wsp = w_s + (size_t)nb * (size_t)p.Kb;
+
+    // Operand of a 16-row tile in LDS: pieces g and 4 + g of row li.
+    auto operand = [&](const u32x4 *base, int r0) __attribute__((always_inline)) {
+        const int r = r0 + li;
+        return join(base[r * 8 + (g ^ (r & 7))], base[r * 8 + ((4 + g) ^ (r & 7))]);
+    };
+
+    issue(0);
+    for (int step = 0; step < steps; ++step) {
+        // This step's stage has landed, and every wavefront has read the
+        // other one, which the next step's loads then fill.
+        wait_and_meet();
+        if (step + 1 < steps)
+            issue(step + 1);
+        const int st = step & 1;
+        const float ws = wsp[min(step * S::KG + kg, p.Kb - 1)];
+        const u32x4 *wb = lds.w[st] + kg * (S::BN * 8), *ab = lds.a[st] + kg * (S::BM * 8);
+        const float *sb = lds.s[st] + kg * S::BM + wm * (S::TM * 16) + li;
+        i32x8 wf[S::TN];
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i)
+            wf[i] = operand(wb, wn * (S::TN * 16) + i * 16);
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
+            const i32x8 af = operand(ab, wm * (S::TM * 16) + j * 16);
+            const float s = sb[j * 16] * ws;
+#pragma unroll
+            for (int i = 0; i < S::TN; ++i) {
+                const f32x4 c = mfma_block(wf[i], af);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[i][j][q] = fmaf(s, c[q], acc[i][j][q]);
+            }
+        }
+    }
+    if constexpr (S::KG == 2) {
+        wait_and_meet();
+        f32x4 *red = reinterpret_cast<f32x4 *>(&lds.w[0][0]);
+        static_assert(sizeof(lds.w) + sizeof(lds.a) >= S::WN * S::WM * S::TN * S::TM * 64 * sizeof(f32x4), "reduction buffer");
+        const int wq = wave % (S::WN * S::WM);
+        if (kg == 1) {
+#pragma unroll
+            for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+                for (int j = 0; j < S::TM; ++j)
+                    red[((wq * S::TN + i) * S::TM + j) * 64 + lane] = acc[i][j];
+        }
+        __syncthreads();
+        if (kg == 1)
+            return;
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TM; ++j)
+                acc[i][j] += red[((wq * S::TN + i) * S::TM + j) * 64 + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) {
+        const int r = wm * (S::TM * 16) + j * 16 + li;
+        int y_row;
+        if constexpr (GROUPED)
+            y_row = lds.row[r];
+        else
+            y_row = r < rows ? m0 + r : -1;
+        if (y_row < 0)
+            continue;
+        uint16_t *yp = p.y + (size_t)y_row * (size_t)p.N;
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i)
+            store4(yp, n0 + wn * (S::TN * 16) + i * 16 + 4 * g, p.N, acc[i][j]);
+    }
+}
+
+using TileLarge = TileShape<2, 4, 8, 4, 1>;    // 256 columns x 256 rows
+using TileMedium = TileShape<2, 2, 4, 4, 2>;   // 128 x 128
+
+template <class S>
+static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
+{
+    const long long tm = ((long long)p.M + S::BM - 1) / S::BM, tn = ((long long)p.N + S::BN - 1) / S::BN;
+    const long long grid = (tm * tn + 7) / 8 * 8;
+    if (grid > 0x7fffffffLL)
+        return hipErrorInvalidValue;
+    return launch_kernel(k_f8_tile<S, false>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p,
+                         Groups{nullptr, nullptr, 0, 0, 1}, (int)tm, (int)tn);
+}
+
+template <int R>
+static hipError_t launch_skinny(const F8Product &p, hipStream_t st)
+{
+    return launch_kernel(k_f8_skinny<R>, dim3((unsigned)(((long long)p.N + 15) / 16), (unsigned)((p.M + 16 * R - 1) / (16 * R))),
+                         dim3(64 * kSkinnyWaves), 0, st, p);
+}
+
+hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
+                          uint16_t *y, int M, int N, int K, hipStream_t st)
+{
+    const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
+    if (M <= 16)
+        return launch_skinny<1>(p, st);
+    if (M <= 32)
+        return launch_skinny<2>(p, st);
+    if (M <= 64)
+        return launch_skinny<4>(p, st);
+    const long long large = (((long long)M + 255) / 256) * (((long long)N + 255) / 256);
+    if (large >= 256)
+        return launch_tiles<TileLarge>(p, st);
+    return launch_tiles<TileMedium>(p, st);
+}
+
+hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
+                                  const float *w_s, const int *offsets, const int *order, int share,
+                                  uint16_t *y, int G, int M, int N, int K, hipStream_t st)
+{
+    const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
+    const Groups gr = {offsets, order, G, M, share};
+    if ((long long)M <= 32LL * G)
+        return launch_kernel(k_f8_skinny_grouped, dim3((unsigned)(((long long)N + 15) / 16), (unsigned)G),
+                             dim3(64 * kSkinnyWaves), 0, st, p, gr);
+    using S = TileMedium;
+    const long long tn = ((long long)N + S::BN - 1) / S::BN;
+    const long long grid = group_grid(G, M, S::BM, tn);
+    if (grid > 0x7fffffffLL)
+        return hipErrorInvalidValue;
+    return launch_kernel(k_f8_tile<S, true>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p, gr,
+                         0, (int)tn);
+}
+
+}  // namespace q4k

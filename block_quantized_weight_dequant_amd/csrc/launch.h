@@ -58,4 +58,20 @@ hipError_t launch_gemm_q8a(WeightFormat fmt, const uint8_t *a_q, const uint8_t *
 hipError_t launch_q8_quantize(const float *x, size_t n_blocks, uint8_t *out, hipStream_t s);
 hipError_t launch_q4_quantize(const float *x, size_t n_blocks, uint8_t *out, hipStream_t s);
 
+// E4M3 codes with one scale per 128 columns of a row (block_rows 1) or per
+// 128 x 128 tile (128).
+hipError_t launch_f8_quantize(const float *x, uint8_t *q, float *s, int M, int K, int block_rows,
+                              hipStream_t st);
+hipError_t launch_f8_quantize_bf16(const uint16_t *x, uint8_t *q, float *s, int M, int K,
+                                   int block_rows, hipStream_t st);
+hipError_t launch_f8_dequant(const uint8_t *q, const float *s, float *out, int M, int K,
+                             int block_rows, hipStream_t st);
+// y: [M, N] bfloat16. K <= 2^22.
+hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
+                          uint16_t *y, int M, int N, int K, hipStream_t st);
+// order may be null; the activations' codes span less than 2^31 bytes.
+hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
+                                  const float *w_s, const int *offsets, const int *order, int share,
+                                  uint16_t *y, int G, int M, int N, int K, hipStream_t st);
+
 }  // namespace q4k

@@ -3,6 +3,7 @@
 // alignment, output/input overlap). Nothing here touches device memory.
 #include "validate.h"
 
+#include "f8.h"
 #include "q4.h"
 
 namespace q4v {
@@ -260,6 +261,53 @@ int check_workspace_span(size_t need, const void *a, size_t a_bytes, const void 
     const size_t y_bytes = (size_t)M * (size_t)N * sizeof(float);
     if (overlaps({ws, need}, {a, a_bytes}) || overlaps({ws, need}, {w, w_bytes}) ||
         overlaps({ws, need}, {y, y_bytes}))
+        return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
+int check_f8_codec(const void *x, size_t x_elem, int M, int K, int block_rows, const void *q,
+                   size_t q_bytes, const void *s, size_t s_elems, bool x_written, bool *empty)
+{
+    *empty = false;
+    if (M < 0 || K < 32 || K % 32 != 0 || (block_rows != 1 && block_rows != 128))
+        return Q4_ERR_SHAPE;
+    const size_t n = (size_t)M * (size_t)K;   // both below 2^31
+    const size_t rows = ((size_t)M + (size_t)block_rows - 1) / (size_t)block_rows;
+    if (q_bytes != n || s_elems != rows * f8_blocks(K) || s_elems >= ((size_t)1 << 31))
+        return Q4_ERR_SIZE;
+    if (M == 0) {
+        *empty = true;
+        return Q4_OK;
+    }
+    if (!x || !q || !s)
+        return Q4_ERR_NULL;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s))
+        return Q4_ERR_ALIGN;
+    const Span xs = {x, n * x_elem}, qs = {q, n}, ss = {s, s_elems * 4};
+    if (overlaps(xs, qs) || overlaps(xs, ss) || (!x_written && overlaps(qs, ss)))
+        return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
+int check_f8_product(const void *a, const void *a_s, const void *w, size_t w_bytes, const void *w_s,
+                     const void *y, int M, int N, int K, int max_rows, bool *empty)
+{
+    *empty = false;
+    if (M < 0 || N < 0 || K < 32 || K % 32 != 0 || K > F8_MAX_K || (max_rows > 0 && M > max_rows))
+        return Q4_ERR_SHAPE;
+    if (w_bytes != (size_t)N * (size_t)K)
+        return Q4_ERR_SIZE;
+    if (M == 0 || N == 0) {
+        *empty = true;
+        return Q4_OK;
+    }
+    if (!a || !a_s || !w || !w_s || !y)
+        return Q4_ERR_NULL;
+    if (!aligned16(a) || !aligned16(a_s) || !aligned16(w) || !aligned16(w_s) || !aligned16(y))
+        return Q4_ERR_ALIGN;
+    const Span ys = {y, (size_t)M * (size_t)N * 2};
+    if (overlaps(ys, {a, (size_t)M * (size_t)K}) || overlaps(ys, {a_s, (size_t)M * f8_blocks(K) * 4}) ||
+        overlaps(ys, {w, w_bytes}) || overlaps(ys, {w_s, f8_blocks(N) * f8_blocks(K) * 4}))
         return Q4_ERR_ALIAS;
     return Q4_OK;
 }

@@ -165,6 +165,16 @@ inline bool gemv_q8a_streams(int M, int N, int K, size_t block_bytes)
            (size_t)M * (size_t)(K / 32) * 34 < ((size_t)1 << 31);
 }
 
+// E4M3 (include/f8.h). Blocks along a row of K, and rows of tiles.
+inline size_t f8_blocks(int n) { return ((size_t)n + 127) / 128; }
+// f8_quantize (x_elem bytes per value, x read, q and s written) and f8_dequant
+// (x_elem 4, x written, q and s read).
+int check_f8_codec(const void *x, size_t x_elem, int M, int K, int block_rows, const void *q,
+                   size_t q_bytes, const void *s, size_t s_elems, bool x_written, bool *empty);
+// max_rows > 0 bounds M.
+int check_f8_product(const void *a, const void *a_s, const void *w, size_t w_bytes, const void *w_s,
+                     const void *y, int M, int N, int K, int max_rows, bool *empty);
+
 bool aligned16(const void *p);
 bool overlaps(Span a, Span b);
 
