@@ -27,6 +27,9 @@ Q4_ERR_LAUNCH = 6
 Q4_ERR_WORKSPACE = 7
 Q4_GEMV_MAX_ROWS = 8
 Q4_GEMM_SCRATCH_BYTES = 64 << 20
+Q4_MAX_EXPERTS = 1024
+Q4_MAX_TOP_K = 32
+Q4_MAX_SLOTS = 1 << 30
 SIZE_MAX = 2 ** 64 - 1
 
 #: Every symbol include/q4.h declares.
@@ -38,10 +41,14 @@ EXPORTS = ("q4_abi_version", "q4_status_string", "q4_dequant", "q4_gemv", "q4_ge
            "q8_gemv_splitk", "q8_gemv_splitk_workspace_bytes", "q4_gemv_prepare_bytes",
            "q4_gemv_prepare", "q4_gemv_prepared", "q8_gemv_prepare_bytes", "q8_gemv_prepare",
            "q8_gemv_prepared", "q4_gemv_q8a", "q8_gemv_q8a", "q4_gemm_q8a",
-           "q4_gemm_q8a_workspace_bytes", "q8_gemm_q8a", "q8_gemm_q8a_workspace_bytes")
+           "q4_gemm_q8a_workspace_bytes", "q8_gemm_q8a", "q8_gemm_q8a_workspace_bytes",
+           "q4_route", "q4_route_workspace_bytes") + tuple(
+               f + "_gemm_grouped" + act + ws for f in ("q4", "q8") for act in ("", "_bf16")
+               for ws in ("", "_workspace_bytes"))
 
 #: Every symbol include/f8.h declares.
-F8_EXPORTS = ("f8_quantize", "f8_quantize_bf16", "f8_dequant", "f8_gemm", "f8_gemv")
+F8_EXPORTS = ("f8_quantize", "f8_quantize_bf16", "f8_dequant", "f8_gemm", "f8_gemv",
+              "f8_gemm_grouped")
 F8_BLOCK = 128
 F8_MAX_K = 4194304
 
@@ -101,11 +108,22 @@ def _load_library():
     for name in ("q8_quantize", "q4_quantize"):
         getattr(lib, name).restype = i32
         getattr(lib, name).argtypes = [P, sz, P, sz, P]
+    lib.q4_route.restype = i32
+    lib.q4_route.argtypes = [P, i32, i32, i32, i32, P, P, P, P, P, sz, P]
+    lib.q4_route_workspace_bytes.restype = sz
+    lib.q4_route_workspace_bytes.argtypes = [i32, i32, i32]
+    for name in ("q4_gemm_grouped", "q4_gemm_grouped_bf16", "q8_gemm_grouped",
+                 "q8_gemm_grouped_bf16"):
+        getattr(lib, name).restype = i32
+        getattr(lib, name).argtypes = [P, P, sz, P, P, i32, P, i32, i32, i32, i32, P, sz, P]
+        getattr(lib, name + "_workspace_bytes").restype = sz
+        getattr(lib, name + "_workspace_bytes").argtypes = [i32, i32, i32, i32]
     for name in F8_EXPORTS:
         getattr(lib, name).restype = i32
     lib.f8_quantize.argtypes = lib.f8_quantize_bf16.argtypes = [P, i32, i32, i32, P, sz, P, sz, P]
     lib.f8_dequant.argtypes = [P, sz, P, sz, i32, i32, i32, P, sz, P]
     lib.f8_gemm.argtypes = lib.f8_gemv.argtypes = [P, P, P, sz, P, P, i32, i32, i32, P]
+    lib.f8_gemm_grouped.argtypes = [P, P, P, sz, P, P, P, i32, P, i32, i32, i32, i32, P]
     return lib
 
 
@@ -488,6 +506,106 @@ def f8_gemm(a, a_s, w, w_s, y, M: int, N: int, K: int, w_bytes=None, stream=None
 def f8_gemv(a, a_s, w, w_s, y, M: int, N: int, K: int, w_bytes=None, stream=None) -> None:
     """f8_gemm for 1 <= M <= 8 rows."""
     _f8_product("f8_gemv", a, a_s, w, w_s, y, M, N, K, w_bytes, stream)
+
+
+def f8_gemm_grouped(a, a_s, w, w_s, offsets, order, y, G: int, M: int, N: int, K: int,
+                    share: int = 1, w_bytes=None, stream=None) -> None:
+    """f8_gemm grouped by expert: row r of group e is ``a``'s row r // share times
+    the e-th of G weight matrices. ``offsets`` [G + 1] and ``order`` [M] (or
+    None: sorted rows) are int32 device tensors, as q4_route writes them."""
+    wb = _nbytes(w) if w_bytes is None else int(w_bytes)
+    _check(lib.f8_gemm_grouped(_addr(a), _addr(a_s), _addr(w), wb, _addr(w_s), _addr(offsets),
+                               _addr(order), int(share), _addr(y), int(G), int(M), int(N), int(K),
+                               _stream(stream)), "f8_gemm_grouped")
+
+
+def q4_route_workspace_bytes(T: int, E: int, top_k: int) -> int:
+    return int(lib.q4_route_workspace_bytes(int(T), int(E), int(top_k)))
+
+
+def q4_route(logits, ids, weights, offsets, order, T: int, E: int, top_k: int, renorm: bool = True,
+             workspace=None, workspace_bytes=None, stream=None) -> None:
+    """Router: f32 ``logits`` [T, E] -> ``ids`` [T, top_k] (int32), ``weights``
+    [T, top_k] (f32), and the slots sorted by expert: ``offsets`` [E + 1],
+    ``order`` [T * top_k] (int32). The workspace comes from PyTorch's allocator
+    when none is passed."""
+    ws = workspace
+    if ws is None:
+        need = int(lib.q4_route_workspace_bytes(int(T), int(E), int(top_k)))
+        if need:
+            ws = _scratch(need, stream, ids)
+    if workspace_bytes is not None:
+        wsb = int(workspace_bytes)
+    else:
+        wsb = _nbytes(ws) if ws is not None and not isinstance(ws, int) else 0
+    _check(lib.q4_route(_addr(logits), int(T), int(E), int(top_k), int(bool(renorm)), _addr(ids),
+                        _addr(weights), _addr(offsets), _addr(order), _addr(ws), wsb,
+                        _stream(stream)), "q4_route")
+
+
+def q4_gemm_grouped_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    return int(lib.q4_gemm_grouped_workspace_bytes(int(G), int(M), int(N), int(K)))
+
+
+def q4_gemm_grouped_bf16_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    return int(lib.q4_gemm_grouped_bf16_workspace_bytes(int(G), int(M), int(N), int(K)))
+
+
+def q8_gemm_grouped_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    return int(lib.q8_gemm_grouped_workspace_bytes(int(G), int(M), int(N), int(K)))
+
+
+def q8_gemm_grouped_bf16_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    return int(lib.q8_gemm_grouped_bf16_workspace_bytes(int(G), int(M), int(N), int(K)))
+
+
+def _gemm_grouped(entry, a, w_q, offsets, order, y, G, M, N, K, share, workspace, workspace_bytes,
+                  w_bytes, stream) -> None:
+    wb = _nbytes(w_q) if w_bytes is None else int(w_bytes)
+    ws = workspace
+    if ws is None:
+        need = int(getattr(lib, entry + "_workspace_bytes")(int(G), int(M), int(N), int(K)))
+        if 0 < need < SIZE_MAX:
+            ws = _scratch(need, stream, y)
+    if workspace_bytes is not None:
+        wsb = int(workspace_bytes)
+    else:
+        wsb = _nbytes(ws) if ws is not None and not isinstance(ws, int) else 0
+    _check(getattr(lib, entry)(_addr(a), _addr(w_q), wb, _addr(offsets), _addr(order), int(share),
+                               _addr(y), int(G), int(M), int(N), int(K), _addr(ws), wsb,
+                               _stream(stream)), entry)
+
+
+def q4_gemm_grouped(a, w_q, offsets, order, y, G: int, M: int, N: int, K: int, share: int = 1,
+                    workspace=None, workspace_bytes=None, w_bytes=None, stream=None) -> None:
+    """Products grouped by expert: y[r] = a[r // share] @ dequant(W[e])^T for the
+    rows r of each group e, W of G Q4_0 matrices [N, K/32]. ``offsets`` [G + 1]
+    and ``order`` [M] (or None: sorted rows) are int32 device tensors, as
+    q4_route writes them; rows of y that no group names are left as they were.
+    The workspace comes from PyTorch's allocator when none is passed."""
+    _gemm_grouped("q4_gemm_grouped", a, w_q, offsets, order, y, G, M, N, K, share, workspace,
+                  workspace_bytes, w_bytes, stream)
+
+
+def q4_gemm_grouped_bf16(a, w_q, offsets, order, y, G: int, M: int, N: int, K: int, share: int = 1,
+                         workspace=None, workspace_bytes=None, w_bytes=None, stream=None) -> None:
+    """As q4_gemm_grouped with bfloat16 activations."""
+    _gemm_grouped("q4_gemm_grouped_bf16", a, w_q, offsets, order, y, G, M, N, K, share, workspace,
+                  workspace_bytes, w_bytes, stream)
+
+
+def q8_gemm_grouped(a, w_q, offsets, order, y, G: int, M: int, N: int, K: int, share: int = 1,
+                    workspace=None, workspace_bytes=None, w_bytes=None, stream=None) -> None:
+    """As q4_gemm_grouped over Q8_0 matrices."""
+    _gemm_grouped("q8_gemm_grouped", a, w_q, offsets, order, y, G, M, N, K, share, workspace,
+                  workspace_bytes, w_bytes, stream)
+
+
+def q8_gemm_grouped_bf16(a, w_q, offsets, order, y, G: int, M: int, N: int, K: int, share: int = 1,
+                         workspace=None, workspace_bytes=None, w_bytes=None, stream=None) -> None:
+    """As q4_gemm_grouped_bf16 over Q8_0 matrices."""
+    _gemm_grouped("q8_gemm_grouped_bf16", a, w_q, offsets, order, y, G, M, N, K, share, workspace,
+                  workspace_bytes, w_bytes, stream)
 
 
 def raw_status(entry: str, *args) -> int:

@@ -455,3 +455,125 @@ Q4_EXPORT int f8_gemv(const uint8_t *a, const float *a_s, const uint8_t *w, size
 {
     return f8_product(a, a_s, w, w_bytes, w_s, y, M, N, K, Q4_GEMV_MAX_ROWS, stream);
 }
+
+Q4_EXPORT size_t q4_route_workspace_bytes(int T, int E, int top_k)
+{
+    return q4v::route_workspace_bytes(T, E, top_k);
+}
+
+Q4_EXPORT int q4_route(const float *logits, int T, int E, int top_k, int renorm, int32_t *ids,
+                       float *weights, int32_t *offsets, int32_t *order, void *workspace,
+                       size_t workspace_bytes, void *stream)
+{
+    bool empty = false;
+    int st = q4v::check_route(logits, T, E, top_k, ids, weights, offsets, order, workspace,
+                              workspace_bytes, q4v::route_workspace_bytes(T, E, top_k), &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    return launched(q4k::launch_route(logits, ids, weights, offsets, order, workspace, T, E, top_k,
+                                      renorm != 0, as_stream(stream)));
+}
+
+static int gemm_grouped(q4k::WeightFormat fmt, size_t block_bytes, bool bf16, const void *a,
+                        const void *w_q, size_t w_bytes, const int32_t *offsets,
+                        const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = q4v::check_group_shape(G, M, N, K, 64, 1 << 22, share);
+    if (st != Q4_OK)
+        return st;
+    // G <= 2^10, N < 2^31, K <= 2^22: the counts fit 64 bits.
+    if (w_bytes != (size_t)G * (size_t)N * ((size_t)(K / 32) * block_bytes))
+        return Q4_ERR_SIZE;
+    if (M == 0 || N == 0)
+        return Q4_OK;
+    const size_t a_rows = ((size_t)M - 1) / (size_t)share + 1;
+    const q4v::GroupedArgs g = {a, a_rows * (size_t)K * (bf16 ? 2 : 4), nullptr, 0, w_q, w_bytes,
+                                nullptr, 0, offsets, order, y, (size_t)M * (size_t)N * 4, G, M};
+    st = q4v::check_grouped(g);
+    if (st == Q4_OK)
+        st = q4v::check_grouped_workspace(g, q4v::grouped_workspace_bytes(G, M, N, K, bf16 ? 1 : 2),
+                                          workspace, workspace_bytes);
+    if (st != Q4_OK)
+        return st;
+    return launched(q4k::launch_gemm_grouped(fmt, bf16, a, static_cast<const uint8_t *>(w_q), offsets,
+                                             order, share, y, G, M, N, K, workspace,
+                                             as_stream(stream)));
+}
+
+Q4_EXPORT int q4_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                              const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    return gemm_grouped(q4k::WeightFormat::kQ4_0, 18, false, a, w_q, w_bytes, offsets, order, share, y, G,
+                        M, N, K, workspace, workspace_bytes, stream);
+}
+
+Q4_EXPORT size_t q4_gemm_grouped_workspace_bytes(int G, int M, int N, int K)
+{
+    return q4v::grouped_workspace_bytes(G, M, N, K, 2);
+}
+
+Q4_EXPORT int q4_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                                   const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    return gemm_grouped(q4k::WeightFormat::kQ4_0, 18, true, a, w_q, w_bytes, offsets, order, share, y, G,
+                        M, N, K, workspace, workspace_bytes, stream);
+}
+
+Q4_EXPORT size_t q4_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K)
+{
+    return q4v::grouped_workspace_bytes(G, M, N, K, 1);
+}
+
+Q4_EXPORT int q8_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                              const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    return gemm_grouped(q4k::WeightFormat::kQ8_0, 34, false, a, w_q, w_bytes, offsets, order, share, y, G,
+                        M, N, K, workspace, workspace_bytes, stream);
+}
+
+Q4_EXPORT size_t q8_gemm_grouped_workspace_bytes(int G, int M, int N, int K)
+{
+    return q4v::grouped_workspace_bytes(G, M, N, K, 2);
+}
+
+Q4_EXPORT int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                                   const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    return gemm_grouped(q4k::WeightFormat::kQ8_0, 34, true, a, w_q, w_bytes, offsets, order, share, y, G,
+                        M, N, K, workspace, workspace_bytes, stream);
+}
+
+Q4_EXPORT size_t q8_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K)
+{
+    return q4v::grouped_workspace_bytes(G, M, N, K, 1);
+}
+
+Q4_EXPORT int f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,
+                              const float *w_s, const int32_t *offsets, const int32_t *order,
+                              int share, uint16_t *y, int G, int M, int N, int K, void *stream)
+{
+    int st = q4v::check_group_shape(G, M, N, K, 32, F8_MAX_K, share);
+    const size_t a_rows = st == Q4_OK && M > 0 ? ((size_t)M - 1) / (size_t)share + 1 : 0;
+    if (st == Q4_OK && a_rows * (size_t)K >= ((size_t)1 << 31))
+        st = Q4_ERR_SHAPE;
+    if (st != Q4_OK)
+        return st;
+    if (w_bytes != (size_t)G * (size_t)N * (size_t)K)
+        return Q4_ERR_SIZE;
+    if (M == 0 || N == 0)
+        return Q4_OK;
+    const size_t kb = q4v::f8_blocks(K);
+    const q4v::GroupedArgs g = {a, a_rows * (size_t)K, a_s, a_rows * kb * 4, w, w_bytes, w_s,
+                                (size_t)G * q4v::f8_blocks(N) * kb * 4, offsets, order, y,
+                                (size_t)M * (size_t)N * 2, G, M};
+    st = q4v::check_grouped(g);
+    if (st != Q4_OK)
+        return st;
+    return launched(q4k::launch_f8_gemm_grouped(a, a_s, w, w_s, offsets, order, share, y, G, M, N, K,
+                                                as_stream(stream)));
+}

@@ -58,6 +58,30 @@ __device__ __forceinline__ T bitcast(U u)
     return __builtin_bit_cast(T, u);
 }
 
+// Largest of a non-negative 32-bit value over the wavefront, in every lane:
+// DPP within quads, half-rows and rows, then one readlane per row.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+{
+    int x = (int)v;
+    x = (int)max((uint32_t)x, (uint32_t)__builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false));    // quad_perm 1,0,3,2
+    x = (int)max((uint32_t)x, (uint32_t)__builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false));    // quad_perm 2,3,0,1
+    x = (int)max((uint32_t)x, (uint32_t)__builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false));   // row_half_mirror
+    x = (int)max((uint32_t)x, (uint32_t)__builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false));   // row_mirror
+    return max(max((uint32_t)__builtin_amdgcn_readlane(x, 0), (uint32_t)__builtin_amdgcn_readlane(x, 16)),
+               max((uint32_t)__builtin_amdgcn_readlane(x, 32), (uint32_t)__builtin_amdgcn_readlane(x, 48)));
+}
+
+// Direct-to-LDS loads of 16 and of 4 bytes a lane: lane l's bytes go to dst +
+// 16 l (4 l).
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, base, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 4, off, base, 0, 0);
+}
+
 // Launch a kernel and return the runtime's verdict on this launch alone. Each
 // argument is first converted to the kernel's own parameter type.
 template <typename Kernel, typename Tuple, size_t... I>

@@ -496,17 +496,6 @@ __device__ __forceinline__ void wait_and_meet()
     asm volatile("" ::: "memory");
 }
 
-// Direct-to-LDS loads of 16 and of 4 bytes a lane: lane l's bytes go to dst +
-// 16 l (4 l).
-__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, base, 0, 0);
-}
-__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 4, off, base, 0, 0);
-}
-
 template <class S, bool GROUPED>
 __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, int tiles_m,
                                                           int tiles_n)

@@ -1,0 +1,337 @@
+// Products grouped by expert over Q4_0 and Q8_0 weights, f32 or bfloat16
+// activations: y[r] = a[r / share] @ dequant(W[e])^T for the rows r of each
+// group e (groups.h), each group with its own number of rows.
+//
+// The arithmetic is the GEMM's (gemm.hip): a row of activations is scaled by
+// a power of two and written once as binary16 matrix-core operands (two terms
+// of f32, one of bfloat16), weights decode to exact binary16 codes, and every
+// block's sum is scaled by its d in f32. What is new is where rows and weights
+// come from, and a form for few rows.
+//
+// The preparation gathers the rows: each group's rows fill tiles of bm rows,
+// the last one short; operands [tile][block][term][16-row subtile][lane], row
+// exponents [tile row].
+#include "device_common.h"
+#include "formats.h"
+#include "gemm_split.h"
+#include "groups.h"
+#include "launch.h"
+#include "validate.h"
+
+namespace q4k {
+
+// Workgroup (x, q): 16-row subtile x of the tiles, K part q. One wavefront per
+// row finds the row's exponent over the whole row, then the wavefronts take
+// the part's blocks in turn, lane (g, li) the slots of lane group g of row li.
+// Subtiles past a group's last row write nothing: their operands reach only
+// rows of y that are not stored.
+template <class F, bool BF, int BM>
+__global__ __launch_bounds__(64 * kPrepWaves) void k_grouped_prep(const void *__restrict__ a,
+                                                                Groups gr, int *__restrict__ row_exp,
+                                                                u32x4 *__restrict__ ops, int K,
+                                                                int part_blocks)
+{
+    __shared__ int s_p[16], s_row[16];
+    constexpr int SUBS = BM / 16, TERMS = BF ? 1 : 2;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int t = blockIdx.x / SUBS, sub = blockIdx.x % SUBS;
+    const GroupTile gt = find_group_tile(gr, t, BM, 1);
+    const int p0 = gt.lo + gt.mt * BM + sub * 16;
+    if (gt.e < 0 || p0 >= gt.hi)
+        return;
+    const float *af = static_cast<const float *>(a);
+    const uint16_t *ab = static_cast<const uint16_t *>(a);
+    const int r = p0 + wave < gt.hi ? group_row(gr, p0 + wave) : -1;
+    int p = 0;
+    if (r >= 0) {
+        const size_t at = (size_t)(r / gr.share) * (size_t)K;
+        p = BF ? row_exp_from_bits(row_max_bits_bf16(ab + at, K, lane))
+               : row_exp_from_bits_f32(row_max_bits_f32(af + at, K, lane));
+    }
+    if (lane == 0) {
+        s_p[wave] = p;
+        s_row[wave] = r;
+        if (blockIdx.y == 0)
+            row_exp[(size_t)t * BM + sub * 16 + wave] = p;
+    }
+    __syncthreads();
+    const int li = lane & 15, g = lane >> 4;
+    const int row = s_row[li], pl = s_p[li], ph = pl - F::kHiLog2;
+    const size_t at = (size_t)(max(row, 0) / gr.share) * (size_t)K;
+    const int nblk = K >> 5;
+    const int kb0 = (int)blockIdx.y * part_blocks, kb1 = min(kb0 + part_blocks, nblk);
+#pragma unroll 2
+    for (int kb = kb0 + wave; kb < kb1; kb += kPrepWaves) {
+        float e[8];
+        if constexpr (BF) {
+            const uint16_t *blk = ab + at + (size_t)kb * 32;
+            const uint2 L = *reinterpret_cast<const uint2 *>(blk + F::a_lo(g));
+            const uint2 H = *reinterpret_cast<const uint2 *>(blk + F::a_hi(g));
+            const float v[8] = {bf16_bits_to_f32(L.x & 0xFFFFu), bf16_bits_to_f32(L.y & 0xFFFFu),
+                                bf16_bits_to_f32(L.x >> 16), bf16_bits_to_f32(L.y >> 16),
+                                bf16_bits_to_f32(H.x & 0xFFFFu), bf16_bits_to_f32(H.y & 0xFFFFu),
+                                bf16_bits_to_f32(H.x >> 16), bf16_bits_to_f32(H.y >> 16)};
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                e[s] = ldexpf(v[s], s < 4 ? pl : ph);
+        } else {
+            const float *blk = af + at + (size_t)kb * 32;
+            const float4 L = *reinterpret_cast<const float4 *>(blk + F::a_lo(g));
+            const float4 H = *reinterpret_cast<const float4 *>(blk + F::a_hi(g));
+            const float v[8] = {L.x, L.z, L.y, L.w, H.x, H.z, H.y, H.w};
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                e[s] = ldexpf(v[s], s < 4 ? pl : ph);
+        }
+        f16x8 hi, lo;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float x = row >= 0 ? e[s] : 0.0f;
+            const f16 h = (f16)x;
+            hi[s] = h;
+            lo[s] = (f16)((x - (float)h) * 2048.0f);
+        }
+        u32x4 *dst = ops + (((size_t)t * nblk + kb) * TERMS * SUBS + sub) * 64 + lane;
+        dst[0] = bitcast<u32x4>(hi);
+        if constexpr (!BF)
+            dst[SUBS * 64] = bitcast<u32x4>(lo);
+    }
+}
+
+template <class F, bool HO>
+__global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
+    const u32x4 *__restrict__ ahl, const uint8_t *__restrict__ w, float *__restrict__ y, int N,
+    int nblk_row, int nblk, int tiles_n, const int *__restrict__ row_exp, int accumulate, Groups gr)
+{
+    gemm_split_body<F, HO, true>(ahl, w, y, 0, N, nblk_row, nblk, 0, tiles_n, row_exp, accumulate, gr);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows a group: bound by the bytes of the weights. Workgroup (x, e) takes
+// 16 CT weight rows of group e past the group's rows, 16 R at a time. Its eight
+// wavefronts deal the row's chunks of 8 blocks (256 elements: 144 or 272
+// bytes, whole 16-byte pieces) among themselves; each stages its own chunk's
+// raw bytes in its own LDS by 16-byte direct loads, one chunk ahead, and so
+// waits only for its own loads, never for the others. A row of a staged chunk
+// is 36 or 68 dwords, 4 mod 32, so the sixteen rows an operand read touches lie
+// in different banks. The activation operands of a chunk go from L2 to
+// registers (they are the wavefront's own: no other reads that chunk), once
+// for all 16 CT weight rows. The partial tiles are added through LDS.
+constexpr int kFewWaves = 8, kFewBlocks = 8;
+
+template <class F, int CT>
+struct FewGeom {
+    static constexpr int kRowBytes = kFewBlocks * F::kBytes;    // of a chunk
+    static constexpr int kPieces = kRowBytes / 16;
+    static constexpr int kRows = 16 * CT;
+    static constexpr int kLoads = (kRows * kPieces + 63) / 64;  // 16-byte loads of a wavefront per chunk
+    static constexpr int kStage = kLoads * 64;                  // 16-byte LDS words
+};
+
+template <class F, bool HO, int CT, int R>
+struct FewLds {
+    union {
+        u32x4 w[kFewWaves][2][FewGeom<F, CT>::kStage];
+        f32x4 red[kFewWaves][R * CT][64];
+    };
+};
+
+template <class F, bool HO, int CT, int R>
+__global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__restrict__ ops,
+                                                              const int *__restrict__ row_exp,
+                                                              const uint8_t *__restrict__ w,
+                                                              float *__restrict__ y, int N, int K,
+                                                              Groups gr)
+{
+    using G = FewGeom<F, CT>;
+    constexpr int TERMS = HO ? 1 : 2;
+    __shared__ FewLds<F, HO, CT, R> lds;
+    const int e = blockIdx.y;
+    int lo, hi;
+    group_bounds(gr, e, lo, hi);
+    if (lo >= hi)
+        return;
+    int tile = group_tiles_before(gr, e, 16);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, g = lane >> 4;
+    const int nblk = K >> 5, chunks = K / (32 * kFewBlocks);
+    const int n0 = blockIdx.x * G::kRows;
+    const uint32_t row_bytes = (uint32_t)nblk * F::kBytes;
+    const int wrows = min(G::kRows, N - n0);
+    // At most 64 rows of 28672 elements: the offsets are far below 2^31.
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w + ((size_t)e * (size_t)N + (size_t)n0) * (size_t)row_bytes), (short)0,
+        (int)((uint32_t)wrows * row_bytes), kBufferRsrcWord3);
+    uint32_t off[G::kLoads];
+#pragma unroll
+    for (int j = 0; j < G::kLoads; ++j) {
+        const int t = min(j * 64 + lane, G::kRows * G::kPieces - 1);   // surplus lanes re-read the last piece
+        const int row = t / G::kPieces;
+        off[j] = (uint32_t)min(row, wrows - 1) * row_bytes + 16u * (uint32_t)(t - row * G::kPieces);
+    }
+    const uint32_t magic = magic_vgpr<F>();
+    auto issue = [&](int c, int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < G::kLoads; ++j)
+            load16_to_lds(wr, lds.w[wave][buf] + j * 64, off[j], c * G::kRowBytes);
+    };
+    const f16 sc = (f16)0x1p-11f;
+    const f16x8 scale = {sc, sc, sc, sc, sc, sc, sc, sc};
+    const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
+
+    for (; lo < hi; lo += 16 * R, tile += R) {
+        const int subs = min(R, (hi - lo + 15) / 16);
+        f32x4 acc[R][CT];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                acc[r][ct] = zero4;
+        const int last = chunks - 1;
+        if (wave < chunks) {
+            issue(wave, 0);
+            int buf = 0;
+            for (int c = wave; c < chunks; c += kFewWaves, buf ^= 1) {
+                // This chunk's operands, then the next chunk's bytes: waiting for
+                // the operands leaves those in flight. Past the last chunk the
+                // last one is read again, into the buffer nobody reads.
+                f16x8 aop[R][TERMS][kFewBlocks];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const u32x4 *src = ops + ((size_t)(tile + min(r, subs - 1)) * nblk + c * kFewBlocks) * (TERMS * 64) + lane;
+#pragma unroll
+                    for (int b = 0; b < kFewBlocks; ++b)
+#pragma unroll
+                        for (int h = 0; h < TERMS; ++h)
+                            aop[r][h][b] = bitcast<f16x8>(src[(b * TERMS + h) * 64]);
+                }
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));   // the other buffer has been read
+                issue(min(c + kFewWaves, last), buf ^ 1);
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(G::kLoads));
+                asm volatile("" ::: "memory");
+                const uint32_t *base = reinterpret_cast<const uint32_t *>(lds.w[wave][buf]) + li * (G::kRowBytes / 4);
+                auto block = [&](auto b_c) __attribute__((always_inline)) {
+                    constexpr int b = decltype(b_c)::value;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const uint32_t *row = base + ct * 16 * (G::kRowBytes / 4);
+                        uint32_t x[F::kQsDwords];
+                        read_qs<F, b>(row, g, x);
+                        const float d = f16_bits_to_f32(read_d_bits<F, b>(row));
+                        const f16x8 q = F::decode(x, magic);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            f32x4 s = zero4;
+                            if constexpr (!HO)
+                                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][1][b], q * scale, s, 0, 0, 0);
+                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][0][b], q, s, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[r][ct][i] = fmaf(d, s[i], acc[r][ct][i]);
+                        }
+                    }
+                };
+                block(std::integral_constant<int, 0>{});
+                block(std::integral_constant<int, 1>{});
+                block(std::integral_constant<int, 2>{});
+                block(std::integral_constant<int, 3>{});
+                block(std::integral_constant<int, 4>{});
+                block(std::integral_constant<int, 5>{});
+                block(std::integral_constant<int, 6>{});
+                block(std::integral_constant<int, 7>{});
+            }
+        }
+        // Every load has landed before its LDS serves the partial tiles.
+        ring_barrier<0>();
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                lds.red[wave][r * CT + ct][lane] = acc[r][ct];
+        __syncthreads();
+        for (int i = wave; i < R * CT; i += kFewWaves) {
+            const int r = i / CT, ct = i % CT, n = n0 + ct * 16 + li;
+            f32x4 v = lds.red[0][i][lane];
+#pragma unroll
+            for (int s = 1; s < kFewWaves; ++s)
+                v += lds.red[s][i][lane];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int at = lo + 16 * r + 4 * g + q;
+                const int row = at < hi ? group_row(gr, at) : -1;
+                if (row >= 0 && n < N)
+                    y[(size_t)row * (size_t)N + n] = ldexpf(v[q], -row_exp[(size_t)(tile + r) * 16 + 4 * g + q]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <class F, bool BF, int CT, int R>
+static hipError_t launch_few(const u32x4 *ops, const int *row_exp, const uint8_t *w, float *y,
+                             int N, int K, const Groups &gr, hipStream_t s)
+{
+    static_assert(sizeof(FewLds<F, BF, CT, R>) <= (size_t)kLdsBytes, "the stages fit in LDS");
+    return launch_kernel(k_grouped_few<F, BF, CT, R>, dim3((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)gr.G),
+                         dim3(64 * kFewWaves), 0, s, ops, row_exp, w, y, N, K, gr);
+}
+
+template <class F, bool BF>
+static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, int N, int K,
+                                   const Groups &gr, void *workspace, hipStream_t s)
+{
+    const bool few = q4v::grouped_few(gr.G, gr.M, K);
+    const int bm = few ? 16 : 128, nblk = K >> 5;
+    const long long tiles = q4v::group_row_tiles(gr.G, gr.M, bm);
+    int *row_exp = static_cast<int *>(workspace);
+    u32x4 *ops = reinterpret_cast<u32x4 *>(static_cast<char *>(workspace) + q4v::grouped_exp_bytes(gr.G, gr.M, K));
+    const long long groups = tiles * (bm / 16);
+    const int part = prep_part_blocks(groups, nblk, 1);
+    hipError_t e = launch_kernel(few ? k_grouped_prep<F, BF, 16> : k_grouped_prep<F, BF, 128>,
+                                 dim3((unsigned)groups, (unsigned)((nblk + part - 1) / part)),
+                                 dim3(64 * kPrepWaves), 0, s, a, gr, row_exp, ops, K, part);
+    if (e != hipSuccess)
+        return e;
+    if (few) {
+        // Weight rows of a workgroup: as many as leave two workgroups for each
+        // compute unit (more of them share one pass over the operands).
+        const long long hit = gr.G < gr.M ? gr.G : gr.M;
+        const bool two = gr.M > 16LL * hit;   // more than 16 rows a group on average
+        constexpr int CTL = F::kBytes == kQ8Bytes ? 2 : 4;
+        if (hit * N >= 512LL * 16 * CTL)
+            return two ? launch_few<F, BF, CTL, 2>(ops, row_exp, w, y, N, K, gr, s)
+                       : launch_few<F, BF, CTL, 1>(ops, row_exp, w, y, N, K, gr, s);
+        return launch_few<F, BF, 1, 1>(ops, row_exp, w, y, N, K, gr, s);
+    }
+    const long long tn = ((long long)N + kGemmBN - 1) / kGemmBN;
+    const long long grid = group_grid(gr.G, gr.M, kGemmBM, tn);
+    if (grid > 0x7fffffffLL)
+        return hipErrorInvalidValue;
+    const KSegments sg = k_segments(nblk, 2);
+    for (int i = 0; i < sg.n; ++i) {
+        const int kb0 = i * sg.len, nb = min(sg.len, nblk - kb0);
+        e = launch_kernel(k_gemm_split_grouped<F, BF>, dim3((unsigned)grid), dim3(kSplitGemmThreads),
+                          0, s, (const u32x4 *)(ops + (size_t)kb0 * slab_ops<BF>()),
+                          w + (size_t)kb0 * F::kBytes, y, N, nblk, nb, (int)tn,
+                          (const int *)row_exp, i > 0 ? 1 : 0, gr);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_gemm_grouped(WeightFormat fmt, bool bf16, const void *a, const uint8_t *w,
+                               const int *offsets, const int *order, int share, float *y, int G,
+                               int M, int N, int K, void *workspace, hipStream_t s)
+{
+    const Groups gr = {offsets, order, G, M, share};
+    if (fmt == WeightFormat::kQ8_0)
+        return bf16 ? launch_grouped_f<FmtQ8_0, true>(a, w, y, N, K, gr, workspace, s)
+                    : launch_grouped_f<FmtQ8_0, false>(a, w, y, N, K, gr, workspace, s);
+    return bf16 ? launch_grouped_f<FmtQ4_0, true>(a, w, y, N, K, gr, workspace, s)
+                : launch_grouped_f<FmtQ4_0, false>(a, w, y, N, K, gr, workspace, s);
+}
+
+}  // namespace q4k

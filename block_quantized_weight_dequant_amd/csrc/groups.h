@@ -10,6 +10,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "validate.h"
 
 namespace q4k {
 
@@ -37,6 +38,7 @@ struct GroupTile {
     int e;        // group, or -1 past the last tile
     int lo, hi;   // its positions
     int mt, nt;   // row tile and column tile within the group
+    int before;   // row tiles of the groups before it
 };
 
 // Tile t of the grid that covers the groups one after another, each with
@@ -72,11 +74,27 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
             const int tm = (g.hi - g.lo + bm - 1) / bm, in = t - first;
             g.nt = in / tm;
             g.mt = in - g.nt * tm;
+            g.before = first / tiles_n;
             return g;
         }
         run += __builtin_amdgcn_readlane(sum, 63);
     }
-    return {-1, 0, 0, 0, 0};
+    return {-1, 0, 0, 0, 0, 0};
+}
+
+// Row tiles of bm rows in the groups before group e, by one wavefront.
+__device__ __forceinline__ int group_tiles_before(const Groups &gr, int e, int bm)
+{
+    int sum = 0;
+    for (int i = threadIdx.x & 63; i < e; i += 64) {
+        int lo, hi;
+        group_bounds(gr, i, lo, hi);
+        sum += (hi - lo + bm - 1) / bm;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        sum += __shfl_xor(sum, d);
+    return sum;
 }
 
 // Workgroups go to the eight XCDs in turn: tile index of workgroup L such that
@@ -87,9 +105,7 @@ __device__ __forceinline__ int xcd_runs(int L) { return (L & ~63) | ((L & 7) << 
 // Grid that covers every tile of at most M rows in G groups, whole runs.
 inline long long group_grid(long long G, long long M, long long bm, long long tiles_n)
 {
-    const long long extra = G < M ? G : M;   // groups that can end in a part of a tile
-    const long long t = (M / bm + extra) * tiles_n;
-    return (t + 63) / 64 * 64;
+    return (q4v::group_row_tiles(G, M, bm) * tiles_n + 63) / 64 * 64;
 }
 
 }  // namespace q4k

@@ -69,6 +69,14 @@ hipError_t launch_f8_dequant(const uint8_t *q, const float *s, float *out, int M
 // y: [M, N] bfloat16. K <= 2^22.
 hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
                           uint16_t *y, int M, int N, int K, hipStream_t st);
+// The router. workspace: q4v::route_workspace_bytes(T, E, top_k) bytes.
+hipError_t launch_route(const float *logits, int *ids, float *weights, int *offsets, int *order,
+                        void *workspace, int T, int E, int top_k, bool renorm, hipStream_t st);
+// The grouped products over Q4_0 and Q8_0 weights: f32 or bfloat16 (bf16)
+// activations; order may be null. workspace: q4v::grouped_workspace_bytes.
+hipError_t launch_gemm_grouped(WeightFormat fmt, bool bf16, const void *a, const uint8_t *w,
+                               const int *offsets, const int *order, int share, float *y, int G,
+                               int M, int N, int K, void *workspace, hipStream_t st);
 // order may be null; the activations' codes span less than 2^31 bytes.
 hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
                                   const float *w_s, const int *offsets, const int *order, int share,

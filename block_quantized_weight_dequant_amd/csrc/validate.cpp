@@ -312,4 +312,105 @@ int check_f8_product(const void *a, const void *a_s, const void *w, size_t w_byt
     return Q4_OK;
 }
 
+size_t grouped_workspace_bytes(int G, int M, int N, int K, int terms)
+{
+    if (check_group_shape(G, M, N, K, 64, 1 << 22, 1) != Q4_OK || M == 0 || N == 0)
+        return 0;
+    const int bm = grouped_few(G, M, K) ? 16 : 128;
+    size_t n = (size_t)group_row_tiles(G, M, bm) * (size_t)bm;   // below 2^39
+    if (!mul_ok(n, (size_t)K, &n) || !mul_ok(n, (size_t)terms * 2, &n))
+        return SIZE_MAX;
+    const size_t e = grouped_exp_bytes(G, M, K);
+    return n > SIZE_MAX - e ? SIZE_MAX : n + e;
+}
+
+int check_group_shape(int G, int M, int N, int K, int k_unit, int k_max, int share)
+{
+    if (G < 1 || G > Q4_MAX_EXPERTS || M < 0 || M > Q4_MAX_SLOTS || N < 0 || K < k_unit ||
+        K % k_unit != 0 || K > k_max || share < 1)
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+int check_grouped(const GroupedArgs &g)
+{
+    const bool scales = g.a_s_bytes != 0;
+    if (!g.a || !g.w || !g.offsets || !g.y || (scales && (!g.a_s || !g.w_s)))
+        return Q4_ERR_NULL;
+    if (!aligned16(g.a) || !aligned16(g.w) || !aligned16(g.offsets) || !aligned16(g.y) ||
+        !aligned16(g.order) || (scales && (!aligned16(g.a_s) || !aligned16(g.w_s))))
+        return Q4_ERR_ALIGN;
+    const Span y = {g.y, g.y_bytes};
+    if (overlaps(y, {g.a, g.a_bytes}) || overlaps(y, {g.w, g.w_bytes}) ||
+        overlaps(y, {g.offsets, (size_t)(g.G + 1) * 4}) ||
+        overlaps(y, {g.order, g.order ? (size_t)g.M * 4 : 0}) || overlaps(y, {g.a_s, g.a_s_bytes}) ||
+        overlaps(y, {g.w_s, g.w_s_bytes}))
+        return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
+int check_grouped_workspace(const GroupedArgs &g, size_t need, const void *ws, size_t ws_bytes)
+{
+    if (need == SIZE_MAX)
+        return Q4_ERR_SIZE;
+    if (ws_bytes < need)
+        return Q4_ERR_WORKSPACE;
+    if (!ws)
+        return Q4_ERR_NULL;
+    if (!aligned16(ws))
+        return Q4_ERR_ALIGN;
+    const Span w = {ws, need};
+    if (overlaps(w, {g.a, g.a_bytes}) || overlaps(w, {g.w, g.w_bytes}) ||
+        overlaps(w, {g.y, g.y_bytes}) || overlaps(w, {g.offsets, (size_t)(g.G + 1) * 4}) ||
+        overlaps(w, {g.order, g.order ? (size_t)g.M * 4 : 0}))
+        return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
+size_t route_workspace_bytes(int T, int E, int top_k)
+{
+    if (T <= 0 || E < 1 || E > Q4_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > Q4_MAX_TOP_K ||
+        (long long)T * top_k > Q4_MAX_SLOTS)
+        return 0;
+    return route_chunks(T) > 1 ? (size_t)route_chunks(T) * (size_t)E * 4 : 0;
+}
+
+int check_route(const void *logits, int T, int E, int top_k, const void *ids, const void *weights,
+                const void *offsets, const void *order, const void *ws, size_t ws_bytes, size_t need,
+                bool *empty)
+{
+    *empty = false;
+    if (T < 0 || E < 1 || E > Q4_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > Q4_MAX_TOP_K ||
+        (long long)T * top_k > Q4_MAX_SLOTS)
+        return Q4_ERR_SHAPE;
+    if (T == 0) {
+        *empty = true;
+        return Q4_OK;
+    }
+    if (!logits || !ids || !weights || !offsets || !order)
+        return Q4_ERR_NULL;
+    const size_t slots = (size_t)T * (size_t)top_k * 4;
+    const Span spans[6] = {{ids, slots}, {weights, slots}, {order, slots}, {offsets, (size_t)(E + 1) * 4},
+                           {logits, (size_t)T * (size_t)E * 4}, {ws, need}};
+    for (int i = 0; i < 5; ++i)
+        if (!aligned16(spans[i].p))
+            return Q4_ERR_ALIGN;
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 5; ++j)
+            if (overlaps(spans[i], spans[j]))
+                return Q4_ERR_ALIAS;
+    if (need == 0)
+        return Q4_OK;
+    if (ws_bytes < need)
+        return Q4_ERR_WORKSPACE;
+    if (!ws)
+        return Q4_ERR_NULL;
+    if (!aligned16(ws))
+        return Q4_ERR_ALIGN;
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(spans[i], spans[5]))
+            return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
 }  // namespace q4v

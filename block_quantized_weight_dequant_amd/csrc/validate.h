@@ -175,6 +175,73 @@ int check_f8_codec(const void *x, size_t x_elem, int M, int K, int block_rows, c
 int check_f8_product(const void *a, const void *a_s, const void *w, size_t w_bytes, const void *w_s,
                      const void *y, int M, int N, int K, int max_rows, bool *empty);
 
+// Ragged groups of rows (the products grouped by expert). Row tiles of bm rows
+// that M positions in G groups can take, every group ending in a part of one.
+inline long long group_row_tiles(long long G, long long M, long long bm)
+{
+    return M / bm + (G < M ? G : M);
+}
+
+// The grouped product's form. few: 16-row tiles streamed past the weights, for
+// groups of at most 32 rows on average; it needs 16-byte aligned weight rows
+// (K % 256 == 0) and keeps a wavefront's chain of block partials at 112 or
+// fewer (K <= 28672), as the GEMM's segments do. Otherwise 128-row tiles of
+// the GEMM's split kernel.
+inline bool grouped_few(int G, int M, int K)
+{
+    return K % 256 == 0 && K <= 28672 && (long long)M <= 32LL * G;
+}
+
+// Workspace of q4_gemm_grouped and its kin: the row exponents of the tiles'
+// rows (int32, padded to 256 bytes), then their operands, terms binary16 values
+// an element. 0 for an empty or invalid shape, SIZE_MAX when it does not fit.
+size_t grouped_workspace_bytes(int G, int M, int N, int K, int terms);
+inline size_t grouped_exp_bytes(int G, int M, int K)
+{
+    const int bm = grouped_few(G, M, K) ? 16 : 128;
+    return ((size_t)group_row_tiles(G, M, bm) * (size_t)bm * 4 + 255) / 256 * 256;
+}
+
+// Sizes, then pointers, of a grouped product: a (a_bytes in all, and a_s of
+// a_s_bytes, 0 if there is none), w (w_want bytes asked, w_bytes given), w_s,
+// offsets [G + 1], order [M] (may be NULL), y of y_bytes. Shapes are checked
+// before, by check_group_shape.
+int check_group_shape(int G, int M, int N, int K, int k_unit, int k_max, int share);
+struct GroupedArgs {
+    const void *a;
+    size_t a_bytes;
+    const void *a_s;
+    size_t a_s_bytes;
+    const void *w;
+    size_t w_bytes;
+    const void *w_s;
+    size_t w_s_bytes;
+    const void *offsets, *order, *y;
+    size_t y_bytes;
+    int G, M;
+};
+int check_grouped(const GroupedArgs &g);
+// The workspace against every span of g.
+int check_grouped_workspace(const GroupedArgs &g, size_t need, const void *ws, size_t ws_bytes);
+
+// q4_route.
+int check_route(const void *logits, int T, int E, int top_k, const void *ids, const void *weights,
+                const void *offsets, const void *order, const void *ws, size_t ws_bytes, size_t need,
+                bool *empty);
+// Tokens of a workgroup's chunk: up to kRouteOneChunk tokens one workgroup
+// does all; otherwise at least two for each of its 16 wavefronts, and at most
+// 256 chunks, over which every workgroup of the second launch adds.
+constexpr int kRouteOneChunk = 64;
+inline int route_chunk(int T)
+{
+    if (T <= kRouteOneChunk)
+        return kRouteOneChunk;
+    const int c = (T + 255) / 256;
+    return c < 32 ? 32 : c;
+}
+inline int route_chunks(int T) { return (T + route_chunk(T) - 1) / route_chunk(T); }
+size_t route_workspace_bytes(int T, int E, int top_k);
+
 bool aligned16(const void *p);
 bool overlaps(Span a, Span b);
 

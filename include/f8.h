@@ -83,6 +83,23 @@ int f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes
 int f8_gemv(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes, const float *w_s,
             uint16_t *y, int M, int N, int K, void *stream);
 
+/*
+ * f8_gemm_grouped — q4.h's q4_gemm_grouped over E4M3 weights and activations:
+ *   y[r, n] = sum_b a_s[r / share, b] w_s[e, n / 128, b] sum_{k in b} a w
+ * for the rows r of each group e.
+ *   a, a_s      codes [ceil(M / share), K], scales [.., ceil(K / 128)]; the
+ *               codes span less than 2^31 bytes (else Q4_ERR_SHAPE).
+ *   w, w_bytes  G weight matrices [N, K], w_bytes == G * N * K.
+ *   w_s         their scales, [G, ceil(N / 128), ceil(K / 128)].
+ *   y           [M, N] bfloat16. Rows that no group names are left as they were.
+ *   offsets, order, share, G, M, and what wrong list contents do: as
+ *   q4_gemm_grouped. K as f8_gemm. No workspace.
+ * Accuracy: as f8_gemm. Deterministic for rows named once.
+ */
+int f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,
+                    const float *w_s, const int32_t *offsets, const int32_t *order, int share,
+                    uint16_t *y, int G, int M, int N, int K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,7 @@
 extern "C" {
 #endif
 
-#define Q4_ABI_VERSION 10
+#define Q4_ABI_VERSION 11
 
 #define Q4_OK 0
 #define Q4_ERR_NULL 1   /* a required pointer is NULL */
@@ -59,6 +59,12 @@ extern "C" {
 
 /* Largest number of activation rows q4_gemv and q8_gemv accept. */
 #define Q4_GEMV_MAX_ROWS 8
+
+/* Largest expert (group) count and choices per token, and most slots or rows
+ * of a grouped call (2^30). */
+#define Q4_MAX_EXPERTS 1024
+#define Q4_MAX_TOP_K 32
+#define Q4_MAX_SLOTS 1073741824
 
 /* Bytes of device memory each GPU holds for q4_gemm and q8_gemm (64 MiB). */
 #define Q4_GEMM_SCRATCH_BYTES 67108864u
@@ -419,6 +425,94 @@ int q8_gemm_q8a(const void *a_q, size_t a_bytes, const void *w_q, size_t w_bytes
 
 /* q8_gemm_q8a_workspace_bytes — the same function as q4_gemm_q8a_workspace_bytes. */
 size_t q8_gemm_q8a_workspace_bytes(int M, int N, int K);
+
+/*
+ * q4_route — the router of a mixture of experts: each token's top_k experts,
+ * their weights, and the token slots grouped by expert, which the grouped
+ * products (below, and f8.h's) take.
+ *   logits    [T, E] f32. -inf masks an expert; any other value is finite.
+ *   T, E, top_k  T >= 0, 1 <= E <= Q4_MAX_EXPERTS, 1 <= top_k <= min(E,
+ *             Q4_MAX_TOP_K), T * top_k <= Q4_MAX_SLOTS (else Q4_ERR_SHAPE).
+ *   renorm    non-zero: the weights are the softmax over the chosen experts;
+ *             zero: the chosen experts' share of the softmax over all E.
+ *   ids       [T, top_k] int32: the experts of the largest logits, in falling
+ *             order, the lowest expert first among equal logits (-0 equals +0).
+ *   weights   [T, top_k] f32. 0 where every expert of the token is masked.
+ *   offsets   [E + 1] int32, order [T * top_k] int32: positions offsets[e] ..
+ *             offsets[e + 1] - 1 of order hold the slots t * top_k + j with
+ *             ids[t, j] == e, in rising order.
+ *   workspace, workspace_bytes: q4_route_workspace_bytes(T, E, top_k) bytes of
+ *             device scratch (0, NULL allowed, up to 64 tokens), as for
+ *             q4_gemm_ws (Q4_ERR_WORKSPACE when smaller).
+ * The choice, offsets and order are exact and deterministic. Weights are exp
+ * in f32 of exact-to-rounding differences, summed in f32: within (E + 16) 2^-24
+ * of the exact value, relative, plus 2^-126. T == 0 is an empty problem:
+ * nothing is written, offsets included. NaN logits give unspecified weights;
+ * ids, offsets and order stay a valid grouping.
+ */
+int q4_route(const float *logits, int T, int E, int top_k, int renorm, int32_t *ids,
+             float *weights, int32_t *offsets, int32_t *order, void *workspace,
+             size_t workspace_bytes, void *stream);
+
+/* q4_route_workspace_bytes — 0 up to 64 tokens and for invalid or empty shapes,
+ * else at most 256 * E * 4. Pure function of its arguments. */
+size_t q4_route_workspace_bytes(int T, int E, int top_k);
+
+/*
+ * q4_gemm_grouped — products grouped by expert with ragged sizes: for every
+ * group e and every row r that the list names for it,
+ *   y[r, n] = sum_k a[r / share, k] dequant(W[e])[n, k].
+ *   a         [ceil(M / share), K] f32. share >= 1 (else Q4_ERR_SHAPE): the
+ *             slots of one token are consecutive, so share = top_k multiplies
+ *             each token's row by all its experts, share = 1 takes a row per slot.
+ *   w_q       G weight matrices [N, K/32] Q4_0, one after another: w_bytes ==
+ *             G * N * (K/32) * 18 (else Q4_ERR_SIZE).
+ *   offsets   [G + 1] int32 on the device, order [M] int32 on the device:
+ *             group e's rows are order[offsets[e]] .. order[offsets[e + 1] - 1],
+ *             as q4_route writes them. order may be NULL: then the rows are
+ *             already sorted, and position p is row p. Groups may be empty.
+ *   y         [M, N] f32. Rows that no group names are left as they were.
+ *   G in [1, Q4_MAX_EXPERTS], 0 <= M <= Q4_MAX_SLOTS, N >= 0, K a positive
+ *   multiple of 64, K <= 2^22 (else Q4_ERR_SHAPE).
+ *   workspace, workspace_bytes: at least q4_gemm_grouped_workspace_bytes(G, M,
+ *             N, K), as for q4_gemm_ws.
+ * The contents of offsets and order are read on the device only, and kept in
+ * bounds there: a bound is clamped to [previous bound of the same group, M],
+ * a row outside [0, M) is skipped, and a row named twice gets one of its
+ * values, element by element. Errors in the order shape, size, empty (M == 0
+ * or N == 0), NULL, alignment, overlap, workspace.
+ * Accuracy: as q4_gemm_ws. Deterministic for rows named once.
+ */
+int q4_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                    const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* q4_gemm_grouped_bf16 — the same with bfloat16 activations (raw 16-bit
+ * patterns; accuracy as q4_gemm_bf16). */
+int q4_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                         const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* q8_gemm_grouped, q8_gemm_grouped_bf16 — the same over Q8_0 weights (w_bytes
+ * == G * N * (K/32) * 34). */
+int q8_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                    const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                    void *workspace, size_t workspace_bytes, void *stream);
+int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
+                         const int32_t *order, int share, float *y, int G, int M, int N, int K,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * q4_gemm_grouped_workspace_bytes and its kin — the row exponents and operands
+ * of the groups' row tiles. With bm = 16 when K % 256 == 0, K <= 28672 and M
+ * <= 32 G, else 128, and R = (M / bm + min(G, M)) * bm rows: R * 4 bytes padded
+ * to 256, then R * K * 4 (f32) or R * K * 2 (bfloat16). 0 for invalid or empty
+ * shapes, SIZE_MAX on overflow. Pure functions of their arguments.
+ */
+size_t q4_gemm_grouped_workspace_bytes(int G, int M, int N, int K);
+size_t q4_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K);
+size_t q8_gemm_grouped_workspace_bytes(int G, int M, int N, int K);
+size_t q8_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K);
 
 /*
  * q8_quantize — f32 to Q8_0 blocks (section quantize_q8_0).
