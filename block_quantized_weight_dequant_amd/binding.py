@@ -148,10 +148,13 @@ def _nbytes(x) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
+        # Before PyTorch has initialised the GPU its current stream is the
+        # default one. The raw handle costs 0.3 us a call, against 3.5 us
+        # through a torch.cuda.Stream object.
         import torch
-        if not torch.cuda.is_available():
+        if not torch.cuda.is_initialized():
             return 0
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

@@ -71,6 +71,19 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
                max((uint32_t)__builtin_amdgcn_readlane(x, 32), (uint32_t)__builtin_amdgcn_readlane(x, 48)));
 }
 
+// f(integral_constant<int, 0>{}) .. f(integral_constant<int, N - 1>{}), in order:
+// a loop whose index is a constant, however long its body.
+template <class F, int... I>
+__device__ __forceinline__ void unroll_impl(F &&f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unroll(F &&f)
+{
+    unroll_impl(f, std::make_integer_sequence<int, N>{});
+}
+
 // Direct-to-LDS loads of 16 and of 4 bytes a lane: lane l's bytes go to dst +
 // 16 l (4 l).
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void *dst, uint32_t off, int base)

@@ -9,6 +9,7 @@
 #include "device_common.h"
 #include "groups.h"
 #include "launch.h"
+#include <stdlib.h>
 
 namespace q4k {
 
@@ -455,50 +456,87 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_f8_skinny_grouped(F8Produ
 }
 
 // Many rows: bound by the matrix instructions. A workgroup of eight wavefronts
-// computes BN x BM of y^T. Per step of 128 KG of K it stages both operands and
-// the activation scales in LDS by direct loads, one stage ahead; 16-byte
-// pieces of a row's 128 bytes are stored at piece ^ (row % 8), so that the 8
-// rows that an LDS read serves at a time lie in different banks (the lanes'
-// global addresses carry the permutation; the LDS side of a direct load is
-// contiguous).
-//   WN x WM wavefronts of TN x TM tiles each, KG groups of them: with KG = 2
-//   the second group takes the odd blocks of K and the two tiles are added
-//   through LDS at the end, so that a small tile still has two wavefronts a
-//   SIMD and one's FMAs run beside the other's matrix instructions.
-template <int WN_, int WM_, int TN_, int TM_, int KG_>
+// computes BN x BM of y^T, WN x WM wavefronts of TN x TM tiles each. Per step
+// (one block of K) it stages both operands in LDS by direct loads, in a ring of
+// NS stages; 16-byte pieces of a row's 128 bytes are
+// stored at piece ^ (row % 8), so that the 8 rows that an LDS read serves at a
+// time lie in different banks (the lanes' global addresses carry the
+// permutation; the LDS side of a direct load is contiguous). The activation
+// scales of eight steps are staged at a time: loaded step by step, a scale of
+// each of 64 rows a load, they took as many cache lines as both operands twice
+// over.
+template <int WN_, int WM_, int TN_, int TM_, int NS_>
 struct TileShape {
-    static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, KG = KG_;
+    static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NS = NS_;
     static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-    static constexpr int kThreads = 64 * WN * WM * KG;
-    static constexpr int kWLoads = BN * 8 * KG / kThreads, kALoads = BM * 8 * KG / kThreads;
-    static constexpr int kSWaves = BM * KG / 64;   // wavefronts that load scales
-    static_assert(BN * 8 * KG % kThreads == 0 && BM * 8 * KG % kThreads == 0 && BM * KG % 64 == 0, "whole loads");
-    static_assert(kSWaves <= kThreads / 64, "one scale load a wavefront");
+    static constexpr int kThreads = 64 * WN * WM;
+    static constexpr int kWLoads = BN * 8 / kThreads, kALoads = BM * 8 / kThreads;
+    static constexpr int kLoads = kWLoads + kALoads;       // of every wavefront and step
+    static constexpr int kSLoads = BM * 8 / kThreads;      // of a chunk of scales
+    static constexpr int kInFlight = (NS - 2) * kLoads;    // younger than the stage that a turn waits for
+    // Matrix instructions of a step and wavefront; the one before which the
+    // stages change over, with one column of tiles to go.
+    static constexpr int kTiles = TN * TM, kTurn = (TM - 1) * TN;
+    // Slots of a step's loads: behind the matrix instructions from the turn to
+    // the end of the step, then of the next step's first kSpread (which end
+    // before its turn; with two stages the loads must land by then, so they
+    // stop earlier). kTailLoads of the loads fall before the step's end.
+    static constexpr int kSpread = NS == 2 ? 2 * TN : kTurn, kSlots = TN + kSpread;
+    static constexpr int kTailLoads = TN * kLoads / kSlots;
+    static constexpr int kRowBytes = BN * 2 + 16;          // of a row of y in LDS
+    static_assert(BN * 8 % kThreads == 0 && BM * 8 % kThreads == 0 && BM % 64 == 0 && BM <= kThreads, "whole loads");
     static_assert(TN * 16 <= 128 && 128 % (TN * 16) == 0, "a wavefront's columns share a weight scale");
+    static_assert(TM % 2 == 0, "activation operands alternate between two registers");
+    static_assert(NS >= 2 && kInFlight < 64, "vmcnt counts to 63");
 };
 
 template <class S>
 struct TileLds {
-    u32x4 w[2][S::KG * S::BN * 8];
-    u32x4 a[2][S::KG * S::BM * 8];
-    float s[2][S::KG * S::BM];
+    union {
+        struct {
+            u32x4 w[S::NS][S::BN * 8];
+            u32x4 a[S::NS][S::BM * 8];
+        };
+        uint8_t y[S::BM * S::kRowBytes];
+    };
+    float s[2][S::BM * 8];   // of eight steps: [row / 8][step][row % 8]
     int row[S::BM];
 };
 
 constexpr uint32_t kOutOfRange = 0x80000000u;   // past every resource below (each spans at most 2^31 bytes)
 constexpr int kRawBuffer = 0x00020000;          // resource word 3: raw, 32-bit data format
 
+// Wait until at most VM of the wavefront's loads are in flight and its LDS
+// operations are done, then meet the others.
+template <int VM>
 __device__ __forceinline__ void wait_and_meet()
 {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
+// Tiles to XCDs (workgroup index mod 8): XCD (x, y) of an nx x ny grid takes a
+// rectangle of rn x rm tiles, walked in strips of eight row tiles, so that the
+// workgroups that run on it together share both operands in its L2.
+struct TileOrder {
+    int tn, tm;   // tiles
+    int nx, rn, rm;
+};
+
+__device__ __forceinline__ bool tile_of(const TileOrder &o, int &nt, int &mt)
+{
+    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int xn = x % o.nx, xm = x / o.nx;
+    const int strip = i / (8 * o.rn), h = min(8, o.rm - 8 * strip), r = i - strip * 8 * o.rn;
+    nt = xn * o.rn + r / h;
+    mt = xm * o.rm + 8 * strip + r % h;
+    return nt < o.tn && mt < o.tm;
+}
+
 template <class S, bool GROUPED>
-__global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, int tiles_m,
-                                                          int tiles_n)
+__global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, TileOrder order)
 {
     __shared__ TileLds<S> lds;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -507,7 +545,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     const uint8_t *w = p.w;
     const float *w_s = p.w_s;
     if constexpr (GROUPED) {
-        const GroupTile g = find_group_tile(gr, xcd_runs(blockIdx.x), S::BM, tiles_n);
+        const GroupTile g = find_group_tile(gr, xcd_runs(blockIdx.x), S::BM, order.tn);
         if (g.e < 0)
             return;
         mt = g.mt, nt = g.nt;
@@ -519,18 +557,13 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
             lds.row[tid] = tid < rows ? group_row(gr, lo + tid) : -1;
         __syncthreads();
     } else {
-        // XCD x (workgroup index mod 8) takes a contiguous run of the tiles,
-        // row tiles fastest: its L2 holds few weight columns at a time.
-        const int T = tiles_m * tiles_n, per = (T + 7) / 8;
-        const int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-        if ((int)(blockIdx.x >> 3) >= per || t >= T)
+        if (!tile_of(order, nt, mt))
             return;
-        nt = t / tiles_m, mt = t - nt * tiles_m;
         rows = min(S::BM, p.M - mt * S::BM);
     }
     const int n0 = nt * S::BN, m0 = mt * S::BM;
     const int li = lane & 15, g = lane >> 4;
-    const int kg = wave / (S::WN * S::WM), wn = wave % S::WN, wm = (wave / S::WN) % S::WM;
+    const int wn = wave % S::WN, wm = wave / S::WN;
 
     // Resources: this tile's weight rows; its activation rows and scales, or
     // (grouped) all of them.
@@ -553,51 +586,55 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
             return r < rows ? r : -1;
         }
     };
-    uint32_t wo[S::kWLoads], ao[S::kALoads], so = kOutOfRange;
-    // K offset of each load's piece, for the last step.
-    int wk[S::kWLoads], ak[S::kALoads], sk = 0;
+    // Offsets of this lane's pieces in step 0. Load j of a wavefront covers rows
+    // of one residue mod 8, so its piece of the row is the same in all of them.
+    uint32_t wo[S::kWLoads], ao[S::kALoads], so[S::kSLoads];
+    const int piece = ((tid ^ (tid >> 3)) & 7) * 16;
+    static_assert(S::kThreads % 64 == 0, "rows of a load are equal mod 8");
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
-        const int c = j * S::kThreads + tid, r = c / 8 % S::BN;
-        wk[j] = c / (8 * S::BN) * 128 + ((c ^ r) & 7) * 16;
-        wo[j] = r < wrows ? (uint32_t)r * (uint32_t)p.K + (uint32_t)wk[j] : kOutOfRange;
+        const int r = (j * S::kThreads + tid) >> 3;
+        wo[j] = r < wrows ? (uint32_t)r * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
     }
 #pragma unroll
     for (int j = 0; j < S::kALoads; ++j) {
-        const int c = j * S::kThreads + tid, r = c / 8 % S::BM, x = a_row(r);
-        ak[j] = c / (8 * S::BM) * 128 + ((c ^ r) & 7) * 16;
-        ao[j] = x >= 0 ? (uint32_t)x * (uint32_t)p.K + (uint32_t)ak[j] : kOutOfRange;
+        const int x = a_row((j * S::kThreads + tid) >> 3);
+        ao[j] = x >= 0 ? (uint32_t)x * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
     }
-    if (wave < S::kSWaves) {
-        const int x = a_row(tid % S::BM);
-        sk = tid / S::BM;
-        so = x >= 0 ? ((uint32_t)x * (uint32_t)p.Kb + (uint32_t)sk) * 4u : kOutOfRange;
+#pragma unroll
+    for (int j = 0; j < S::kSLoads; ++j) {
+        const int x = a_row((j * S::kThreads + tid) / 64 * 8 + (lane & 7));
+        so[j] = x >= 0 ? ((uint32_t)x * (uint32_t)p.Kb + (uint32_t)(lane >> 3)) * 4u : kOutOfRange;
     }
-    constexpr int kStepK = 128 * S::KG;
-    const int steps = (p.K + kStepK - 1) / kStepK;
-    auto issue = [&](int step) __attribute__((always_inline)) {
-        const int st = step & 1, k0 = step * kStepK;
-        if (k0 + kStepK <= p.K) {
+    const int steps = p.Kb;
+    // Called before a step's loads, in order of the steps: in a short last step
+    // the pieces past K, and after it everything, move out of range, where they
+    // read as zero. No earlier step needs the offsets again.
+    auto trim = [&](int step) __attribute__((always_inline)) {
+        const int left = p.K - step * 128;
+        if (left >= 128)
+            return;
+        const bool out = piece >= left;
 #pragma unroll
-            for (int j = 0; j < S::kWLoads; ++j)
-                load16_to_lds(wr, lds.w[st] + j * S::kThreads + wave * 64, wo[j], k0);
+        for (int j = 0; j < S::kWLoads; ++j)
+            wo[j] = out ? kOutOfRange : wo[j];
 #pragma unroll
-            for (int j = 0; j < S::kALoads; ++j)
-                load16_to_lds(ar, lds.a[st] + j * S::kThreads + wave * 64, ao[j], k0);
-            if (wave < S::kSWaves)
-                load4_to_lds(sr, lds.s[st] + wave * 64, so, step * (S::KG * 4));
-        } else {   // pieces past K read as zero
+        for (int j = 0; j < S::kALoads; ++j)
+            ao[j] = out ? kOutOfRange : ao[j];
+    };
+    // The scales of steps 8 c .. 8 c + 7; those past the last step read as zero.
+    auto issue_scales = [&](int c) __attribute__((always_inline)) {
+        const bool in = 8 * c + (lane >> 3) < steps;
 #pragma unroll
-            for (int j = 0; j < S::kWLoads; ++j)
-                load16_to_lds(wr, lds.w[st] + j * S::kThreads + wave * 64,
-                              k0 + wk[j] < p.K ? wo[j] : kOutOfRange, k0);
-#pragma unroll
-            for (int j = 0; j < S::kALoads; ++j)
-                load16_to_lds(ar, lds.a[st] + j * S::kThreads + wave * 64,
-                              k0 + ak[j] < p.K ? ao[j] : kOutOfRange, k0);
-            if (wave < S::kSWaves)
-                load4_to_lds(sr, lds.s[st] + wave * 64, step * S::KG + sk < p.Kb ? so : kOutOfRange, step * (S::KG * 4));
-        }
+        for (int j = 0; j < S::kSLoads; ++j)
+            load4_to_lds(sr, lds.s[c & 1] + j * S::kThreads + wave * 64, in ? so[j] : kOutOfRange, c * 32);
+    };
+    // Load l of a step into its stage st.
+    auto issue = [&](int step, int st, int l) __attribute__((always_inline)) {
+        if (l < S::kWLoads)
+            load16_to_lds(wr, lds.w[st] + l * S::kThreads + wave * 64, wo[l], step * 128);
+        else
+            load16_to_lds(ar, lds.a[st] + (l - S::kWLoads) * S::kThreads + wave * 64, ao[l - S::kWLoads], step * 128);
     };
 
     f32x4 acc[S::TN][S::TM];
@@ -607,92 +644,194 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         for (int j = 0; j < S::TM; ++j)
             acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     const int nb = min((n0 + wn * (S::TN * 16)) >> 7, p.Nb - 1);
-    const float *wsp = w_s + (size_t)nb * (size_t)p.Kb;
+    // Uniform over the wavefront: read through the scalar cache, so that waiting
+    // for it does not wait for the vector loads in flight.
+    const __attribute__((address_space(4))) int *wsp =
+        (const __attribute__((address_space(4))) int *)(uintptr_t)(w_s + (size_t)nb * (size_t)p.Kb);
 
     // Operand of a 16-row tile in LDS: pieces g and 4 + g of row li.
-    auto operand = [&](const u32x4 *base, int r0) __attribute__((always_inline)) {
-        const int r = r0 + li;
-        return join(base[r * 8 + (g ^ (r & 7))], base[r * 8 + ((4 + g) ^ (r & 7))]);
+    const int o0 = li * 8 + (g ^ (li & 7)), o1 = li * 8 + ((4 + g) ^ (li & 7));
+    auto operand = [&](const u32x4 *base) __attribute__((always_inline)) { return join(base[o0], base[o1]); };
+    auto w_operand = [&](int st, int i) __attribute__((always_inline)) {
+        return operand(lds.w[st] + (wn * S::TN + i) * 128);
+    };
+    auto a_operand = [&](int st, int j) __attribute__((always_inline)) {
+        return operand(lds.a[st] + (wm * S::TM + j) * 128);
     };
 
-    issue(0);
-    for (int step = 0; step < steps; ++step) {
-        // This step's stage has landed, and every wavefront has read the
-        // other one, which the next step's loads then fill.
-        wait_and_meet();
-        if (step + 1 < steps)
-            issue(step + 1);
-        const int st = step & 1;
-        const float ws = wsp[min(step * S::KG + kg, p.Kb - 1)];
-        const u32x4 *wb = lds.w[st] + kg * (S::BN * 8), *ab = lds.a[st] + kg * (S::BM * 8);
-        const float *sb = lds.s[st] + kg * S::BM + wm * (S::TM * 16) + li;
-        i32x8 wf[S::TN];
+    auto read_scales = [&](int step, float (&to)[S::TM]) __attribute__((always_inline)) {
+        const float *base = lds.s[(step >> 3) & 1] + (wm * S::TM * 2 + (li >> 3)) * 64 + (step & 7) * 8 + (li & 7);
 #pragma unroll
-        for (int i = 0; i < S::TN; ++i)
-            wf[i] = operand(wb, wn * (S::TN * 16) + i * 16);
+        for (int x = 0; x < S::TM; ++x)
+            to[x] = base[x * 128];
+    };
+
+    // The pipeline. Step s multiplies stage s mod NS. Its weight operands, its
+    // first activation operand and its scales are in registers when it begins.
+    // At kTurn every wavefront has read the last of the stage (the wait and the
+    // barrier) and the next stage has landed: the step's last column of tiles
+    // runs from registers while each weight operand that it has used is read
+    // again from the next stage, and the loads of step s + NS begin to fill the
+    // stage just left; they are spread into the next step, since a burst of
+    // them from every wavefront at once stalls the issue of all. No step begins by waiting for LDS. Tile t's FMAs follow
+    // matrix instruction t + kLag, when its result is ready. The group barriers
+    // keep that order; the empty asm keeps the FMAs where they are written.
+    constexpr int kLag = 2;
+    i32x8 wf[S::TN], af[2];
+    float as[S::TM];
+    int ws_next;
+    auto run_step = [&](auto st_c, int step) __attribute__((always_inline)) {
+        constexpr int P = decltype(st_c)::value, Q = (P + 1) % S::NS;
+        float sc[S::TM];
+        f32x4 c[kLag + 1];
+        const float ws = __int_as_float(ws_next);
 #pragma unroll
-        for (int j = 0; j < S::TM; ++j) {
-            const i32x8 af = operand(ab, wm * (S::TM * 16) + j * 16);
-            const float s = sb[j * 16] * ws;
-#pragma unroll
-            for (int i = 0; i < S::TN; ++i) {
-                const f32x4 c = mfma_block(wf[i], af);
+        for (int j = 0; j < S::TM; ++j)
+            sc[j] = as[j] * ws;
+        // Chunk step / 8 - 1 was last read before the previous step's end, so
+        // the next chunk may take its place; it lands within eight steps, older
+        // by then than any load that a turn leaves in flight.
+        if ((step & 7) == 0)
+            issue_scales((step >> 3) + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        unroll<S::kTiles + kLag>([&](auto t_c) __attribute__((always_inline)) {
+            constexpr int t = decltype(t_c)::value, i = t % S::TN, j = t / S::TN;
+            if constexpr (t == S::kTurn) {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_and_meet<S::kInFlight>();
+                asm volatile("" : "+s"(ws_next));
+                trim(step + S::NS);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (t < S::kTiles) {
+                c[t % (kLag + 1)] = mfma_block(wf[i], af[j & 1]);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if constexpr (i == 0 && j + 1 < S::TM) {
+                    af[(j + 1) & 1] = a_operand(P, j + 1);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                }
+                if constexpr (t == S::kTurn - S::TN) {
+                    // Here no LDS result is waited for before the turn, so the
+                    // scalar load in flight makes no such wait longer.
+                    __builtin_amdgcn_sched_barrier(0);
+                    ws_next = wsp[min(step + 1, p.Kb - 1)];
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if constexpr (t >= S::kTurn && t < S::kTiles) {
+                wf[i] = w_operand(Q, i);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                if constexpr (i == 0) {   // the last column reads af[1]
+                    af[0] = a_operand(Q, 0);
+                    read_scales(step + 1, as);
+                }
+            }
+            if constexpr (t < S::kSpread || (t >= S::kTurn && t < S::kTiles)) {
+                constexpr bool tail = t >= S::kTurn;
+                constexpr int u = tail ? i : S::TN + t;
+                constexpr int l0 = u * S::kLoads / S::kSlots, l1 = (u + 1) * S::kLoads / S::kSlots;
+                unroll<l1 - l0>([&](auto l) __attribute__((always_inline)) {
+                    issue(step + S::NS - (tail ? 0 : 1), tail ? P : (P + S::NS - 1) % S::NS, l0 + l.value);
+                    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                });
+            }
+            if constexpr (t >= kLag) {
+                constexpr int u = t - kLag, ui = u % S::TN, uj = u / S::TN;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    acc[i][j][q] = fmaf(s, c[q], acc[i][j][q]);
+                    acc[ui][uj][q] = fmaf(sc[uj], c[u % (kLag + 1)][q], acc[ui][uj][q]);
+                asm volatile("" : "+v"(acc[ui][uj]));
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+            }
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    issue_scales(0);
+#pragma unroll
+    for (int s = 0; s < S::NS; ++s) {
+        trim(s);
+#pragma unroll
+        for (int l = 0; l < (s < S::NS - 1 ? S::kLoads : S::kTailLoads); ++l)
+            issue(s, s, l);
+    }
+    ws_next = wsp[0];
+    wait_and_meet<S::kInFlight + S::kTailLoads>();
+#pragma unroll
+    for (int i = 0; i < S::TN; ++i)
+        wf[i] = w_operand(0, i);
+    af[0] = a_operand(0, 0);
+    read_scales(0, as);
+    for (int step = 0; step < steps; step += S::NS)
+        unroll<S::NS>([&](auto s) __attribute__((always_inline)) {
+            if (step + s.value < steps)
+                run_step(s, step + s.value);
+        });
+    wait_and_meet<0>();   // no load is on its way into the LDS that the epilogue uses
+
+    // y: through LDS, so that whole rows of the tile leave as 16-byte stores of
+    // consecutive lanes (where the rows of y allow them).
+    auto y_row = [&](int r) __attribute__((always_inline)) {
+        if constexpr (GROUPED)
+            return lds.row[r];
+        else
+            return r < rows ? m0 + r : -1;
+    };
+    if ((p.N & 7) == 0) {
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
+            uint8_t *row = lds.y + ((wm * S::TM + j) * 16 + li) * S::kRowBytes + (wn * (S::TN * 16) + 4 * g) * 2;
+#pragma unroll
+            for (int i = 0; i < S::TN; ++i) {
+                const f32x4 v = acc[i][j];
+                *reinterpret_cast<bf16x4 *>(row + i * 32) = (bf16x4){(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
             }
         }
-    }
-    if constexpr (S::KG == 2) {
-        wait_and_meet();
-        f32x4 *red = reinterpret_cast<f32x4 *>(&lds.w[0][0]);
-        static_assert(sizeof(lds.w) + sizeof(lds.a) >= S::WN * S::WM * S::TN * S::TM * 64 * sizeof(f32x4), "reduction buffer");
-        const int wq = wave % (S::WN * S::WM);
-        if (kg == 1) {
+        __syncthreads();
+        constexpr int kLanes = S::BN / 8, kRowsAtOnce = S::kThreads / kLanes;   // 16-byte pieces of a row
+        const int n = n0 + tid % kLanes * 8;
+        for (int r = tid / kLanes; r < S::BM; r += kRowsAtOnce) {
+            const int to = y_row(r);
+            if (to >= 0 && n < p.N)
+                *reinterpret_cast<u32x4 *>(p.y + (size_t)to * (size_t)p.N + n) =
+                    *reinterpret_cast<const u32x4 *>(lds.y + r * S::kRowBytes + tid % kLanes * 16);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
+            const int to = y_row((wm * S::TM + j) * 16 + li);
+            if (to < 0)
+                continue;
+            uint16_t *yp = p.y + (size_t)to * (size_t)p.N;
 #pragma unroll
             for (int i = 0; i < S::TN; ++i)
-#pragma unroll
-                for (int j = 0; j < S::TM; ++j)
-                    red[((wq * S::TN + i) * S::TM + j) * 64 + lane] = acc[i][j];
+                store4(yp, n0 + wn * (S::TN * 16) + i * 16 + 4 * g, p.N, acc[i][j]);
         }
-        __syncthreads();
-        if (kg == 1)
-            return;
-#pragma unroll
-        for (int i = 0; i < S::TN; ++i)
-#pragma unroll
-            for (int j = 0; j < S::TM; ++j)
-                acc[i][j] += red[((wq * S::TN + i) * S::TM + j) * 64 + lane];
-    }
-#pragma unroll
-    for (int j = 0; j < S::TM; ++j) {
-        const int r = wm * (S::TM * 16) + j * 16 + li;
-        int y_row;
-        if constexpr (GROUPED)
-            y_row = lds.row[r];
-        else
-            y_row = r < rows ? m0 + r : -1;
-        if (y_row < 0)
-            continue;
-        uint16_t *yp = p.y + (size_t)y_row * (size_t)p.N;
-#pragma unroll
-        for (int i = 0; i < S::TN; ++i)
-            store4(yp, n0 + wn * (S::TN * 16) + i * 16 + 4 * g, p.N, acc[i][j]);
     }
 }
 
-using TileLarge = TileShape<2, 4, 8, 4, 1>;    // 256 columns x 256 rows
-using TileMedium = TileShape<2, 2, 4, 4, 2>;   // 128 x 128
+using TileLarge = TileShape<2, 4, 8, 4, 2>;    // 256 columns x 256 rows
+using TileWide = TileShape<4, 2, 4, 4, 3>;     // 256 x 128
+using TileSmall = TileShape<2, 4, 4, 2, 4>;    // 128 x 128
 
 template <class S>
 static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
 {
+    static_assert(sizeof(TileLds<S>) <= 160 * 1024, "the ring fits in LDS");
     const long long tm = ((long long)p.M + S::BM - 1) / S::BM, tn = ((long long)p.N + S::BN - 1) / S::BN;
-    const long long grid = (tm * tn + 7) / 8 * 8;
-    if (grid > 0x7fffffffLL)
+    // The split of the tiles over the XCDs that leaves the fewest slots empty,
+    // and of those the one whose rectangle is nearest a square.
+    TileOrder o = {(int)tn, (int)tm, 0, 0, 0};
+    long long best = 0;
+    for (int nx = 1; nx <= 8; nx *= 2) {
+        const long long rn = (tn + nx - 1) / nx, rm = (tm + 8 / nx - 1) / (8 / nx);
+        if (!best || rn * rm < best || (rn * rm == best && rn + rm < (long long)o.rn + o.rm))
+            best = rn * rm, o.nx = nx, o.rn = (int)rn, o.rm = (int)rm;
+    }
+    if (best * 8 > 0x7fffffffLL)
         return hipErrorInvalidValue;
-    return launch_kernel(k_f8_tile<S, false>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p,
-                         Groups{nullptr, nullptr, 0, 0, 1}, (int)tm, (int)tn);
+    return launch_kernel(k_f8_tile<S, false>, dim3((unsigned)(best * 8)), dim3(S::kThreads), 0, st, p,
+                         Groups{nullptr, nullptr, 0, 0, 1}, o);
 }
 
 template <int R>
@@ -700,6 +839,14 @@ static hipError_t launch_skinny(const F8Product &p, hipStream_t st)
 {
     return launch_kernel(k_f8_skinny<R>, dim3((unsigned)(((long long)p.N + 15) / 16), (unsigned)((p.M + 16 * R - 1) / (16 * R))),
                          dim3(64 * kSkinnyWaves), 0, st, p);
+}
+
+static int f8_form(int M, int N)
+{
+    if (const char *e = getenv("F8FORM"))
+        return atoi(e);
+    const long long large = (((long long)M + 255) / 256) * (((long long)N + 255) / 256);
+    return large >= 256 ? 2 : 0;
 }
 
 hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
@@ -712,10 +859,12 @@ hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, 
         return launch_skinny<2>(p, st);
     if (M <= 64)
         return launch_skinny<4>(p, st);
-    const long long large = (((long long)M + 255) / 256) * (((long long)N + 255) / 256);
-    if (large >= 256)
+    const int form = f8_form(M, N);
+    if (form == 2)
         return launch_tiles<TileLarge>(p, st);
-    return launch_tiles<TileMedium>(p, st);
+    if (form == 1)
+        return launch_tiles<TileWide>(p, st);
+    return launch_tiles<TileSmall>(p, st);
 }
 
 hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
@@ -727,13 +876,13 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
     if ((long long)M <= 32LL * G)
         return launch_kernel(k_f8_skinny_grouped, dim3((unsigned)(((long long)N + 15) / 16), (unsigned)G),
                              dim3(64 * kSkinnyWaves), 0, st, p, gr);
-    using S = TileMedium;
+    using S = TileSmall;
     const long long tn = ((long long)N + S::BN - 1) / S::BN;
     const long long grid = group_grid(G, M, S::BM, tn);
     if (grid > 0x7fffffffLL)
         return hipErrorInvalidValue;
     return launch_kernel(k_f8_tile<S, true>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p, gr,
-                         0, (int)tn);
+                         TileOrder{(int)tn, 0, 0, 0, 0});
 }
 
 }  // namespace q4k
