@@ -9,7 +9,6 @@
 #include "device_common.h"
 #include "groups.h"
 #include "launch.h"
-#include <stdlib.h>
 
 namespace q4k {
 
@@ -293,167 +292,195 @@ __device__ __forceinline__ void store4(uint16_t *__restrict__ row, int n, int N,
     }
 }
 
-// Few rows: bound by the weights' bytes. A workgroup takes 16 weight rows and
-// up to 16 R activation rows; its eight wavefronts take the blocks of K in
-// turn, U at a time with all their loads in flight, straight into registers
-// (nothing is shared between wavefronts but the activations, which L1 and L2
-// serve), and add their partial tiles through LDS.
-constexpr int kSkinnyWaves = 8;
+constexpr uint32_t kOutOfRange = 0x80000000u;   // past every resource below (each spans at most 2^31 bytes)
+constexpr int kRawBuffer = 0x00020000;          // resource word 3: raw, 32-bit data format
 
-template <int R, int U>
-__device__ __forceinline__ void skinny_tile(const F8Product &p, const uint8_t *__restrict__ w,
-                                            const float *__restrict__ w_s, int n0,
-                                            const int (&row)[R], const int (&arow)[R], f32x4 *red)
+// vmcnt(vm) lgkmcnt(0).
+constexpr int wait_loads(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x70; }
+
+// Few rows: bound by the weights' bytes. A workgroup takes 16 weight rows and up
+// to 16 RG activation rows; its NW wavefronts each take a contiguous run of the
+// blocks of K and add their partial tiles through LDS at the end. A wavefront
+// stages its own blocks in its own LDS by direct loads, whole 128-byte lines of
+// eight rows a load, in a ring of NST blocks, and so waits for its own loads
+// only (registers would take each row in two half lines, and hold fewer
+// bytes in flight). 16-byte pieces are stored at piece ^ (row % 8): the eight
+// rows of an LDS read lie in different banks. The rows' scales come four blocks
+// at a time, the weights' scales 64 at a time, one a lane.
+template <int RG_, int NW_, int NST_>
+struct RowsShape {
+    static constexpr int RG = RG_, NW = NW_, NST = NST_;
+    static constexpr int kThreads = 64 * NW;
+    static constexpr int kLoads = 2 + 2 * RG;                 // of a block
+    static constexpr int kStage = 128 + RG * 128;             // 16-byte words of a block: weights, activations
+    static_assert(NST >= 2 && (NST - 2) * kLoads < 64 && NST <= 5, "vmcnt counts to 63; scales land a chunk ahead");
+};
+
+template <class S>
+struct RowsLds {
+    union {
+        struct {
+            u32x4 blk[S::NW][S::NST][S::kStage];
+            float s[S::NW][2][S::RG * 64];                    // [row / 16][block % 4][row % 16]
+        };
+        f32x4 red[S::RG][S::NW][64];
+    };
+};
+
+// Weight rows n0 .. n0 + 15 of (w, w_s) times the rows at(0) .. at(16 RG - 1)
+// (activation row and row of y; -1 for none).
+template <class S, class At>
+__device__ __forceinline__ void rows_tile(const F8Product &p, const uint8_t *__restrict__ w,
+                                          const float *__restrict__ w_s, uint32_t a_rows, int n0,
+                                          At at, RowsLds<S> &lds)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, g = lane >> 4;
-    const uint8_t *wp = w + (size_t)min(n0 + li, p.N - 1) * (size_t)p.K + 16 * g;
-    const float *wsp = w_s + (size_t)(n0 >> 7) * (size_t)p.Kb;
-    const uint8_t *ap[R];
-    const float *asp[R];
+    const int wrows = min(16, p.N - n0);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w + (size_t)n0 * (size_t)p.K), (short)0, (int)((uint32_t)wrows * (uint32_t)p.K), kRawBuffer);
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)p.a, (short)0, (int)(a_rows * (uint32_t)p.K), kRawBuffer);
+    const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)p.a_s, (short)0, (int)(a_rows * (uint32_t)p.Kb * 4u), kRawBuffer);
+    const int per = (p.Kb + S::NW - 1) / S::NW;
+    const int b0 = wave * per, b1 = min(b0 + per, p.Kb);
+
+    // Load j: rows 8 j + lane / 8, piece (lane % 8) ^ (row % 8).
+    const int lr = lane >> 3, piece = ((lane ^ lr) & 7) * 16;
+    uint32_t wo[2], ao[2 * S::RG], so[S::RG];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        ap[r] = p.a + (size_t)arow[r] * (size_t)p.K + 16 * g;
-        asp[r] = p.a_s + (size_t)arow[r] * (size_t)p.Kb;
+    for (int j = 0; j < 2; ++j) {
+        const int r = 8 * j + lr;
+        wo[j] = r < wrows ? (uint32_t)r * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
     }
-    f32x4 acc[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int j = 0; j < 2 * S::RG; ++j) {
+        const int x = at(8 * j + lr).x;
+        ao[j] = x >= 0 ? (uint32_t)x * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
+    }
+#pragma unroll
+    for (int r = 0; r < S::RG; ++r) {
+        const int x = at(16 * r + li).x;
+        so[r] = x >= 0 ? ((uint32_t)x * (uint32_t)p.Kb + (uint32_t)g) * 4u : kOutOfRange;
+    }
+    auto issue = [&](int b) __attribute__((always_inline)) {
+        u32x4 *to = lds.blk[wave][(unsigned)(b - b0) % S::NST];
+        // Pieces past K, and blocks past the run, read as zero.
+        const bool in = b < b1 && piece < p.K - b * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            load16_to_lds(wr, to + j * 64, in ? wo[j] : kOutOfRange, b * 128);
+#pragma unroll
+        for (int j = 0; j < 2 * S::RG; ++j)
+            load16_to_lds(ar, to + 128 + j * 64, in ? ao[j] : kOutOfRange, b * 128);
+    };
+    auto issue_scales = [&](int c) __attribute__((always_inline)) {   // blocks b0 + 4 c ..
+        const bool in = b0 + 4 * c + g < b1;
+#pragma unroll
+        for (int r = 0; r < S::RG; ++r)
+            load4_to_lds(sr, lds.s[wave][c & 1] + r * 64, in ? so[r] : kOutOfRange, (b0 + 4 * c) * 4);
+    };
+
+    f32x4 acc[S::RG];
+#pragma unroll
+    for (int r = 0; r < S::RG; ++r)
         acc[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    const int full = p.K >> 7;   // whole blocks
-    auto run = [&](int kb, int n) __attribute__((always_inline)) {
-        u32x4 wl[U][2], al[U][R][2];
-        float ws[U], as[U][R];
+    const int o0 = li * 8 + (g ^ (li & 7)), o1 = li * 8 + ((4 + g) ^ (li & 7));
+    if (b0 < b1) {
+        float ws64 = w_s[min(b0 + lane, p.Kb - 1)];
+        issue_scales(0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = min(kb + u * kSkinnyWaves, full - 1);
-            wl[u][0] = *reinterpret_cast<const u32x4 *>(wp + (size_t)k * 128);
-            wl[u][1] = *reinterpret_cast<const u32x4 *>(wp + (size_t)k * 128 + 64);
-        }
+        for (int d = 0; d < S::NST - 1; ++d)
+            issue(b0 + d);
+        for (int b = b0; b < b1; ++b) {
+            const int i = b - b0;
+            if ((i & 63) == 0 && i > 0)
+                ws64 = w_s[min(b + lane, p.Kb - 1)];
+            const float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws64), i & 63));
+            // This block (and its scales, which are older) has landed, and the
+            // block before it is in registers: its place takes block b + NST - 1.
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(wait_loads((S::NST - 2) * S::kLoads));
+            asm volatile("" ::: "memory");
+            if ((i & 3) == 0)
+                issue_scales((i >> 2) + 1);
+            issue(b + S::NST - 1);
+            asm volatile("" ::: "memory");
+            const u32x4 *from = lds.blk[wave][(unsigned)i % S::NST];
+            const float *sp = lds.s[wave][(i >> 2) & 1] + (i & 3) * 16 + li;
+            const i32x8 wf = join(from[o0], from[o1]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = min(kb + u * kSkinnyWaves, full - 1);
-            ws[u] = u < n ? wsp[k] : 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                al[u][r][0] = *reinterpret_cast<const u32x4 *>(ap[r] + (size_t)k * 128);
-                al[u][r][1] = *reinterpret_cast<const u32x4 *>(ap[r] + (size_t)k * 128 + 64);
-                as[u][r] = asp[r][k];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u >= n)
-                break;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const f32x4 c = mfma_block(join(wl[u][0], wl[u][1]), join(al[u][r][0], al[u][r][1]));
-                const float s = as[u][r] * ws[u];
+            for (int r = 0; r < S::RG; ++r) {
+                const i32x8 af = join(from[128 + r * 128 + o0], from[128 + r * 128 + o1]);
+                const f32x4 c = mfma_block(wf, af);
+                const float s = sp[r * 64] * ws;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     acc[r][q] = fmaf(s, c[q], acc[r][q]);
             }
         }
-    };
-    int kb = wave;
-    for (; kb + (U - 1) * kSkinnyWaves < full; kb += U * kSkinnyWaves)
-        run(kb, U);
-    if (kb < full)
-        run(kb, (full - kb + kSkinnyWaves - 1) / kSkinnyWaves);
-    if (full < p.Kb && wave == full % kSkinnyWaves) {
-        // The short last block: pieces past K are zero in both operands.
-        const int k0 = full * 128;
-        const bool in0 = k0 + 16 * g < p.K, in1 = k0 + 64 + 16 * g < p.K;
-        const u32x4 w0 = in0 ? *reinterpret_cast<const u32x4 *>(wp + k0) : zero;
-        const u32x4 w1 = in1 ? *reinterpret_cast<const u32x4 *>(wp + k0 + 64) : zero;
-        const float ws = wsp[full];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const u32x4 a0 = in0 ? *reinterpret_cast<const u32x4 *>(ap[r] + k0) : zero;
-            const u32x4 a1 = in1 ? *reinterpret_cast<const u32x4 *>(ap[r] + k0 + 64) : zero;
-            const f32x4 c = mfma_block(join(w0, w1), join(a0, a1));
-            const float s = asp[r][full] * ws;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                acc[r][q] = fmaf(s, c[q], acc[r][q]);
-        }
     }
-    // Partial tiles, [r][wave][lane]; wavefront r mod 8 adds tile r's eight in
-    // wavefront order.
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        red[(r * kSkinnyWaves + wave) * 64 + lane] = acc[r];
+    // Partial tiles; wavefront r mod NW adds tile r's in wavefront order.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_loads(0));
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (r % kSkinnyWaves != wave || row[r] < 0)
+    for (int r = 0; r < S::RG; ++r)
+        lds.red[r][wave][lane] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < S::RG; ++r) {
+        const int to = at(16 * r + li).y;
+        if (r % S::NW != wave || to < 0)
             continue;
-        f32x4 v = red[r * kSkinnyWaves * 64 + lane];
+        f32x4 v = lds.red[r][0][lane];
 #pragma unroll
-        for (int s = 1; s < kSkinnyWaves; ++s)
-            v += red[(r * kSkinnyWaves + s) * 64 + lane];
-        store4(p.y + (size_t)row[r] * (size_t)p.N, n0 + 4 * g, p.N, v);
+        for (int s = 1; s < S::NW; ++s)
+            v += lds.red[r][s][lane];
+        store4(p.y + (size_t)to * (size_t)p.N, n0 + 4 * g, p.N, v);
     }
 }
 
-template <int R>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void k_f8_skinny(F8Product p)
+template <class S>
+__global__ __launch_bounds__(S::kThreads) void k_f8_rows(F8Product p)
 {
-    __shared__ f32x4 red[R * kSkinnyWaves * 64];
-    const int li = threadIdx.x & 15, m0 = blockIdx.y * (16 * R);
-    int row[R], arow[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int m = m0 + 16 * r + li;
-        row[r] = m < p.M ? m : -1;
-        arow[r] = min(m, p.M - 1);
-    }
-    constexpr int U = R == 1 ? 4 : R == 2 ? 4 : R == 4 ? 2 : 1;
-    skinny_tile<R, U>(p, p.w, p.w_s, blockIdx.x * 16, row, arow, red);
+    __shared__ RowsLds<S> lds;
+    auto at = [&](int r) __attribute__((always_inline)) {
+        const int m = r < p.M ? r : -1;
+        return int2{m, m};
+    };
+    rows_tile<S>(p, p.w, p.w_s + (size_t)(blockIdx.x >> 3) * (size_t)p.Kb, (uint32_t)p.M, blockIdx.x * 16, at, lds);
 }
 
-// The same over groups: workgroup (x, e) takes 16 weight rows of group e
-// through the group's rows, 16 R at a time.
-template <int R>
-__device__ __forceinline__ void skinny_rows(const F8Product &p, const Groups &gr,
-                                            const uint8_t *w, const float *w_s, int lo, int hi,
-                                            f32x4 *red)
+// The same over groups: workgroup (x, e) takes 16 weight rows of group e past
+// the group's rows, 16 RG at a time.
+template <class S>
+__global__ __launch_bounds__(S::kThreads) void k_f8_rows_grouped(F8Product p, Groups gr)
 {
-    const int li = threadIdx.x & 15;
-    int row[R], arow[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int at = lo + 16 * r + li;
-        row[r] = at < hi ? group_row(gr, at) : -1;
-        arow[r] = max(row[r], 0) / gr.share;
-    }
-    constexpr int U = R == 1 ? 4 : 2;
-    skinny_tile<R, U>(p, w, w_s, blockIdx.x * 16, row, arow, red);
-}
-
-__global__ __launch_bounds__(64 * kSkinnyWaves) void k_f8_skinny_grouped(F8Product p, Groups gr)
-{
-    __shared__ f32x4 red[4 * kSkinnyWaves * 64];
+    __shared__ RowsLds<S> lds;
     const int e = blockIdx.y;
     int lo, hi;
     group_bounds(gr, e, lo, hi);
     const uint8_t *w = p.w + (size_t)e * (size_t)p.N * (size_t)p.K;
-    const float *w_s = p.w_s + (size_t)e * (size_t)p.Nb * (size_t)p.Kb;
-    while (lo < hi) {
-        if (hi - lo <= 16) {
-            skinny_rows<1>(p, gr, w, w_s, lo, hi, red);
-            return;
-        }
-        if (hi - lo <= 32) {
-            skinny_rows<2>(p, gr, w, w_s, lo, hi, red);
-            return;
-        }
-        skinny_rows<4>(p, gr, w, w_s, lo, hi, red);
-        lo += 64;
-        __syncthreads();   // red is read before the next rows write it
+    const float *w_s = p.w_s + ((size_t)e * (size_t)p.Nb + (size_t)(blockIdx.x >> 3)) * (size_t)p.Kb;
+    const uint32_t a_rows = (uint32_t)((gr.M - 1) / gr.share + 1);
+    for (; lo < hi; lo += 16 * S::RG) {
+        auto at = [&](int r) __attribute__((always_inline)) {
+            const int y = lo + r < hi ? group_row(gr, lo + r) : -1;
+            return int2{y < 0 ? -1 : y / gr.share, y};
+        };
+        rows_tile<S>(p, w, w_s, a_rows, blockIdx.x * 16, at, lds);
+        __syncthreads();   // the partial tiles are read before the next rows' loads
     }
 }
+
+using Rows1 = RowsShape<1, 8, 4>;
+using Rows2 = RowsShape<2, 8, 3>;
+using Rows3 = RowsShape<3, 4, 4>;
+using Rows4 = RowsShape<4, 4, 3>;
+using Rows8 = RowsShape<8, 4, 2>;
 
 // Many rows: bound by the matrix instructions. A workgroup of eight wavefronts
 // computes BN x BM of y^T, WN x WM wavefronts of TN x TM tiles each. Per step
@@ -481,7 +508,7 @@ struct TileShape {
     // the end of the step, then of the next step's first kSpread (which end
     // before its turn; with two stages the loads must land by then, so they
     // stop earlier). kTailLoads of the loads fall before the step's end.
-    static constexpr int kSpread = NS == 2 ? 2 * TN : kTurn, kSlots = TN + kSpread;
+    static constexpr int kSpread = NS == 2 ? TN : kTurn, kSlots = TN + kSpread;
     static constexpr int kTailLoads = TN * kLoads / kSlots;
     static constexpr int kRowBytes = BN * 2 + 16;          // of a row of y in LDS
     static_assert(BN * 8 % kThreads == 0 && BM * 8 % kThreads == 0 && BM % 64 == 0 && BM <= kThreads, "whole loads");
@@ -503,16 +530,13 @@ struct TileLds {
     int row[S::BM];
 };
 
-constexpr uint32_t kOutOfRange = 0x80000000u;   // past every resource below (each spans at most 2^31 bytes)
-constexpr int kRawBuffer = 0x00020000;          // resource word 3: raw, 32-bit data format
-
 // Wait until at most VM of the wavefront's loads are in flight and its LDS
 // operations are done, then meet the others.
 template <int VM>
 __device__ __forceinline__ void wait_and_meet()
 {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
+    __builtin_amdgcn_s_waitcnt(wait_loads(VM));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -676,15 +700,30 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     // them from every wavefront at once stalls the issue of all. No step begins by waiting for LDS. Tile t's FMAs follow
     // matrix instruction t + kLag, when its result is ready. The group barriers
     // keep that order; the empty asm keeps the FMAs where they are written.
-    constexpr int kLag = 2;
+    // The last kLag tiles' FMAs of a step run in the next one (kCarry), which
+    // then begins with matrix instructions; not in the large form, whose
+    // registers are all taken, and where they are a sixteenth of the tiles.
+    constexpr int kLag = 2, kRing = 4;
+    constexpr bool kCarry = S::kTiles < 32;
+    static_assert(S::kTiles % kRing == 0 && S::TN >= kLag, "results of two steps do not meet");
     i32x8 wf[S::TN], af[2];
-    float as[S::TM];
+    f32x4 c[kRing];
+    float as[S::TM], sc[S::TM], sc_last = 0.0f;
     int ws_next;
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+        c[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    auto add_tile = [&](auto u_c, float s) __attribute__((always_inline)) {
+        constexpr int u = decltype(u_c)::value, i = u % S::TN, j = u / S::TN;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            acc[i][j][q] = fmaf(s, c[u % kRing][q], acc[i][j][q]);
+        asm volatile("" : "+v"(acc[i][j]));
+    };
     auto run_step = [&](auto st_c, int step) __attribute__((always_inline)) {
         constexpr int P = decltype(st_c)::value, Q = (P + 1) % S::NS;
-        float sc[S::TM];
-        f32x4 c[kLag + 1];
         const float ws = __int_as_float(ws_next);
+        sc_last = sc[S::TM - 1];
 #pragma unroll
         for (int j = 0; j < S::TM; ++j)
             sc[j] = as[j] * ws;
@@ -694,7 +733,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         if ((step & 7) == 0)
             issue_scales((step >> 3) + 1);
         __builtin_amdgcn_sched_barrier(0);
-        unroll<S::kTiles + kLag>([&](auto t_c) __attribute__((always_inline)) {
+        unroll<S::kTiles + (kCarry ? 0 : kLag)>([&](auto t_c) __attribute__((always_inline)) {
             constexpr int t = decltype(t_c)::value, i = t % S::TN, j = t / S::TN;
             if constexpr (t == S::kTurn) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -704,7 +743,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
                 __builtin_amdgcn_sched_barrier(0);
             }
             if constexpr (t < S::kTiles) {
-                c[t % (kLag + 1)] = mfma_block(wf[i], af[j & 1]);
+                c[t % kRing] = mfma_block(wf[i], af[j & 1]);
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 if constexpr (i == 0 && j + 1 < S::TM) {
                     af[(j + 1) & 1] = a_operand(P, j + 1);
@@ -735,12 +774,11 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
                     __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
                 });
             }
-            if constexpr (t >= kLag) {
-                constexpr int u = t - kLag, ui = u % S::TN, uj = u / S::TN;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[ui][uj][q] = fmaf(sc[uj], c[u % (kLag + 1)][q], acc[ui][uj][q]);
-                asm volatile("" : "+v"(acc[ui][uj]));
+            if constexpr (t >= kLag || kCarry) {
+                if constexpr (t >= kLag)
+                    add_tile(std::integral_constant<int, t - kLag>{}, sc[(t - kLag) / S::TN]);
+                else
+                    add_tile(std::integral_constant<int, S::kTiles - kLag + t>{}, sc_last);
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
             }
         });
@@ -762,10 +800,17 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         wf[i] = w_operand(0, i);
     af[0] = a_operand(0, 0);
     read_scales(0, as);
+#pragma unroll
+    for (int x = 0; x < S::TM; ++x)
+        sc[x] = 0.0f;
     for (int step = 0; step < steps; step += S::NS)
         unroll<S::NS>([&](auto s) __attribute__((always_inline)) {
             if (step + s.value < steps)
                 run_step(s, step + s.value);
+        });
+    if constexpr (kCarry)
+        unroll<kLag>([&](auto t) __attribute__((always_inline)) {
+            add_tile(std::integral_constant<int, S::kTiles - kLag + t.value>{}, sc[S::TM - 1]);
         });
     wait_and_meet<0>();   // no load is on its way into the LDS that the epilogue uses
 
@@ -834,37 +879,56 @@ static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
                          Groups{nullptr, nullptr, 0, 0, 1}, o);
 }
 
-template <int R>
-static hipError_t launch_skinny(const F8Product &p, hipStream_t st)
+template <class S>
+static hipError_t launch_rows(const F8Product &p, hipStream_t st)
 {
-    return launch_kernel(k_f8_skinny<R>, dim3((unsigned)(((long long)p.N + 15) / 16), (unsigned)((p.M + 16 * R - 1) / (16 * R))),
-                         dim3(64 * kSkinnyWaves), 0, st, p);
+    static_assert(sizeof(RowsLds<S>) <= 160 * 1024, "the rings fit in LDS");
+    return launch_kernel(k_f8_rows<S>, dim3((unsigned)(((long long)p.N + 15) / 16)), dim3(S::kThreads), 0, st, p);
 }
 
-static int f8_form(int M, int N)
+template <class S>
+static hipError_t launch_rows_grouped(const F8Product &p, const Groups &gr, hipStream_t st)
 {
-    if (const char *e = getenv("F8FORM"))
-        return atoi(e);
-    const long long large = (((long long)M + 255) / 256) * (((long long)N + 255) / 256);
-    return large >= 256 ? 2 : 0;
+    return launch_kernel(k_f8_rows_grouped<S>, dim3((unsigned)(((long long)p.N + 15) / 16), (unsigned)gr.G),
+                         dim3(S::kThreads), 0, st, p, gr);
 }
+
+// Which kernel: the one whose rounds of 256 workgroups cost least. Times of a
+// round per block of K, in 10 ns on MI355X: a row form by its row groups, with
+// the weights streaming (M = 1, 32, 40, 64 and 128 at 4096 x 4096 and 4096 x
+// 14336), a tile with the chip full. At 4096 columns 128 rows take 12.7 us by
+// rows and 16.2 us by tiles; at 14336 columns 43 and 18 us.
+static int rows_cost(int rg) { return rg == 1 ? 11 : rg == 2 ? 12 : rg == 3 ? 14 : rg == 4 ? 19 : 30; }
+constexpr int kSmallCost = 52;
+
+// Row groups for M rows, 0 past 128.
+static int row_groups(long long M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : M <= 64 ? 4 : M <= 128 ? 8 : 0; }
+
+static long long rounds(long long workgroups) { return (workgroups + 255) / 256; }
 
 hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
                           uint16_t *y, int M, int N, int K, hipStream_t st)
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
-    if (M <= 16)
-        return launch_skinny<1>(p, st);
-    if (M <= 32)
-        return launch_skinny<2>(p, st);
-    if (M <= 64)
-        return launch_skinny<4>(p, st);
-    const int form = f8_form(M, N);
-    if (form == 2)
+    const long long tn = ((long long)N + 127) / 128, tm = ((long long)M + 127) / 128;
+    const int rg = row_groups(M);
+    if (rg && rounds(tn * 8) * rows_cost(rg) <= rounds(tn) * kSmallCost) {
+        switch (rg) {
+        case 1: return launch_rows<Rows1>(p, st);
+        case 2: return launch_rows<Rows2>(p, st);
+        case 3: return launch_rows<Rows3>(p, st);
+        case 4: return launch_rows<Rows4>(p, st);
+        default: return launch_rows<Rows8>(p, st);
+        }
+    }
+    // With the chip full a step of the large tiles takes 1.9 us, of the wide
+    // ones 1.1 us and of the small ones 0.7 us (2048 x 14336 x 4096: 129, 149
+    // and 163 us; 1001 x 4096 x 4096: 46, 28 and 21 us).
+    const long long tn2 = (tn + 1) / 2, tm2 = (tm + 1) / 2;
+    const long long large = rounds(tm2 * tn2) * 19, wide = rounds(tm * tn2) * 11, small = rounds(tm * tn) * 7;
+    if (large <= wide && large <= small)
         return launch_tiles<TileLarge>(p, st);
-    if (form == 1)
-        return launch_tiles<TileWide>(p, st);
-    return launch_tiles<TileSmall>(p, st);
+    return wide <= small ? launch_tiles<TileWide>(p, st) : launch_tiles<TileSmall>(p, st);
 }
 
 hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
@@ -873,9 +937,18 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
     const Groups gr = {offsets, order, G, M, share};
-    if ((long long)M <= 32LL * G)
-        return launch_kernel(k_f8_skinny_grouped, dim3((unsigned)(((long long)N + 15) / 16), (unsigned)G),
-                             dim3(64 * kSkinnyWaves), 0, st, p, gr);
+    // As above, for groups of the mean size; groups that are longer take the row
+    // form's passes several times, and shorter ones a part of a tile.
+    const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit, cols = ((long long)N + 127) / 128;
+    const int rg = mean <= 8 ? 1 : mean <= 16 ? 2 : mean <= 32 ? 4 : mean <= 64 ? 8 : 0;
+    if (rg && rounds(hit * cols * 8) * rows_cost(rg) <= rounds(hit * cols) * kSmallCost) {
+        switch (rg) {
+        case 1: return launch_rows_grouped<Rows1>(p, gr, st);
+        case 2: return launch_rows_grouped<Rows2>(p, gr, st);
+        case 4: return launch_rows_grouped<Rows4>(p, gr, st);
+        default: return launch_rows_grouped<Rows8>(p, gr, st);
+        }
+    }
     using S = TileSmall;
     const long long tn = ((long long)N + S::BN - 1) / S::BN;
     const long long grid = group_grid(G, M, S::BM, tn);
