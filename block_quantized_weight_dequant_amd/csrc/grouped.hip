@@ -14,6 +14,7 @@
 #include "device_common.h"
 #include "formats.h"
 #include "gemm_split.h"
+#include "gemv_stream.h"
 #include "groups.h"
 #include "launch.h"
 #include "validate.h"
@@ -269,6 +270,48 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     }
 }
 
+// One to kGemvSlots rows in all: each is a decode GEMV of one activation row
+// (gemv_stream.h) with its group's weights, in one launch and no preparation.
+// Workgroup (x, p) takes 16 weight rows for position p; rows of one group read
+// its weights once each, which costs more only where such rows are many.
+constexpr int kGemvSlots = 8;
+
+template <class F, bool BF, int CH, bool LA>
+__global__ __launch_bounds__(64 * kGemvStreamWaves) void k_grouped_gemv(const void *__restrict__ a,
+                                                                      const uint8_t *__restrict__ w,
+                                                                      float *__restrict__ y, int N,
+                                                                      int K, Groups gr)
+{
+    const int p = blockIdx.y;
+    int e = -1;
+    for (int base = 0; base < gr.G && e < 0; base += 64) {
+        int lo = 0, hi = 0;
+        if (base + (int)(threadIdx.x & 63) < gr.G)
+            group_bounds(gr, base + (int)(threadIdx.x & 63), lo, hi);
+        const uint64_t in = __ballot(lo <= p && p < hi);
+        if (in)
+            e = base + __builtin_ctzll(in);
+    }
+    const int row = __builtin_amdgcn_readfirstlane(group_row(gr, p));
+    if (e < 0 || row < 0)
+        return;
+    const int nblk = K >> 5;
+    gemv_stream_body<F, 1, kGemvStreamWaves, CH, BF, 1, 16, LA, false, LA>(
+        static_cast<const uint8_t *>(a) + (size_t)(row / gr.share) * (size_t)K * (BF ? 2 : 4),
+        w + (size_t)e * (size_t)N * ((size_t)nblk * F::kBytes), y + (size_t)row * (size_t)N, N, K,
+        nblk, 0);
+}
+
+template <class F, bool BF, bool LA>
+static hipError_t launch_grouped_gemv(const void *a, const uint8_t *w, float *y, int N, int K,
+                                      const Groups &gr, hipStream_t s)
+{
+    return launch_kernel(q4v::gemv_chunk_blocks(K / 32, K / 32) == 16 ? k_grouped_gemv<F, BF, 16, LA>
+                                                                     : k_grouped_gemv<F, BF, 8, LA>,
+                         dim3((unsigned)((N + 15LL) / 16), (unsigned)gr.M), dim3(64 * kGemvStreamWaves),
+                         0, s, a, w, y, N, K, gr);
+}
+
 template <class F, bool BF, int CT, int R>
 static hipError_t launch_few(const u32x4 *ops, const int *row_exp, const uint8_t *w, float *y,
                              int N, int K, const Groups &gr, hipStream_t s)
@@ -282,6 +325,9 @@ template <class F, bool BF>
 static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, int N, int K,
                                    const Groups &gr, void *workspace, hipStream_t s)
 {
+    if (gr.M <= kGemvSlots && q4v::gemv_streams(1, N, K, F::kBytes, BF ? 2 : 4))
+        return gemv_rows_line_aligned<F>(w, K) ? launch_grouped_gemv<F, BF, true>(a, w, y, N, K, gr, s)
+                                               : launch_grouped_gemv<F, BF, false>(a, w, y, N, K, gr, s);
     const bool few = q4v::grouped_few(gr.G, gr.M, K);
     const int bm = few ? 16 : 128, nblk = K >> 5;
     const long long tiles = q4v::group_row_tiles(gr.G, gr.M, bm);
