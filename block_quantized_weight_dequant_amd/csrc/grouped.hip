@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
 
 // ---------------------------------------------------------------------------
 // Few rows a group: bound by the bytes of the weights. Workgroup (x, e) takes
-// 16 CT weight rows of group e past the group's rows, 16 R at a time. Its eight
+// 16 CT weight rows of group e past the group's rows, 16 R at a time. Its four
 // wavefronts deal the row's chunks of 8 blocks (256 elements: 144 or 272
 // bytes, whole 16-byte pieces) among themselves; each stages its own chunk's
 // raw bytes in its own LDS by 16-byte direct loads, one chunk ahead, and so
@@ -117,8 +117,16 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
 // is 36 or 68 dwords, 4 mod 32, so the sixteen rows an operand read touches lie
 // in different banks. The activation operands of a chunk go from L2 to
 // registers (they are the wavefront's own: no other reads that chunk), once
-// for all 16 CT weight rows. The partial tiles are added through LDS.
-constexpr int kFewWaves = 8, kFewBlocks = 8;
+// for all 16 CT weight rows. The partial tiles are added through LDS. Four
+// wavefronts, so that two workgroups share a compute unit and one streams while
+// the other decodes or adds up (37 tokens, 2 of 8 experts, 14336 x 4096: Q8_0
+// 154 -> 128 us, Q4_0 with f32 activations 118 -> 106, 100 tokens of bfloat16
+// 134 -> 124). Also measured, and no faster (90-100 us of Q4_0, bfloat16):
+// persistent workgroups with the loads running on into the next tile, three
+// stages, loads spread between the blocks' decodes. The decode (14 vector
+// instructions a matrix instruction) and the streaming each take about 60 us
+// alone, and 3 TB/s is what the decode GEMV of 8 rows reaches on this shape.
+constexpr int kFewWaves = 4, kFewBlocks = 8;
 
 template <class F, int CT>
 struct FewGeom {
