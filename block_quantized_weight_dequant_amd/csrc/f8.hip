@@ -64,9 +64,26 @@ struct Eight {
     __device__ __forceinline__ u32x2 codes(float s) const
     {
         float q[8];
+        if (s >= 0x1p-90f && s <= 0x1p90f) {
+            // The correctly rounded quotient from the correctly rounded
+            // reciprocal: each step takes the exact remainder (an FMA), the
+            // first to within a unit in the last place, the second to the
+            // nearest (Markstein's theorem). No intermediate leaves the normal
+            // range here but where the quotient is far below the smallest
+            // code, and no quotient rounds past 448. Five operations an
+            // element; a division takes about twice that.
+            const float r = 1.0f / s;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[i] = s == 0.0f ? 0.0f : fminf(fmaxf(v[i] / s, -kE4M3Max), kE4M3Max);
+            for (int i = 0; i < 8; ++i) {
+                const float q0 = v[i] * r;
+                const float q1 = fmaf(fmaf(-q0, s, v[i]), r, q0);
+                q[i] = fmaf(fmaf(-q1, s, v[i]), r, q1);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = s == 0.0f ? 0.0f : fminf(fmaxf(v[i] / s, -kE4M3Max), kE4M3Max);
+        }
         u32x2 r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -87,40 +104,29 @@ __device__ __forceinline__ float max16(float v)
     return v;
 }
 
-// One scale per 128 columns of a row. 16 R blocks per 256-thread workgroup.
-template <class T, int R>
+// One scale per 128 columns of a row: 16 blocks per 256-thread workgroup, one a
+// thread group (2048 x 4096 bfloat16: 6.4 us, 3.9 TB/s; two or four blocks in
+// flight a group, with half and a quarter of the workgroups, take 6.6 and 7.3).
+template <class T>
 __global__ __launch_bounds__(256) void k_f8_quantize_rows(const T *__restrict__ x,
                                                          uint8_t *__restrict__ q,
                                                          float *__restrict__ s, int K, unsigned Kb,
                                                          unsigned n_blocks)
 {
-    const unsigned tid = threadIdx.x, p = tid & 15;
-    const unsigned b0 = blockIdx.x * (16u * R) + (tid >> 4);
-    Eight<T> v[R];
-    size_t at[R];
-    bool in[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        // Unconditional loads, from a valid place where the lane has none: a
-        // load under a branch would be waited for before the next one.
-        const unsigned b = min(b0 + 16 * r, n_blocks - 1);
-        const unsigned row = b / Kb, col = (b - row * Kb) * 128 + 8 * p;
-        in[r] = col < (unsigned)K;
-        at[r] = (size_t)row * (size_t)K + (in[r] ? col : 0u);
-        v[r].load(x + at[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        v[r].clear_if(!in[r]);
-        const float sc = max16(v[r].amax()) / kE4M3Max;
-        const unsigned b = b0 + 16 * r;
-        if (b < n_blocks) {
-            if (in[r])
-                *reinterpret_cast<u32x2 *>(q + at[r]) = v[r].codes(sc);
-            if (p == 0)
-                s[b] = sc;
-        }
-    }
+    const unsigned p = threadIdx.x & 15, b = blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (b >= n_blocks)   // whole groups of 16 lanes
+        return;
+    const unsigned row = b / Kb, col = (b - row * Kb) * 128 + 8 * p;
+    const bool in = col < (unsigned)K;
+    const size_t at = (size_t)row * (size_t)K + (in ? col : 0u);
+    Eight<T> v;
+    v.load(x + at);
+    v.clear_if(!in);
+    const float sc = max16(v.amax()) / kE4M3Max;
+    if (in)
+        *reinterpret_cast<u32x2 *>(q + at) = v.codes(sc);
+    if (p == 0)
+        s[b] = sc;
 }
 
 // One scale per 128 x 128 tile: a workgroup holds the tile in registers
@@ -174,13 +180,8 @@ static hipError_t launch_quantize_t(const T *x, uint8_t *q, float *s, int M, int
     const unsigned Kb = (unsigned)(K + 127) / 128;
     if (block_rows == 1) {
         const unsigned nb = (unsigned)M * Kb;   // < 2^31, checked
-        // Four blocks a thread group where that still leaves four workgroups
-        // for each compute unit; otherwise one, for the spread.
-        if (nb >= 64u * 1024u)
-            return launch_kernel(k_f8_quantize_rows<T, 4>, dim3((nb + 63) / 64), dim3(256), 0, st,
-                                 x, q, s, K, Kb, nb);
-        return launch_kernel(k_f8_quantize_rows<T, 1>, dim3((nb + 15) / 16), dim3(256), 0, st, x,
-                             q, s, K, Kb, nb);
+        return launch_kernel(k_f8_quantize_rows<T>, dim3((nb + 15) / 16), dim3(256), 0, st, x, q, s,
+                             K, Kb, nb);
     }
     const unsigned Mb = (unsigned)(((long long)M + 127) / 128);
     return launch_kernel(k_f8_quantize_tiles<T>, dim3(Mb * Kb), dim3(256), 0, st, x, q, s, M, K,
@@ -931,6 +932,17 @@ hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, 
     return wide <= small ? launch_tiles<TileWide>(p, st) : launch_tiles<TileSmall>(p, st);
 }
 
+template <class S>
+static hipError_t launch_grouped_tiles(const F8Product &p, const Groups &gr, hipStream_t st)
+{
+    const long long tn = ((long long)p.N + S::BN - 1) / S::BN;
+    const long long grid = group_grid(gr.G, gr.M, S::BM, tn);
+    if (grid > 0x7fffffffLL)
+        return hipErrorInvalidValue;
+    return launch_kernel(k_f8_tile<S, true>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p, gr,
+                         TileOrder{(int)tn, 0, 0, 0, 0});
+}
+
 hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,
                                   const float *w_s, const int *offsets, const int *order, int share,
                                   uint16_t *y, int G, int M, int N, int K, hipStream_t st)
@@ -949,13 +961,11 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
         default: return launch_rows_grouped<Rows8>(p, gr, st);
         }
     }
-    using S = TileSmall;
-    const long long tn = ((long long)N + S::BN - 1) / S::BN;
-    const long long grid = group_grid(G, M, S::BM, tn);
-    if (grid > 0x7fffffffLL)
-        return hipErrorInvalidValue;
-    return launch_kernel(k_f8_tile<S, true>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p, gr,
-                         TileOrder{(int)tn, 0, 0, 0, 0});
+    // Wide tiles where they fill the chip (1024 tokens, 4 of 32 experts, 4096 x
+    // 1792: 84 us, small ones 94); else the small ones, twice as many.
+    if (hit * ((cols + 1) / 2) >= 256)
+        return launch_grouped_tiles<TileWide>(p, gr, st);
+    return launch_grouped_tiles<TileSmall>(p, gr, st);
 }
 
 }  // namespace q4k

@@ -48,68 +48,75 @@ __device__ __forceinline__ float key_logit(uint32_t k)
     return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// One token by one wavefront: lane l holds experts l, l + 64, ... Lane j < top_k
-// ends with choice j.
-template <int V>
-__device__ __forceinline__ void route_token(const float *__restrict__ x, int E, int top_k, int renorm,
-                                            int *__restrict__ ids, float *__restrict__ weights,
-                                            uint16_t *s_ids)
+// Tokens t and t + kRouteWaves by one wavefront, side by side (their steps are
+// chains of short latencies): lane l holds experts l, l + 64, ... of each. Lane
+// j < top_k ends with choice j. s_ids(i) takes token i's choices.
+template <int V, class Ids>
+__device__ __forceinline__ void route_tokens(const float *__restrict__ logits, int E, int top_k,
+                                             int renorm, int *__restrict__ ids,
+                                             float *__restrict__ weights, const int (&tok)[2],
+                                             int n, Ids s_ids)
 {
     const int lane = threadIdx.x & 63;
-    uint32_t key[V];
+    uint32_t key[2][V], first[2][V], my_key[2] = {0, 0}, top[2] = {0, 0};
+    int my_id[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = e < E ? logit_key(x[e]) : 0u;
-    }
-    uint32_t first[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        first[i] = key[i];
-    uint32_t my_key = 0, top = 0;
-    int my_id = 0;
-    for (int j = 0; j < top_k; ++j) {
-        uint32_t m = key[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i)
-            m = max(m, key[i]);
-        const uint32_t best = wave_max_u32(m);
-        // The lowest expert with the best key: the first i in which any lane
-        // has it, and there the lowest lane.
-        int id = -1;
+    for (int u = 0; u < 2; ++u) {
+        const float *x = logits + (size_t)tok[u] * (size_t)E;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint64_t has = __ballot(key[i] == best);
-            if (id < 0 && has) {
-                const int l = __builtin_ctzll(has);
-                id = 64 * i + l;
-                key[i] = lane == l ? 0u : key[i];
-            }
+            const int e = lane + 64 * i;
+            const float v = x[min(e, E - 1)];
+            key[u][i] = first[u][i] = e < E ? logit_key(v) : 0u;
         }
-        if (j == 0)
-            top = best;
-        if (lane == j)
-            my_key = best, my_id = id;
     }
-    // exp(l - max) is in [0, 1]; a row of -inf (every expert masked) weighs 0.
-    const float mx = key_logit(top);
-    const bool none = mx == -__builtin_inff();
-    const float w = lane < top_k && !none ? expf(key_logit(my_key) - mx) : 0.0f;
-    float total;
-    if (renorm) {
-        total = wave_sum(w);
-    } else {
-        float s = 0.0f;
+    for (int j = 0; j < top_k; ++j) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (first[i] != 0u && !none)
-                s += expf(key_logit(first[i]) - mx);
-        total = wave_sum(s);
+        for (int u = 0; u < 2; ++u) {
+            uint32_t m = key[u][0];
+#pragma unroll
+            for (int i = 1; i < V; ++i)
+                m = max(m, key[u][i]);
+            const uint32_t best = wave_max_u32(m);
+            // The lowest expert with the best key: the first i in which any lane
+            // has it, and there the lowest lane.
+            int id = -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint64_t has = __ballot(key[u][i] == best);
+                if (id < 0 && has) {
+                    const int l = __builtin_ctzll(has);
+                    id = 64 * i + l;
+                    key[u][i] = lane == l ? 0u : key[u][i];
+                }
+            }
+            if (j == 0)
+                top[u] = best;
+            if (lane == j)
+                my_key[u] = best, my_id[u] = id;
+        }
     }
-    if (lane < top_k) {
-        ids[lane] = my_id;
-        weights[lane] = none ? 0.0f : w / total;
-        s_ids[lane] = (uint16_t)my_id;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        // exp(l - max) is in [0, 1]; a row of -inf (every expert masked) weighs 0.
+        const float mx = key_logit(top[u]);
+        const bool none = mx == -__builtin_inff();
+        const float w = lane < top_k && !none ? expf(key_logit(my_key[u]) - mx) : 0.0f;
+        float s = w;
+        if (!renorm) {
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (first[u][i] != 0u && !none)
+                    s += expf(key_logit(first[u][i]) - mx);
+        }
+        const float total = wave_sum(s);
+        if (u < n && lane < top_k) {
+            const size_t at = (size_t)tok[u] * (size_t)top_k + lane;
+            ids[at] = my_id[u];
+            weights[at] = none ? 0.0f : w / total;
+            s_ids(u)[lane] = (uint16_t)my_id[u];
+        }
     }
 }
 
@@ -149,8 +156,9 @@ __device__ __forceinline__ void place(RouteLds &l, Fn expert, int s0, int n, int
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int b = 0; b < n; b += kRouteThreads) {
+        const int used = (min(n - b, kRouteThreads) + 63) / 64;   // wavefronts with slots
         if (tid < E)
-            for (int w = 0; w < kRouteWaves; ++w)
+            for (int w = 0; w < used; ++w)
                 l.waves[w][tid] = 0;
         __syncthreads();
         const int i = b + tid;
@@ -167,7 +175,7 @@ __device__ __forceinline__ void place(RouteLds &l, Fn expert, int s0, int n, int
         __syncthreads();
         if (tid < E) {      // counts -> slots of the batch before each wavefront's
             int before = 0;
-            for (int w = 0; w < kRouteWaves; ++w) {
+            for (int w = 0; w < used; ++w) {
                 const int c = l.waves[w][tid];
                 l.waves[w][tid] = (uint16_t)before;
                 before += c;
@@ -197,21 +205,23 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const float *__restrict
                                                         int top_k, int renorm, int chunk, int bits)
 {
     __shared__ RouteLds l;
-    __shared__ uint16_t s_ids[kOneChunk * kMaxTopK];
+    __shared__ uint16_t s_ids[kOneChunk * kMaxTopK];   // at least two tokens a wavefront
     const int tid = threadIdx.x, wave = tid >> 6;
     if (tid < E)
         l.cursor[tid] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, T);
-    uint16_t *mine = s_ids + wave * (kOneChunk / kRouteWaves) * kMaxTopK;
-    for (int t = t0 + wave, r = 0; t < t1; t += kRouteWaves, ++r) {
+    for (int t = t0 + wave; t < t1; t += 2 * kRouteWaves) {
+        const int tok[2] = {t, min(t + kRouteWaves, t1 - 1)}, n = t + kRouteWaves < t1 ? 2 : 1;
         // One workgroup alone keeps every token's choice, in slot order.
-        uint16_t *to = counts ? mine : s_ids + (t - t0) * top_k;
-        route_token<V>(logits + (size_t)t * E, E, top_k, renorm, ids + (size_t)t * top_k,
-                       weights + (size_t)t * top_k, to);
+        auto to = [&](int u) __attribute__((always_inline)) {
+            return s_ids + (counts ? (wave * 2 + u) * kMaxTopK : (tok[u] - t0) * top_k);
+        };
+        route_tokens<V>(logits, E, top_k, renorm, ids, weights, tok, n, to);
         __builtin_amdgcn_wave_barrier();
-        if ((tid & 63) < top_k)
-            atomicAdd(&l.cursor[to[tid & 63]], 1);
+        for (int u = 0; u < n; ++u)
+            if ((tid & 63) < top_k)
+                atomicAdd(&l.cursor[to(u)[tid & 63]], 1);
     }
     __syncthreads();
     const int count = tid < E ? l.cursor[tid] : 0;
