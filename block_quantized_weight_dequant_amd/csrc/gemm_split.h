@@ -242,19 +242,20 @@ constexpr int ring_in_flight(int par, int da, int lb, int na, int nb)
 // GROUPED: the row tiles are those of the groups, each padded to whole tiles,
 // in the operands and in row_exp; group e multiplies the e-th weight matrix,
 // and row r of y is the one that the group's list names (none for the
-// padding).
-template <class F, bool HO, bool GROUPED>
+// padding). RMH: row subtiles that the hi-only form computes (the tile's rows
+// past 16 RMH, of which a group's last tile can have many, are not there).
+template <class F, bool HO, bool GROUPED, int RMH = 8>
 __device__ __forceinline__ void gemm_split_body(
     const u32x4 *__restrict__ ahl, const uint8_t *__restrict__ w, float *__restrict__ y, int M,
     int N, int nblk_row, int nblk, int tiles_m, int tiles_n, const int *__restrict__ row_exp,
-    int accumulate, const Groups &gr)
+    int accumulate, const Groups &gr, const GroupTile &gt, SplitLds<F, HO> &lds)
 {
     using G = PairGeom<F>;
     // MFMA tiles per wavefront: the hi-only form takes 128 rows x 32 columns
     // (8 x 2), so no two wavefronts of a K group decode the same weight
     // columns; the two-term form keeps 64 x 64 (4 x 4), which leaves room for
     // its lo operands in registers.
-    constexpr int RM = HO ? 8 : 4, CN = HO ? 2 : 4;
+    constexpr int RM = HO ? RMH : 4, CN = HO ? 2 : 4;
     constexpr int SO = slab_ops<HO>();           // A operands per (tile, block)
     // A loads (1 KB each) per pair in eighths of the workgroup (the four
     // loading wavefronts issue twice these).
@@ -264,14 +265,10 @@ __device__ __forceinline__ void gemm_split_body(
     // the first PRO steps' loads precede the first pair.
     constexpr int LB = 2 * DBQ - 1, PRO = DA > LB ? DA : LB;
     static_assert(DA >= 3 && DBQ >= 2, "ring depths");
-    __shared__ SplitLds<F, HO> lds;
 
     int mt, m0, n0;
     [[maybe_unused]] int pos0 = 0, pos1 = 0;   // GROUPED: the tile's positions
     if constexpr (GROUPED) {
-        const GroupTile gt = find_group_tile(gr, xcd_runs(blockIdx.x), kGemmBM, tiles_n);
-        if (gt.e < 0)
-            return;
         mt = gt.before + gt.mt, m0 = mt * kGemmBM, n0 = gt.nt * kGemmBN;
         pos0 = gt.lo + gt.mt * kGemmBM, pos1 = gt.hi;
         w += (size_t)gt.e * (size_t)N * ((size_t)nblk_row * F::kBytes);
@@ -464,7 +461,9 @@ __device__ __forceinline__ void gemm_split_body(
                         acc[ms][np][q] = fmaf(dp, cp[ms][q], acc[ms][np][q]);
                 // Pin these FMAs to this region: IR passes would otherwise sink
                 // them past the scheduling barriers, to the end of the pair.
-                if constexpr (RM == 4)
+                if constexpr (RM == 2)
+                    asm volatile("" : "+v"(acc[0][np]), "+v"(acc[1][np]));
+                else if constexpr (RM == 4)
                     asm volatile("" : "+v"(acc[0][np]), "+v"(acc[1][np]), "+v"(acc[2][np]), "+v"(acc[3][np]));
                 else
                     asm volatile("" : "+v"(acc[0][np]), "+v"(acc[1][np]), "+v"(acc[2][np]), "+v"(acc[3][np]),
@@ -483,7 +482,7 @@ __device__ __forceinline__ void gemm_split_body(
                 // the VALU work.
                 constexpr int NM = RM * (HO ? 1 : 2);
                 constexpr int kDsPerSlot = (kDsReads + NM - 1) / NM;
-                constexpr int kValuPerSlot = HO ? (F::kBytes == kQ4Bytes ? 7 : 6) : 4;
+                constexpr int kValuPerSlot = HO ? (F::kBytes == kQ4Bytes ? 4 + 24 / RM : 4 + 16 / RM) : 4;
                 constexpr int kRegionLoads = (NLK + CN - 1) / CN;   // at most, per region
                 const int nl = (NLK * (ns + 1) + CN - 1) / CN - (NLK * ns + CN - 1) / CN;
 #pragma unroll
@@ -644,8 +643,10 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split(
     int N, int nblk_row, int nblk, int tiles_m, int tiles_n, const int *__restrict__ row_exp,
     int accumulate)
 {
+    __shared__ SplitLds<F, HO> lds;
     gemm_split_body<F, HO, false>(ahl, w, y, M, N, nblk_row, nblk, tiles_m, tiles_n, row_exp,
-                                  accumulate, Groups{nullptr, nullptr, 0, 0, 1});
+                                  accumulate, Groups{nullptr, nullptr, 0, 0, 1},
+                                  GroupTile{0, 0, 0, 0, 0, 0}, lds);
 }
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits) { return __uint_as_float(bits << 16); }

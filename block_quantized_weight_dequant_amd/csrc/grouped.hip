@@ -104,7 +104,24 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
     const u32x4 *__restrict__ ahl, const uint8_t *__restrict__ w, float *__restrict__ y, int N,
     int nblk_row, int nblk, int tiles_n, const int *__restrict__ row_exp, int accumulate, Groups gr)
 {
-    gemm_split_body<F, HO, true>(ahl, w, y, 0, N, nblk_row, nblk, 0, tiles_n, row_exp, accumulate, gr);
+    __shared__ SplitLds<F, HO> lds;
+    const GroupTile gt = find_group_tile(gr, xcd_runs(blockIdx.x), kGemmBM, tiles_n);
+    if (gt.e < 0)
+        return;
+    if constexpr (HO) {
+        // A group's last tile computes a half or a quarter of its rows where it
+        // has no more.
+        const int rows = gt.hi - gt.lo - gt.mt * kGemmBM;
+        if (rows <= 32) {
+            gemm_split_body<F, HO, true, 2>(ahl, w, y, 0, N, nblk_row, nblk, 0, tiles_n, row_exp, accumulate, gr, gt, lds);
+            return;
+        }
+        if (rows <= 64) {
+            gemm_split_body<F, HO, true, 4>(ahl, w, y, 0, N, nblk_row, nblk, 0, tiles_n, row_exp, accumulate, gr, gt, lds);
+            return;
+        }
+    }
+    gemm_split_body<F, HO, true>(ahl, w, y, 0, N, nblk_row, nblk, 0, tiles_n, row_exp, accumulate, gr, gt, lds);
 }
 
 // ---------------------------------------------------------------------------
