@@ -63,11 +63,11 @@ F32_VECTOR_PEAK_TFLOPS = 157.3     # MI355X f32 vector arithmetic
 LLC_BYTES = 256 * 2 ** 20          # MI355X last-level (MALL) cache
 PROFILES = os.path.join(ROOT, "profiles")
 KERNEL_SOURCES = {
-    "gemv": "block_quantized_weight_dequant_amd/csrc/gemv.hip",
-    "gemm": "block_quantized_weight_dequant_amd/csrc/gemm.hip",
-    "dequant": "block_quantized_weight_dequant_amd/csrc/dequant.hip",
-    "quantize": "block_quantized_weight_dequant_amd/csrc/quantize.hip",
-    "probe": "block_quantized_weight_dequant_amd/csrc/probe/stream_read.hip",
+    "gemv": ("gemv.hip", "gemv_stream.h"),
+    "gemm": ("gemm.hip", "gemm_split.h"),
+    "dequant": ("dequant.hip",),
+    "quantize": ("quantize.hip",),
+    "probe": ("probe/stream_read.hip",),
 }
 
 
@@ -103,8 +103,12 @@ def log(msg):
 
 
 def source_sha256(kind):
-    with open(os.path.join(ROOT, KERNEL_SOURCES[kind]), "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    """Of the files that hold the kernels of one kind, in the order listed."""
+    h = hashlib.sha256()
+    for name in KERNEL_SOURCES[kind]:
+        with open(os.path.join(ROOT, "block_quantized_weight_dequant_amd", "csrc", name), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 def kernel_kind(kernel):

@@ -179,9 +179,19 @@ static hipError_t launch_quantize_t(const T *x, uint8_t *q, float *s, int M, int
 {
     const unsigned Kb = (unsigned)(K + 127) / 128;
     if (block_rows == 1) {
-        const unsigned nb = (unsigned)M * Kb;   // < 2^31, checked
-        return launch_kernel(k_f8_quantize_rows<T>, dim3((nb + 15) / 16), dim3(256), 0, st, x, q, s,
-                             K, Kb, nb);
+        // At most 2^23 workgroups a launch (2^31 threads).
+        const int rows = (int)((1u << 27) / Kb);   // K <= 2^31: at least 8
+        for (int r0 = 0; r0 < M; r0 += rows) {
+            const unsigned nb = (unsigned)(M - r0 < rows ? M - r0 : rows) * Kb;
+            const hipError_t e = launch_kernel(k_f8_quantize_rows<T>, dim3((nb + 15) / 16), dim3(256), 0, st,
+                                               x + (size_t)r0 * (size_t)K, q + (size_t)r0 * (size_t)K,
+                                               s + (size_t)r0 * Kb, K, Kb, nb);
+            if (e != hipSuccess)
+                return e;
+            if (rows > M - r0)
+                break;
+        }
+        return hipSuccess;
     }
     const unsigned Mb = (unsigned)(((long long)M + 127) / 128);
     return launch_kernel(k_f8_quantize_tiles<T>, dim3(Mb * Kb), dim3(256), 0, st, x, q, s, M, K,
@@ -877,7 +887,7 @@ static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
     if (best * 8 > 0x7fffffffLL)
         return hipErrorInvalidValue;
     return launch_kernel(k_f8_tile<S, false>, dim3((unsigned)(best * 8)), dim3(S::kThreads), 0, st, p,
-                         Groups{nullptr, nullptr, 0, 0, 1}, o);
+                         Groups{nullptr, nullptr, 0, 0, 1, 0}, o);
 }
 
 template <class S>
@@ -948,7 +958,7 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
                                   uint16_t *y, int G, int M, int N, int K, hipStream_t st)
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
-    const Groups gr = {offsets, order, G, M, share};
+    const Groups gr = {offsets, order, G, M, share, 0};
     // As above, for groups of the mean size; groups that are longer take the row
     // form's passes several times, and shorter ones a part of a tile.
     const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit, cols = ((long long)N + 127) / 128;

@@ -645,7 +645,7 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split(
 {
     __shared__ SplitLds<F, HO> lds;
     gemm_split_body<F, HO, false>(ahl, w, y, M, N, nblk_row, nblk, tiles_m, tiles_n, row_exp,
-                                  accumulate, Groups{nullptr, nullptr, 0, 0, 1},
+                                  accumulate, Groups{nullptr, nullptr, 0, 0, 1, 0},
                                   GroupTile{0, 0, 0, 0, 0, 0}, lds);
 }
 

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
 {
     __shared__ SplitLds<F, HO> lds;
     const GroupTile gt = find_group_tile(gr, xcd_runs(blockIdx.x), kGemmBM, tiles_n);
-    if (gt.e < 0)
+    if (gt.e < 0 || gt.before + gt.mt >= gr.tiles)
         return;
     if constexpr (HO) {
         // A group's last tile computes a half or a quarter of its rows where it
@@ -206,8 +206,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     const f16x8 scale = {sc, sc, sc, sc, sc, sc, sc, sc};
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
 
-    for (; lo < hi; lo += 16 * R, tile += R) {
-        const int subs = min(R, (hi - lo + 15) / 16);
+    // (Right lists end at gr.tiles by themselves.)
+    for (; lo < hi && tile < gr.tiles; lo += 16 * R, tile += R) {
+        const int subs = min(min(R, (hi - lo + 15) / 16), gr.tiles - tile);
         f32x4 acc[R][CT];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int at = lo + 16 * r + 4 * g + q;
-                const int row = at < hi ? group_row(gr, at) : -1;
+                const int row = at < hi && r < subs ? group_row(gr, at) : -1;
                 if (row >= 0 && n < N)
                     y[(size_t)row * (size_t)N + n] = ldexpf(v[q], -row_exp[(size_t)(tile + r) * 16 + 4 * g + q]);
             }
@@ -397,7 +398,8 @@ hipError_t launch_gemm_grouped(WeightFormat fmt, bool bf16, const void *a, const
                                const int *offsets, const int *order, int share, float *y, int G,
                                int M, int N, int K, void *workspace, hipStream_t s)
 {
-    const Groups gr = {offsets, order, G, M, share};
+    const int bm = q4v::grouped_few(G, M, K) ? 16 : 128;
+    const Groups gr = {offsets, order, G, M, share, (int)q4v::group_row_tiles(G, M, bm)};
     if (fmt == WeightFormat::kQ8_0)
         return bf16 ? launch_grouped_f<FmtQ8_0, true>(a, w, y, N, K, gr, workspace, s)
                     : launch_grouped_f<FmtQ8_0, false>(a, w, y, N, K, gr, workspace, s);

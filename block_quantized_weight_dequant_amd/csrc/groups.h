@@ -5,8 +5,10 @@
 //
 // offsets and order are device data that the host never sees, so they are
 // clamped where they are read: a bound outside [previous bound, M] is pulled
-// into it, and a row outside [0, M) is skipped. Wrong contents give wrong
-// rows, never an access outside the arrays.
+// into it, and a row outside [0, M) is skipped. Groups may even overlap (bounds
+// that fall): their tiles are counted without overflow, and those that pass
+// the tiles of a workspace are left out. Wrong contents give wrong rows, never
+// an access outside the arrays.
 #pragma once
 
 #include "device_common.h"
@@ -18,6 +20,7 @@ struct Groups {
     const int *offsets;   // [G + 1]
     const int *order;     // [M], or null
     int G, M, share;
+    int tiles;            // row tiles of the workspace (which holds no others), if there is one
 };
 
 // Rows of group e: positions lo .. hi - 1.
@@ -55,7 +58,9 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
         int lo = 0, hi = 0;
         if (base + lane < gr.G)
             group_bounds(gr, base + lane, lo, hi);
-        const int tiles = (hi - lo + bm - 1) / bm * tiles_n;
+        // A right list has fewer tiles than any grid has workgroups (2^23 of 512
+        // threads); a wrong one is cut there, where the sums cannot overflow.
+        const int tiles = (int)min((long long)((hi - lo + bm - 1) / bm) * tiles_n, 1LL << 23);
         int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -77,23 +82,24 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
             g.before = first / tiles_n;
             return g;
         }
-        run += __builtin_amdgcn_readlane(sum, 63);
+        run = min(run + __builtin_amdgcn_readlane(sum, 63), 1 << 30);
     }
     return {-1, 0, 0, 0, 0, 0};
 }
 
-// Row tiles of bm rows in the groups before group e, by one wavefront.
+// Row tiles of bm rows in the groups before group e, by one wavefront; at most
+// gr.tiles.
 __device__ __forceinline__ int group_tiles_before(const Groups &gr, int e, int bm)
 {
     int sum = 0;
     for (int i = threadIdx.x & 63; i < e; i += 64) {
         int lo, hi;
         group_bounds(gr, i, lo, hi);
-        sum += (hi - lo + bm - 1) / bm;
+        sum = min(sum + (hi - lo + bm - 1) / bm, gr.tiles);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1)
-        sum += __shfl_xor(sum, d);
+        sum = min(sum + __shfl_xor(sum, d), gr.tiles);
     return sum;
 }
 

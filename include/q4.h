@@ -445,8 +445,8 @@ size_t q8_gemm_q8a_workspace_bytes(int M, int N, int K);
  *             device scratch (0, NULL allowed, up to 64 tokens), as for
  *             q4_gemm_ws (Q4_ERR_WORKSPACE when smaller).
  * The choice, offsets and order are exact and deterministic. Weights are exp
- * in f32 of exact-to-rounding differences, summed in f32: within (E + 16) 2^-24
- * of the exact value, relative, plus 2^-126. T == 0 is an empty problem:
+ * in f32 of differences rounded to f32, divided by their sum in f32: within
+ * (E + 120) 2^-24 of the exact value, relative, plus 2^-126. T == 0 is an empty problem:
  * nothing is written, offsets included. NaN logits give unspecified weights;
  * ids, offsets and order stay a valid grouping.
  */
@@ -477,9 +477,10 @@ size_t q4_route_workspace_bytes(int T, int E, int top_k);
  *   workspace, workspace_bytes: at least q4_gemm_grouped_workspace_bytes(G, M,
  *             N, K), as for q4_gemm_ws.
  * The contents of offsets and order are read on the device only, and kept in
- * bounds there: a bound is clamped to [previous bound of the same group, M],
- * a row outside [0, M) is skipped, and a row named twice gets one of its
- * values, element by element. Errors in the order shape, size, empty (M == 0
+ * bounds there: a group's bounds are clamped to 0 <= first <= last <= M, a row
+ * outside [0, M) is skipped, and a row named twice gets one of its values,
+ * element by element (where groups overlap so far that they have more row
+ * tiles than M sorted rows can, some of their rows may be left out). Errors in the order shape, size, empty (M == 0
  * or N == 0), NULL, alignment, overlap, workspace.
  * Accuracy: as q4_gemm_ws. Deterministic for rows named once.
  */
