@@ -492,7 +492,7 @@ static int gemm_grouped(q4k::WeightFormat fmt, size_t block_bytes, bool bf16, co
                                 nullptr, 0, offsets, order, y, (size_t)M * (size_t)N * 4, G, M};
     st = q4v::check_grouped(g);
     if (st == Q4_OK)
-        st = q4v::check_grouped_workspace(g, q4v::grouped_workspace_bytes(G, M, N, K, bf16 ? 1 : 2),
+        st = q4v::check_grouped_workspace(g, q4v::grouped_workspace_bytes(G, M, N, K, block_bytes, bf16 ? 2 : 4),
                                           workspace, workspace_bytes);
     if (st != Q4_OK)
         return st;
@@ -511,7 +511,7 @@ Q4_EXPORT int q4_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, c
 
 Q4_EXPORT size_t q4_gemm_grouped_workspace_bytes(int G, int M, int N, int K)
 {
-    return q4v::grouped_workspace_bytes(G, M, N, K, 2);
+    return q4v::grouped_workspace_bytes(G, M, N, K, 18, 4);
 }
 
 Q4_EXPORT int q4_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
@@ -524,7 +524,7 @@ Q4_EXPORT int q4_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_
 
 Q4_EXPORT size_t q4_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K)
 {
-    return q4v::grouped_workspace_bytes(G, M, N, K, 1);
+    return q4v::grouped_workspace_bytes(G, M, N, K, 18, 2);
 }
 
 Q4_EXPORT int q8_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
@@ -537,7 +537,7 @@ Q4_EXPORT int q8_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, c
 
 Q4_EXPORT size_t q8_gemm_grouped_workspace_bytes(int G, int M, int N, int K)
 {
-    return q4v::grouped_workspace_bytes(G, M, N, K, 2);
+    return q4v::grouped_workspace_bytes(G, M, N, K, 34, 4);
 }
 
 Q4_EXPORT int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
@@ -550,7 +550,7 @@ Q4_EXPORT int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_
 
 Q4_EXPORT size_t q8_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K)
 {
-    return q4v::grouped_workspace_bytes(G, M, N, K, 1);
+    return q4v::grouped_workspace_bytes(G, M, N, K, 34, 2);
 }
 
 Q4_EXPORT int f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes,

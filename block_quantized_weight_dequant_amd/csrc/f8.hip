@@ -136,11 +136,11 @@ template <class T>
 __global__ __launch_bounds__(256) void k_f8_quantize_tiles(const T *__restrict__ x,
                                                           uint8_t *__restrict__ q,
                                                           float *__restrict__ s, int M, int K,
-                                                          int Kb)
+                                                          int Kb, int first)
 {
     __shared__ float wave_max[4];
     const int tid = threadIdx.x;
-    const int rb = blockIdx.x / Kb, kb = blockIdx.x - rb * Kb;
+    const int tile = first + (int)blockIdx.x, rb = tile / Kb, kb = tile - rb * Kb;
     const int col = kb * 128 + 8 * (tid & 15);
     const bool col_in = col < K;
     const T *src = x + (col_in ? col : 0);
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void k_f8_quantize_tiles(const T *__restrict__
     m = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
     const float sc = m / kE4M3Max;
     if (tid == 0)
-        s[blockIdx.x] = sc;
+        s[tile] = sc;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = row0 + 16 * i;
@@ -177,9 +177,9 @@ template <class T>
 static hipError_t launch_quantize_t(const T *x, uint8_t *q, float *s, int M, int K, int block_rows,
                                     hipStream_t st)
 {
-    const unsigned Kb = (unsigned)(K + 127) / 128;
+    // At most 2^23 workgroups (2^31 threads) a launch.
+    const unsigned Kb = ((unsigned)K + 127) / 128;
     if (block_rows == 1) {
-        // At most 2^23 workgroups a launch (2^31 threads).
         const int rows = (int)((1u << 27) / Kb);   // K <= 2^31: at least 8
         for (int r0 = 0; r0 < M; r0 += rows) {
             const unsigned nb = (unsigned)(M - r0 < rows ? M - r0 : rows) * Kb;
@@ -193,9 +193,14 @@ static hipError_t launch_quantize_t(const T *x, uint8_t *q, float *s, int M, int
         }
         return hipSuccess;
     }
-    const unsigned Mb = (unsigned)(((long long)M + 127) / 128);
-    return launch_kernel(k_f8_quantize_tiles<T>, dim3(Mb * Kb), dim3(256), 0, st, x, q, s, M, K,
-                         (int)Kb);
+    const unsigned tiles = ((unsigned)M + 127) / 128 * Kb;   // below 2^31
+    for (unsigned first = 0; first < tiles; first += 1u << 23) {
+        const hipError_t e = launch_kernel(k_f8_quantize_tiles<T>, dim3(std::min(tiles - first, 1u << 23)),
+                                           dim3(256), 0, st, x, q, s, M, K, (int)Kb, (int)first);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_f8_quantize(const float *x, uint8_t *q, float *s, int M, int K, int block_rows,
@@ -240,7 +245,7 @@ hipError_t launch_f8_dequant(const uint8_t *q, const float *s, float *out, int M
     if (grid > 0x7fffffffu)
         return hipErrorInvalidValue;
     return launch_kernel(k_f8_dequant, dim3((unsigned)grid), dim3(256), 0, st, q, s, out, K,
-                         (K + 127) / 128, block_rows, n16);
+                         (int)(((unsigned)K + 127) / 128), block_rows, n16);
 }
 
 // ---------------------------------------------------------------------------

@@ -296,12 +296,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     }
 }
 
-// One to kGemvSlots rows in all: each is a decode GEMV of one activation row
-// (gemv_stream.h) with its group's weights, in one launch and no preparation.
-// Workgroup (x, p) takes 16 weight rows for position p; rows of one group read
-// its weights once each, which costs more only where such rows are many.
-constexpr int kGemvSlots = 8;
-
+// One to eight rows in all (grouped_in_place): each is a decode GEMV of one
+// activation row (gemv_stream.h) with its group's weights, in one launch, with
+// no preparation and no workspace. Workgroup (x, p) takes 16 weight rows for
+// position p; rows of one group read its weights once each, which costs more
+// only where such rows are many.
 template <class F, bool BF, int CH, bool LA>
 __global__ __launch_bounds__(64 * kGemvStreamWaves) void k_grouped_gemv(const void *__restrict__ a,
                                                                       const uint8_t *__restrict__ w,
@@ -351,7 +350,7 @@ template <class F, bool BF>
 static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, int N, int K,
                                    const Groups &gr, void *workspace, hipStream_t s)
 {
-    if (gr.M <= kGemvSlots && q4v::gemv_streams(1, N, K, F::kBytes, BF ? 2 : 4))
+    if (q4v::grouped_in_place(gr.M, N, K, F::kBytes, BF ? 2 : 4))
         return gemv_rows_line_aligned<F>(w, K) ? launch_grouped_gemv<F, BF, true>(a, w, y, N, K, gr, s)
                                                : launch_grouped_gemv<F, BF, false>(a, w, y, N, K, gr, s);
     const bool few = q4v::grouped_few(gr.G, gr.M, K);

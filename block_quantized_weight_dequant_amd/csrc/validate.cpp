@@ -312,13 +312,14 @@ int check_f8_product(const void *a, const void *a_s, const void *w, size_t w_byt
     return Q4_OK;
 }
 
-size_t grouped_workspace_bytes(int G, int M, int N, int K, int terms)
+size_t grouped_workspace_bytes(int G, int M, int N, int K, size_t block_bytes, size_t a_elem)
 {
-    if (check_group_shape(G, M, N, K, 64, 1 << 22, 1) != Q4_OK || M == 0 || N == 0)
+    if (check_group_shape(G, M, N, K, 64, 1 << 22, 1) != Q4_OK || M == 0 || N == 0 ||
+        grouped_in_place(M, N, K, block_bytes, a_elem))
         return 0;
     const int bm = grouped_few(G, M, K) ? 16 : 128;
     size_t n = (size_t)group_row_tiles(G, M, bm) * (size_t)bm;   // below 2^39
-    if (!mul_ok(n, (size_t)K, &n) || !mul_ok(n, (size_t)terms * 2, &n))
+    if (!mul_ok(n, (size_t)K, &n) || !mul_ok(n, a_elem, &n))
         return SIZE_MAX;
     const size_t e = grouped_exp_bytes(G, M, K);
     return n > SIZE_MAX - e ? SIZE_MAX : n + e;
@@ -351,6 +352,8 @@ int check_grouped(const GroupedArgs &g)
 
 int check_grouped_workspace(const GroupedArgs &g, size_t need, const void *ws, size_t ws_bytes)
 {
+    if (need == 0)
+        return Q4_OK;
     if (need == SIZE_MAX)
         return Q4_ERR_SIZE;
     if (ws_bytes < need)

@@ -192,10 +192,17 @@ inline bool grouped_few(int G, int M, int K)
     return K % 256 == 0 && K <= 28672 && (long long)M <= 32LL * G;
 }
 
+// Up to 8 rows are multiplied in place, each by the streaming GEMV kernel with
+// its group's matrix, where that kernel takes the shape: no workspace.
+inline bool grouped_in_place(int M, int N, int K, size_t block_bytes, size_t a_elem)
+{
+    return M <= 8 && gemv_streams(1, N, K, block_bytes, a_elem);
+}
 // Workspace of q4_gemm_grouped and its kin: the row exponents of the tiles'
-// rows (int32, padded to 256 bytes), then their operands, terms binary16 values
-// an element. 0 for an empty or invalid shape, SIZE_MAX when it does not fit.
-size_t grouped_workspace_bytes(int G, int M, int N, int K, int terms);
+// rows (padded to 256 bytes), then their operands: a_elem / 2 binary16 terms an
+// element (two of f32 activations, one of bfloat16). 0 in place, and for invalid
+// or empty shapes; SIZE_MAX on overflow.
+size_t grouped_workspace_bytes(int G, int M, int N, int K, size_t block_bytes, size_t a_elem);
 inline size_t grouped_exp_bytes(int G, int M, int K)
 {
     const int bm = grouped_few(G, M, K) ? 16 : 128;

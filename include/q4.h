@@ -480,9 +480,11 @@ size_t q4_route_workspace_bytes(int T, int E, int top_k);
  * bounds there: a group's bounds are clamped to 0 <= first <= last <= M, a row
  * outside [0, M) is skipped, and a row named twice gets one of its values,
  * element by element (where groups overlap so far that they have more row
- * tiles than M sorted rows can, some of their rows may be left out). Errors in the order shape, size, empty (M == 0
- * or N == 0), NULL, alignment, overlap, workspace.
- * Accuracy: as q4_gemm_ws. Deterministic for rows named once.
+ * tiles than M sorted rows can, some of their rows may be left out). Errors in
+ * the order shape, size, empty (M == 0 or N == 0), NULL, alignment, overlap,
+ * workspace.
+ * Accuracy: as q4_gemm_ws (as q4_gemv in place). Deterministic for rows named
+ * once.
  */
 int q4_gemm_grouped(const float *a, const void *w_q, size_t w_bytes, const int32_t *offsets,
                     const int32_t *order, int share, float *y, int G, int M, int N, int K,
@@ -505,7 +507,9 @@ int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, con
 
 /*
  * q4_gemm_grouped_workspace_bytes and its kin — the row exponents and operands
- * of the groups' row tiles. With bm = 16 when K % 256 == 0, K <= 28672 and M
+ * of the groups' row tiles. 0 (NULL allowed) for M <= 8 rows where K % 256 == 0
+ * and one W[e] and one row of a are below 2^31 bytes: those are multiplied in
+ * place. Else, with bm = 16 when K % 256 == 0, K <= 28672 and M
  * <= 32 G, else 128, and R = (M / bm + min(G, M)) * bm rows: R * 4 bytes padded
  * to 256, then R * K * 4 (f32) or R * K * 2 (bfloat16). 0 for invalid or empty
  * shapes, SIZE_MAX on overflow. Pure functions of their arguments.

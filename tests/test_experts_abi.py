@@ -60,11 +60,16 @@ def test_grouped_workspace_bytes(f, act):
     ws = getattr(binding, f + "_gemm_grouped" + act + "_workspace_bytes")
     e = 2 if act else 4
     pad = lambda n: -(-n // 256) * 256
-    assert ws(8, 2, 64, 4096) == pad(2 * 16 * 4) + 2 * 16 * 4096 * e              # two 16-row tiles at most
+    for M in range(1, 9):
+        assert ws(8, M, 64, 4096) == 0                                            # multiplied in place
+    assert ws(8, 9, 64, 4096) == pad(8 * 16 * 4) + 8 * 16 * 4096 * e              # eight 16-row tiles at most
+    big = 2 ** 31 // (8 * BYTES[f])                                               # the first N whose W[e] reaches 2^31 bytes
+    assert ws(8, 2, big, 256) == 0
+    assert ws(8, 2, big + 1, 256) == pad(2 * 16 * 4) + 2 * 16 * 256 * e
     assert ws(8, 256, 64, 4096) == pad(24 * 16 * 4) + 24 * 16 * 4096 * e
     assert ws(8, 257, 64, 4096) == pad(10 * 128 * 4) + 10 * 128 * 4096 * e
     assert ws(8, 2, 64, 64) == pad(2 * 128 * 4) + 2 * 128 * 64 * e                # K % 256 != 0: 128-row tiles
-    assert ws(8, 2, 64, 28928) == pad(2 * 128 * 4) + 2 * 128 * 28928 * e
+    assert ws(8, 9, 64, 28928) == pad(8 * 128 * 4) + 8 * 128 * 28928 * e
     for G, M, N, K in [(0, 2, 4, 64), (1025, 2, 4, 64), (8, 0, 4, 64), (8, -1, 4, 64), (8, 2, 0, 64), (8, 2, 4, 32),
                        (8, 2, 4, 96), (8, 2, 4, 2 ** 22 + 64), (8, 2 ** 30 + 1, 4, 64)]:
         assert ws(G, M, N, K) == 0, (G, M, N, K)
