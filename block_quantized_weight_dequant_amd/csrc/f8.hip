@@ -6,6 +6,8 @@
 // 128 columns of a row), weights codes [N, K] with scales [ceil(N / 128),
 // ceil(K / 128)] (one per 128 x 128 tile), all row-major; a row's last block
 // may be short.
+#include <algorithm>
+
 #include "device_common.h"
 #include "groups.h"
 #include "launch.h"
@@ -496,24 +498,27 @@ using Rows1 = RowsShape<1, 8, 4>;
 using Rows2 = RowsShape<2, 8, 3>;
 using Rows3 = RowsShape<3, 4, 4>;
 using Rows4 = RowsShape<4, 4, 3>;
-using Rows8 = RowsShape<8, 4, 2>;
 
-// Many rows: bound by the matrix instructions. A workgroup of eight wavefronts
-// computes BN x BM of y^T, WN x WM wavefronts of TN x TM tiles each. Per step
-// (one block of K) it stages both operands in LDS by direct loads, in a ring of
-// NS stages; 16-byte pieces of a row's 128 bytes are
-// stored at piece ^ (row % 8), so that the 8 rows that an LDS read serves at a
-// time lie in different banks (the lanes' global addresses carry the
-// permutation; the LDS side of a direct load is contiguous). The activation
-// scales of eight steps are staged at a time: loaded step by step, a scale of
-// each of 64 rows a load, they took as many cache lines as both operands twice
-// over.
-template <int WN_, int WM_, int TN_, int TM_, int NS_>
+// More rows: bound by the matrix instructions. A workgroup of eight wavefronts
+// computes BN x BM of y^T, WN x WM x KS wavefronts of TN x TM tiles each. Per
+// step (KS blocks of K, each taken by the WN x WM wavefronts of one half) it
+// stages both operands in LDS by direct loads, in a ring of NS stages. With few
+// tiles a step is as long as its chain of latencies (barrier, LDS, matrix
+// instruction, FMA: 0.3 us), so the small shapes take two blocks a step and add
+// the halves at the end (256 x 4096 x 4096 in 64 x 64 tiles: 13.6 us with one
+// block a step, 11.4 with two); the larger shapes need the LDS for the ring.
+// 16-byte pieces of a row's 128 bytes are stored at piece ^ (row % 8), so that
+// the 8 rows that an LDS read serves at a time lie in different banks (the
+// lanes' global addresses carry the permutation; the LDS side of a direct load
+// is contiguous). The activation scales of eight blocks are staged at a time:
+// loaded step by step, a scale of each of 64 rows a load, they took as many
+// cache lines as both operands twice over.
+template <int WN_, int WM_, int TN_, int TM_, int NS_, int KS_ = 1>
 struct TileShape {
-    static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NS = NS_;
+    static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NS = NS_, KS = KS_;
     static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-    static constexpr int kThreads = 64 * WN * WM;
-    static constexpr int kWLoads = BN * 8 / kThreads, kALoads = BM * 8 / kThreads;
+    static constexpr int kThreads = 64 * WN * WM * KS;
+    static constexpr int kWLoads = KS * BN * 8 / kThreads, kALoads = KS * BM * 8 / kThreads;
     static constexpr int kLoads = kWLoads + kALoads;       // of every wavefront and step
     static constexpr int kSLoads = BM * 8 / kThreads;      // of a chunk of scales
     static constexpr int kInFlight = (NS - 2) * kLoads;    // younger than the stage that a turn waits for
@@ -527,7 +532,9 @@ struct TileShape {
     static constexpr int kSpread = NS == 2 ? TN : kTurn, kSlots = TN + kSpread;
     static constexpr int kTailLoads = TN * kLoads / kSlots;
     static constexpr int kRowBytes = BN * 2 + 16;          // of a row of y in LDS
+    static constexpr int kChunk = 8 / KS;                  // steps of a chunk of scales
     static_assert(BN * 8 % kThreads == 0 && BM * 8 % kThreads == 0 && BM % 64 == 0 && BM <= kThreads, "whole loads");
+    static_assert((KS == 1 || KS == 2) && NS - 2 < kChunk - 1, "scales land a chunk ahead");
     static_assert(TN * 16 <= 128 && 128 % (TN * 16) == 0, "a wavefront's columns share a weight scale");
     static_assert(TM % 2 == 0, "activation operands alternate between two registers");
     static_assert(NS >= 2 && kInFlight < 64, "vmcnt counts to 63");
@@ -537,9 +544,10 @@ template <class S>
 struct TileLds {
     union {
         struct {
-            u32x4 w[S::NS][S::BN * 8];
-            u32x4 a[S::NS][S::BM * 8];
+            u32x4 w[S::NS][S::KS * S::BN * 8];
+            u32x4 a[S::NS][S::KS * S::BM * 8];
         };
+        f32x4 red[S::KS == 1 ? 1 : S::WN * S::WM * S::kTiles][64];
         uint8_t y[S::BM * S::kRowBytes];
     };
     float s[2][S::BM * 8];   // of eight steps: [row / 8][step][row % 8]
@@ -603,7 +611,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     }
     const int n0 = nt * S::BN, m0 = mt * S::BM;
     const int li = lane & 15, g = lane >> 4;
-    const int wn = wave % S::WN, wm = wave / S::WN;
+    const int wn = wave % S::WN, wm = wave / S::WN % S::WM, ks = wave / (S::WN * S::WM);
 
     // Resources: this tile's weight rows; its activation rows and scales, or
     // (grouped) all of them.
@@ -633,12 +641,12 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     static_assert(S::kThreads % 64 == 0, "rows of a load are equal mod 8");
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
-        const int r = (j * S::kThreads + tid) >> 3;
+        const int r = ((j * S::kThreads + tid) >> 3) % S::BN;
         wo[j] = r < wrows ? (uint32_t)r * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
     }
 #pragma unroll
     for (int j = 0; j < S::kALoads; ++j) {
-        const int x = a_row((j * S::kThreads + tid) >> 3);
+        const int x = a_row(((j * S::kThreads + tid) >> 3) % S::BM);
         ao[j] = x >= 0 ? (uint32_t)x * (uint32_t)p.K + (uint32_t)piece : kOutOfRange;
     }
 #pragma unroll
@@ -646,25 +654,27 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         const int x = a_row((j * S::kThreads + tid) / 64 * 8 + (lane & 7));
         so[j] = x >= 0 ? ((uint32_t)x * (uint32_t)p.Kb + (uint32_t)(lane >> 3)) * 4u : kOutOfRange;
     }
-    const int steps = p.Kb;
+    const int steps = (p.Kb + S::KS - 1) / S::KS;
+    // Block of a step that load j takes a part of.
+    auto w_block = [](int j) { return j * S::kThreads / (S::BN * 8); };
+    auto a_block = [](int j) { return j * S::kThreads / (S::BM * 8); };
     // Called before a step's loads, in order of the steps: in a short last step
     // the pieces past K, and after it everything, move out of range, where they
     // read as zero. No earlier step needs the offsets again.
     auto trim = [&](int step) __attribute__((always_inline)) {
-        const int left = p.K - step * 128;
-        if (left >= 128)
+        const int left = p.K - step * (S::KS * 128);
+        if (left >= S::KS * 128)
             return;
-        const bool out = piece >= left;
 #pragma unroll
         for (int j = 0; j < S::kWLoads; ++j)
-            wo[j] = out ? kOutOfRange : wo[j];
+            wo[j] = piece >= left - w_block(j) * 128 ? kOutOfRange : wo[j];
 #pragma unroll
         for (int j = 0; j < S::kALoads; ++j)
-            ao[j] = out ? kOutOfRange : ao[j];
+            ao[j] = piece >= left - a_block(j) * 128 ? kOutOfRange : ao[j];
     };
-    // The scales of steps 8 c .. 8 c + 7; those past the last step read as zero.
+    // The scales of blocks 8 c .. 8 c + 7; those past the last block read as zero.
     auto issue_scales = [&](int c) __attribute__((always_inline)) {
-        const bool in = 8 * c + (lane >> 3) < steps;
+        const bool in = 8 * c + (lane >> 3) < p.Kb;
 #pragma unroll
         for (int j = 0; j < S::kSLoads; ++j)
             load4_to_lds(sr, lds.s[c & 1] + j * S::kThreads + wave * 64, in ? so[j] : kOutOfRange, c * 32);
@@ -672,9 +682,11 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     // Load l of a step into its stage st.
     auto issue = [&](int step, int st, int l) __attribute__((always_inline)) {
         if (l < S::kWLoads)
-            load16_to_lds(wr, lds.w[st] + l * S::kThreads + wave * 64, wo[l], step * 128);
+            load16_to_lds(wr, lds.w[st] + l * S::kThreads + wave * 64, wo[l],
+                         (step * S::KS + w_block(l)) * 128);
         else
-            load16_to_lds(ar, lds.a[st] + (l - S::kWLoads) * S::kThreads + wave * 64, ao[l - S::kWLoads], step * 128);
+            load16_to_lds(ar, lds.a[st] + (l - S::kWLoads) * S::kThreads + wave * 64, ao[l - S::kWLoads],
+                          (step * S::KS + a_block(l - S::kWLoads)) * 128);
     };
 
     f32x4 acc[S::TN][S::TM];
@@ -693,14 +705,15 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     const int o0 = li * 8 + (g ^ (li & 7)), o1 = li * 8 + ((4 + g) ^ (li & 7));
     auto operand = [&](const u32x4 *base) __attribute__((always_inline)) { return join(base[o0], base[o1]); };
     auto w_operand = [&](int st, int i) __attribute__((always_inline)) {
-        return operand(lds.w[st] + (wn * S::TN + i) * 128);
+        return operand(lds.w[st] + (ks * (S::BN / 16) + wn * S::TN + i) * 128);
     };
     auto a_operand = [&](int st, int j) __attribute__((always_inline)) {
-        return operand(lds.a[st] + (wm * S::TM + j) * 128);
+        return operand(lds.a[st] + (ks * (S::BM / 16) + wm * S::TM + j) * 128);
     };
 
     auto read_scales = [&](int step, float (&to)[S::TM]) __attribute__((always_inline)) {
-        const float *base = lds.s[(step >> 3) & 1] + (wm * S::TM * 2 + (li >> 3)) * 64 + (step & 7) * 8 + (li & 7);
+        const int b = step * S::KS + ks;
+        const float *base = lds.s[(b >> 3) & 1] + (wm * S::TM * 2 + (li >> 3)) * 64 + (b & 7) * 8 + (li & 7);
 #pragma unroll
         for (int x = 0; x < S::TM; ++x)
             to[x] = base[x * 128];
@@ -746,8 +759,8 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         // Chunk step / 8 - 1 was last read before the previous step's end, so
         // the next chunk may take its place; it lands within eight steps, older
         // by then than any load that a turn leaves in flight.
-        if ((step & 7) == 0)
-            issue_scales((step >> 3) + 1);
+        if (step % S::kChunk == 0)
+            issue_scales(step / S::kChunk + 1);
         __builtin_amdgcn_sched_barrier(0);
         unroll<S::kTiles + (kCarry ? 0 : kLag)>([&](auto t_c) __attribute__((always_inline)) {
             constexpr int t = decltype(t_c)::value, i = t % S::TN, j = t / S::TN;
@@ -769,7 +782,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
                     // Here no LDS result is waited for before the turn, so the
                     // scalar load in flight makes no such wait longer.
                     __builtin_amdgcn_sched_barrier(0);
-                    ws_next = wsp[min(step + 1, p.Kb - 1)];
+                    ws_next = wsp[min((step + 1) * S::KS + ks, p.Kb - 1)];
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -809,7 +822,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
         for (int l = 0; l < (s < S::NS - 1 ? S::kLoads : S::kTailLoads); ++l)
             issue(s, s, l);
     }
-    ws_next = wsp[0];
+    ws_next = wsp[min(ks, p.Kb - 1)];
     wait_and_meet<S::kInFlight + S::kTailLoads>();
 #pragma unroll
     for (int i = 0; i < S::TN; ++i)
@@ -829,6 +842,22 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
             add_tile(std::integral_constant<int, S::kTiles - kLag + t.value>{}, sc[S::TM - 1]);
         });
     wait_and_meet<0>();   // no load is on its way into the LDS that the epilogue uses
+    if constexpr (S::KS == 2) {
+        // The second half of the wavefronts hands its sums to the first.
+        f32x4 (*red)[64] = lds.red + wave % (S::WN * S::WM) * S::kTiles;
+        if (ks != 0) {
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t)
+                red[t][lane] = acc[t % S::TN][t / S::TN];
+        }
+        __syncthreads();
+        if (ks == 0) {
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t)
+                acc[t % S::TN][t / S::TN] += red[t][lane];
+        }
+        __syncthreads();
+    }
 
     // y: through LDS, so that whole rows of the tile leave as 16-byte stores of
     // consecutive lanes (where the rows of y allow them).
@@ -841,6 +870,8 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     if ((p.N & 7) == 0) {
 #pragma unroll
         for (int j = 0; j < S::TM; ++j) {
+            if (ks != 0)
+                break;
             uint8_t *row = lds.y + ((wm * S::TM + j) * 16 + li) * S::kRowBytes + (wn * (S::TN * 16) + 4 * g) * 2;
 #pragma unroll
             for (int i = 0; i < S::TN; ++i) {
@@ -857,7 +888,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
                 *reinterpret_cast<u32x4 *>(p.y + (size_t)to * (size_t)p.N + n) =
                     *reinterpret_cast<const u32x4 *>(lds.y + r * S::kRowBytes + tid % kLanes * 16);
         }
-    } else {
+    } else if (ks == 0) {
 #pragma unroll
         for (int j = 0; j < S::TM; ++j) {
             const int to = y_row((wm * S::TM + j) * 16 + li);
@@ -871,9 +902,11 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     }
 }
 
-using TileLarge = TileShape<2, 4, 8, 4, 2>;    // 256 columns x 256 rows
-using TileWide = TileShape<4, 2, 4, 4, 3>;     // 256 x 128
-using TileSmall = TileShape<2, 4, 4, 2, 4>;    // 128 x 128
+using TileQuarter = TileShape<2, 2, 2, 2, 4, 2>;   // 64 columns x 64 rows
+using TileHalf = TileShape<2, 2, 4, 2, 3, 2>;      // 128 x 64
+using TileSmall = TileShape<2, 4, 4, 2, 4>;        // 128 x 128
+using TileWide = TileShape<4, 2, 4, 4, 3>;         // 256 x 128
+using TileLarge = TileShape<2, 4, 8, 4, 2>;        // 256 x 256
 
 template <class S>
 static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
@@ -909,42 +942,61 @@ static hipError_t launch_rows_grouped(const F8Product &p, const Groups &gr, hipS
                          dim3(S::kThreads), 0, st, p, gr);
 }
 
-// Which kernel: the one whose rounds of 256 workgroups cost least. Times of a
-// round per block of K, in 10 ns on MI355X: a row form by its row groups, with
-// the weights streaming (M = 1, 32, 40, 64 and 128 at 4096 x 4096 and 4096 x
-// 14336), a tile with the chip full. At 4096 columns 128 rows take 12.7 us by
-// rows and 16.2 us by tiles; at 14336 columns 43 and 18 us.
-static int rows_cost(int rg) { return rg == 1 ? 11 : rg == 2 ? 12 : rg == 3 ? 14 : rg == 4 ? 19 : 30; }
-constexpr int kSmallCost = 52;
+// Which kernel. A form costs its rounds of 256 workgroups times a round's time
+// per block of K, in 10 ns on MI355X (beside some 4 us a call): few rows by
+// their row groups with the weights streaming, tiles with the chip full. Few
+// rows are taken where they cost no more than the cheapest tile, else the
+// largest tile that costs no more than that, or than the weights' bytes take at
+// 5.5 TB/s: where those bound the call the larger tiles stream them better (37
+// tokens, 2 of 8 experts of 14336 x 4096: wide 113 us, half 119; 512 tokens, 8 of
+// 128 of 1536 x 2048: wide 87, quarter 96). M x N x K by few rows and by quarter
+// tiles, weights in cache: 64 x 4096 x 4096 9.2 and 9.7 us, 16 x 8192 x 8192 13.9
+// and 14.2, 1 x 14336 x 4096 16.5 and 11.7, 32 x 14336 x 4096 20.1 and 12.4
+// (weights from HBM: 24.9 and 16.1). By quarter, half and small tiles: 256 x 4096
+// x 4096 11.4, 15.9 and 18.3 us, 512 x 4096 x 4096 19.7, 17.1 and 21.5, 1001 x
+// 4096 x 4096 35.8, 26.6 and 21.7. By small, wide and large ones: 1001 x 4096 x
+// 4096 21, 28 and 46 us, 2048 x 14336 x 4096 163, 149 and 129.
+enum Form { kRows, kQuarter, kHalf, kSmall, kWide, kLarge };
 
-// Row groups for M rows, 0 past 128.
-static int row_groups(long long M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : M <= 64 ? 4 : M <= 128 ? 8 : 0; }
+template <class S>
+static long long tile_cost(long long tiles_m, int N, int round)
+{
+    return (tiles_m * (((long long)N + S::BN - 1) / S::BN) + 255) / 256 * round;
+}
 
-static long long rounds(long long workgroups) { return (workgroups + 255) / 256; }
+// For `groups` groups with tiles_m(bm) row tiles of bm rows in all; rg: the
+// row groups of the few-row form, 0 if the groups are too long for it.
+template <class TilesM>
+static Form choose_form(long long groups, int rg, int N, TilesM tiles_m)
+{
+    constexpr int kRowsRound[] = {0, 11, 12, 14, 19};
+    const long long cost[] = {tile_cost<TileQuarter>(tiles_m(64), N, 25), tile_cost<TileHalf>(tiles_m(64), N, 40),
+                              tile_cost<TileSmall>(tiles_m(128), N, 70), tile_cost<TileWide>(tiles_m(128), N, 110),
+                              tile_cost<TileLarge>(tiles_m(256), N, 190)};
+    const long long least = *std::min_element(cost, cost + 5);
+    if (rg && (groups * (((long long)N + 15) / 16) + 255) / 256 * kRowsRound[rg] <= least)
+        return kRows;
+    int i = 4;
+    while (cost[i] > std::max(least, groups * N / 430))
+        --i;
+    return (Form)(kQuarter + i);
+}
 
 hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
                           uint16_t *y, int M, int N, int K, hipStream_t st)
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
-    const long long tn = ((long long)N + 127) / 128, tm = ((long long)M + 127) / 128;
-    const int rg = row_groups(M);
-    if (rg && rounds(tn * 8) * rows_cost(rg) <= rounds(tn) * kSmallCost) {
-        switch (rg) {
-        case 1: return launch_rows<Rows1>(p, st);
-        case 2: return launch_rows<Rows2>(p, st);
-        case 3: return launch_rows<Rows3>(p, st);
-        case 4: return launch_rows<Rows4>(p, st);
-        default: return launch_rows<Rows8>(p, st);
-        }
+    const int rg = M <= 64 ? (M + 15) / 16 : 0;
+    switch (choose_form(1, rg, N, [&](int bm) { return ((long long)M + bm - 1) / bm; })) {
+    case kRows:
+        return rg == 1 ? launch_rows<Rows1>(p, st) : rg == 2 ? launch_rows<Rows2>(p, st)
+             : rg == 3 ? launch_rows<Rows3>(p, st) : launch_rows<Rows4>(p, st);
+    case kQuarter: return launch_tiles<TileQuarter>(p, st);
+    case kHalf: return launch_tiles<TileHalf>(p, st);
+    case kSmall: return launch_tiles<TileSmall>(p, st);
+    case kWide: return launch_tiles<TileWide>(p, st);
+    default: return launch_tiles<TileLarge>(p, st);
     }
-    // With the chip full a step of the large tiles takes 1.9 us, of the wide
-    // ones 1.1 us and of the small ones 0.7 us (2048 x 14336 x 4096: 129, 149
-    // and 163 us; 1001 x 4096 x 4096: 46, 28 and 21 us).
-    const long long tn2 = (tn + 1) / 2, tm2 = (tm + 1) / 2;
-    const long long large = rounds(tm2 * tn2) * 19, wide = rounds(tm * tn2) * 11, small = rounds(tm * tn) * 7;
-    if (large <= wide && large <= small)
-        return launch_tiles<TileLarge>(p, st);
-    return wide <= small ? launch_tiles<TileWide>(p, st) : launch_tiles<TileSmall>(p, st);
 }
 
 template <class S>
@@ -964,23 +1016,21 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
     const Groups gr = {offsets, order, G, M, share, 0};
-    // As above, for groups of the mean size; groups that are longer take the row
-    // form's passes several times, and shorter ones a part of a tile.
-    const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit, cols = ((long long)N + 127) / 128;
-    const int rg = mean <= 8 ? 1 : mean <= 16 ? 2 : mean <= 32 ? 4 : mean <= 64 ? 8 : 0;
-    if (rg && rounds(hit * cols * 8) * rows_cost(rg) <= rounds(hit * cols) * kSmallCost) {
-        switch (rg) {
-        case 1: return launch_rows_grouped<Rows1>(p, gr, st);
-        case 2: return launch_rows_grouped<Rows2>(p, gr, st);
-        case 4: return launch_rows_grouped<Rows4>(p, gr, st);
-        default: return launch_rows_grouped<Rows8>(p, gr, st);
-        }
+    // The host knows the mean size only. Few rows: with room for groups of twice
+    // the mean (longer ones take several passes). Tiles: a group ends within one,
+    // half filled on average.
+    const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit;
+    const int rg = mean <= 8 ? 1 : mean <= 16 ? 2 : mean <= 32 ? 4 : 0;
+    switch (choose_form(hit, rg, N, [&](int bm) { return std::max(hit, M / bm + hit / 2); })) {
+    case kRows:
+        return rg == 1 ? launch_rows_grouped<Rows1>(p, gr, st) : rg == 2 ? launch_rows_grouped<Rows2>(p, gr, st)
+             : launch_rows_grouped<Rows4>(p, gr, st);
+    case kQuarter: return launch_grouped_tiles<TileQuarter>(p, gr, st);
+    case kHalf: return launch_grouped_tiles<TileHalf>(p, gr, st);
+    case kSmall: return launch_grouped_tiles<TileSmall>(p, gr, st);
+    case kWide: return launch_grouped_tiles<TileWide>(p, gr, st);
+    default: return launch_grouped_tiles<TileLarge>(p, gr, st);
     }
-    // Wide tiles where they fill the chip (1024 tokens, 4 of 32 experts, 4096 x
-    // 1792: 84 us, small ones 94); else the small ones, twice as many.
-    if (hit * ((cols + 1) / 2) >= 256)
-        return launch_grouped_tiles<TileWide>(p, gr, st);
-    return launch_grouped_tiles<TileSmall>(p, gr, st);
 }
 
 }  // namespace q4k

@@ -27,7 +27,7 @@
 extern "C" {
 #endif
 
-/* Columns of a block, and the largest K and group count of the products. */
+/* Columns of a block, and the largest K of the products. */
 #define F8_BLOCK 128
 #define F8_MAX_K 4194304
 

@@ -187,6 +187,40 @@ def test_grouped_wide_form(fmt, act):
         check_grouped(fmt, run_grouped(fmt, act, a, w, off, order, 1, G, M, N, K), ref, P, there, K, counts)
 
 
+@pytest.mark.parametrize("counts,N,K", [([150, 3, 247], 4104, 416), ([500, 3, 197], 4100, 288), ([500, 20], 8192, 1056),
+                                        ([3000, 900], 8192, 160), ([60, 50, 64, 0, 40], 14336, 672)])
+def test_grouped_f8_tile_forms(counts, N, K):
+    # Enough rows and columns for each form of larger tiles; the reference in
+    # f64 on the card.
+    G, (off, M) = len(counts), split(counts)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x, v = torch.randn(M, K, generator=g, device=DEV), torch.randn(G * N, K, generator=g, device=DEV)
+    a, a_s, A = torch.empty(M, K, dtype=torch.uint8, device=DEV), torch.empty(M, pl.blocks(K), device=DEV), torch.empty(M, K, device=DEV)
+    q4.f8_quantize(x, a, a_s, M, K)
+    q4.f8_dequant(a, a_s, A, M, K)
+    w = torch.empty(G, N, K, dtype=torch.uint8, device=DEV)
+    w_s = torch.empty(G, pl.blocks(N), pl.blocks(K), device=DEV)
+    W = torch.empty(G, N, K, device=DEV)
+    for e in range(G):
+        s = torch.empty(pl.blocks(N), pl.blocks(K), device=DEV)     # w_s[e] need not be 16-byte aligned
+        q4.f8_quantize(v[e * N:(e + 1) * N], w[e], s, N, K, 128)
+        q4.f8_dequant(w[e], s, W[e], N, K, 128)
+        w_s[e] = s
+    order = torch.randperm(M, generator=g, device=DEV)
+    ref, P = torch.empty(M, N, dtype=torch.float64, device=DEV), torch.empty(M, N, dtype=torch.float64, device=DEV)
+    for e in range(G):
+        rows = order[int(off[e]):int(off[e + 1])]
+        B = W[e].double().t().contiguous()
+        ref[rows], P[rows] = A[rows].double() @ B, A[rows].double().abs() @ B.abs()
+    y = Guarded(M * N, torch.bfloat16, fill=7.0)
+    q4.f8_gemm_grouped(a, a_s, w, w_s, to_dev(np.asarray(off, dtype=np.int32)), order.int(), y.view, G, M, N, K)
+    torch.cuda.synchronize()
+    assert y.guards_intact()
+    tol = 1.01 * pl.product_tolerance(ref.cpu().numpy(), P.cpu().numpy(), K)     # A and W are rounded to f32
+    err = (y.view.double().reshape(M, N) - ref).abs().cpu().numpy()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
 @pytest.mark.parametrize("fmt,act", [("q4", "f32"), ("q8", "bf16"), ("f8", "f8")])
 @pytest.mark.parametrize("M", [6, 300])
 def test_grouped_long_rows(fmt, act, M):
