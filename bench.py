@@ -25,7 +25,9 @@ quantize of a 2048 x 4096 tensor; the same over Q8_0 weights; bfloat16 and
 Q8_0-quantized activations; one GPU's share of an 8-way row split; and
 streaming-read ceilings of the same byte counts. Each row is written to stderr
 as one ``row: {json}`` line (and to ``--rows-out``); stdout ends with ONE
-compact JSON line.
+compact JSON line. ``--rows experts`` measures the operators of an expert layer
+in place of those rows: the E4M3 quantizers and products, the router, and the
+products grouped by expert.
 
 ``roofline.traffic`` comes from the committed counter summary
 profiles/traffic.json (rocprofv3 FETCH_SIZE / WRITE_SIZE, scaled by a copy of
@@ -38,7 +40,7 @@ median of 5 runs of repeated full decode GEMVs, with the tiny and 8-row GEMVs,
 one-core runs, 16 rows of the 1024 x 4096 x 4096 prefill GEMM (TFLOP/s) and
 the dequant and quantize beside it.
 
-    python bench.py [--gpus 1] [--steps K] [--warmup W] [--rows all|headline]
+    python bench.py [--gpus 1] [--steps K] [--warmup W] [--rows all|headline|experts]
     python bench.py --summarize --trace DIR [--fetch DIR --write DIR --mfma DIR]
         (no GPU: reads rocprofv3 output of profiled bench runs, writes profiles/)
 """
@@ -77,7 +79,8 @@ def parse_args():
     p.add_argument("--steps", type=int, default=200)
     p.add_argument("--warmup", type=int, default=50)
     p.add_argument("--reps", type=int, default=5, help="timed replays per row")
-    p.add_argument("--rows", choices=["all", "headline"], default="all")
+    p.add_argument("--rows", choices=["all", "headline", "experts"], default="all",
+                   help="experts: the headline, then the E4M3, router and grouped-product rows")
     p.add_argument("--no-cpu-baseline", action="store_true")
     p.add_argument("--rows-out", help="write every row (and the CPU baseline's detail) here")
     p.add_argument("--spans-out", help="write each row's host-clock span here (for --summarize)")
@@ -601,6 +604,98 @@ def bench_rw_ceiling(torch, groups, read_words, write_words, steps, warmup, reps
     return row
 
 
+# Rows of --rows experts: (name, kind, sizes). Tokens T choose k of E experts.
+EXPERT_ROWS = [
+    ("f8_quantize_bf16_2048x4096", "quantize", dict(M=2048, K=4096, rows=1, act="bf16")),
+    ("f8_quantize_tiles_14336x4096", "quantize", dict(M=14336, K=4096, rows=128, act="f32")),
+    ("f8_gemv_1x4096x4096", "f8", dict(M=1, N=4096, K=4096)),
+    ("f8_gemv_8x14336x4096", "f8", dict(M=8, N=14336, K=4096)),
+    ("f8_gemm_40x4096x14336", "f8", dict(M=40, N=4096, K=14336)),
+    ("f8_gemm_256x4096x4096", "f8", dict(M=256, N=4096, K=4096)),
+    ("f8_gemm_1024x4096x4096", "f8", dict(M=1024, N=4096, K=4096)),
+    ("f8_gemm_2048x14336x4096", "f8", dict(M=2048, N=14336, K=4096)),
+    ("route_32_2of8", "route", dict(T=32, E=8, k=2)),
+    ("route_8192_6of64", "route", dict(T=8192, E=64, k=6)),
+    ("q4_grouped_f32_1_2of8_4096x4096", "grouped", dict(fmt="q4_0", act="f32", T=1, E=8, k=2, N=4096, K=4096)),
+    ("q4_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
+    ("q8_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
+    ("q4_grouped_bf16_2048_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="bf16", T=2048, E=8, k=2, N=14336, K=4096)),
+    ("f8_grouped_37_2of8_14336x4096", "grouped", dict(fmt="f8", act="f8", T=37, E=8, k=2, N=14336, K=4096)),
+    ("f8_grouped_2048_2of8_14336x4096", "grouped", dict(fmt="f8", act="f8", T=2048, E=8, k=2, N=14336, K=4096)),
+]
+
+
+def bench_expert(torch, q4, name, kind, steps, warmup, reps, profile, M=0, N=0, K=0, rows=1, act="f32",
+                 fmt="f8", T=0, E=1, k=1):
+    """One operator of the expert layer on inputs drawn on the device, R sets of
+    them in turn (cold). Bytes: each input read once, each output written once;
+    of the experts' weights only those that have rows."""
+    g = torch.Generator(device="cuda").manual_seed(len(name) + M + N + K + T)
+    dev = dict(device="cuda")
+    normal = lambda *n: torch.randn(*n, generator=g, **dev)
+    kb = -(-K // 128)
+    S = T * k
+
+    def e4m3(x, block_rows):
+        r, c = x.shape
+        q = torch.empty(r, c, dtype=torch.uint8, **dev)
+        s = torch.empty(-(-r // block_rows), -(-c // 128), **dev)
+        q4.f8_quantize(x, q, s, r, c, block_rows)
+        return q, s
+
+    def routed():
+        out = [torch.empty(n, dtype=torch.int32, **dev) for n in (S, E + 1, S)]
+        w, logits = torch.empty(S, **dev), normal(T, E)
+        ws = torch.empty(max(q4.q4_route_workspace_bytes(T, E, k), 16), dtype=torch.uint8, **dev)
+        call = lambda: q4.q4_route(logits, out[0], w, out[1], out[2], T, E, k, workspace=ws)
+        call()
+        return call, out[1], out[2]
+
+    def one_set():
+        """(a launch of the operator, algorithmic bytes, flops)."""
+        if kind == "quantize":
+            x = normal(M, K)
+            f, x = (q4.f8_quantize_bf16, x.bfloat16()) if act == "bf16" else (q4.f8_quantize, x)
+            q, s = torch.empty(M * K, dtype=torch.uint8, **dev), torch.empty(-(-M // rows), kb, **dev)
+            return (lambda: f(x, q, s, M, K, rows)), M * K * (x.element_size() + 1) + s.numel() * 4, 0
+        if kind == "f8":
+            (a, a_s), (w, w_s) = e4m3(normal(M, K), 1), e4m3(normal(N, K), 128)
+            y = torch.empty(M, N, dtype=torch.bfloat16, **dev)
+            f = q4.f8_gemv if M <= 8 else q4.f8_gemm
+            return ((lambda: f(a, a_s, w, w_s, y, M, N, K)),
+                    (M + N) * K + (a_s.numel() + w_s.numel()) * 4 + M * N * 2, 2 * M * N * K)
+        call, offsets, order = routed()
+        if kind == "route":
+            return call, T * E * 4 + S * 12 + (E + 1) * 4, 0
+        hit = int((offsets.diff() > 0).sum())
+        if fmt == "f8":
+            a, a_s = e4m3(normal(T, K), 1)
+            w, w_s = e4m3(normal(E * N, K), 128)    # N % 128 == 0: whole tiles an expert
+            y = torch.empty(S, N, dtype=torch.bfloat16, **dev)
+            return ((lambda: q4.f8_gemm_grouped(a, a_s, w, w_s, offsets, order, y, E, S, N, K, share=k)),
+                    T * K + hit * N * K + S * N * 2, 2 * S * N * K)
+        p = fmt[:2]
+        w = torch.empty(E * N * (K // 32) * BLOCK_BYTES[fmt], dtype=torch.uint8, **dev)
+        (q4.q4_quantize if p == "q4" else q4.q8_quantize)(normal(E * N, K) * 0.02, w)
+        a = normal(T, K).bfloat16() if act == "bf16" else normal(T, K)
+        entry = p + "_gemm_grouped" + ("_bf16" if act == "bf16" else "")
+        need = getattr(q4, entry + "_workspace_bytes")(E, S, N, K)
+        ws, y = torch.empty(max(need, 16), dtype=torch.uint8, **dev), torch.empty(S, N, **dev)
+        f = getattr(q4, entry)
+        return ((lambda: f(a, w, offsets, order, y, E, S, N, K, share=k, workspace=ws)),
+                a.numel() * a.element_size() + hit * (w.numel() // E) + S * N * 4, 2 * S * N * K)
+
+    MARKS.push(name)
+    call, nbytes, flops = one_set()
+    # At most 32 sets: the smallest calls stay in cache.
+    sets = [call] + [one_set()[0] for _ in range(min(copies_for_cold(nbytes), 32) - 1)]
+    t = run_timed(torch, lambda i: sets[i % len(sets)](), steps, warmup, reps, name, profile)
+    MARKS.pop()
+    us = t["kernel_us"]
+    return {"workload": name, "algorithmic_bytes": nbytes, "flops": flops, "input_sets": len(sets),
+            "kernel_GBs": nbytes / us / 1e3, "kernel_TFLOPs": flops / us / 1e6, **t}
+
+
 def probe_sweep(torch, sizes, steps, warmup, reps, out_path=None):
     """The streaming read (libq4probe) of each size, cold, over every launch
     shape q4probe_stream_read_cfg offers: threads per workgroup x loads per
@@ -870,6 +965,9 @@ def main_bench(args):
         emit_row(bench_dequant(torch, q4, wl, min(50, S), small_w, reps, P,
                                "q8_0_dequant_14336x4096"), rows)
         emit_row(bench_stream_ceiling(torch, 2 ** 30, min(10, S), 3, reps, P), rows)
+    if args.rows == "experts":
+        for name, kind, sizes in EXPERT_ROWS:
+            emit_row(bench_expert(torch, q4, name, kind, min(50, S), small_w, reps, P, **sizes), rows)
     if args.calibrate_copy:
         copy_calibration(torch)
 
@@ -1016,8 +1114,10 @@ def summarize(args):
         lines.append("command (trace):")
         lines.append("  cd /tmp && export TMPDIR=/tmp && rocprofv3 --kernel-trace --marker-trace "
                      "--stats --output-format csv -d <trace> -o trace -- python3 <repo>/bench.py "
-                     "--profile --no-cpu-baseline --steps 20 --warmup 5")
-        lines.append("summary: " + cmd_note)
+                     "--profile --no-cpu-baseline --steps 20 --warmup 5"
+                     + (" --rows experts" if args.rows == "experts" else ""))
+        lines.append("summary: " + (cmd_note if args.fetch else
+                                    "python3 bench.py --summarize --rows %s --trace <trace> --out <out>" % args.rows))
         lines.append("rows: dispatches inside each row's timed replays (%s ranges)" % how)
         lines.append("")
         lines.append("%-34s %-48s %6s %9s %9s %9s %9s" % ("workload", "kernel", "n", "mean_us",
