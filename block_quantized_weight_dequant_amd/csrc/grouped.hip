@@ -185,7 +185,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     const int n0 = blockIdx.x * G::kRows;
     const uint32_t row_bytes = (uint32_t)nblk * F::kBytes;
     const int wrows = min(G::kRows, N - n0);
-    // At most 64 rows of 28672 elements: the offsets are far below 2^31.
+    // At most 64 rows of 14336 elements: the offsets are far below 2^31.
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
         (void *)(w + ((size_t)e * (size_t)N + (size_t)n0) * (size_t)row_bytes), (short)0,
         (int)((uint32_t)wrows * row_bytes), kBufferRsrcWord3);

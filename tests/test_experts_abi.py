@@ -69,7 +69,8 @@ def test_grouped_workspace_bytes(f, act):
     assert ws(8, 256, 64, 4096) == pad(24 * 16 * 4) + 24 * 16 * 4096 * e
     assert ws(8, 257, 64, 4096) == pad(10 * 128 * 4) + 10 * 128 * 4096 * e
     assert ws(8, 2, 64, 64) == pad(2 * 128 * 4) + 2 * 128 * 64 * e                # K % 256 != 0: 128-row tiles
-    assert ws(8, 9, 64, 28928) == pad(8 * 128 * 4) + 8 * 128 * 28928 * e
+    assert ws(8, 9, 64, 14336) == pad(8 * 16 * 4) + 8 * 16 * 14336 * e
+    assert ws(8, 9, 64, 14592) == pad(8 * 128 * 4) + 8 * 128 * 14592 * e          # past 112 blocks a wavefront: 128-row tiles
     for G, M, N, K in [(0, 2, 4, 64), (1025, 2, 4, 64), (8, 0, 4, 64), (8, -1, 4, 64), (8, 2, 0, 64), (8, 2, 4, 32),
                        (8, 2, 4, 96), (8, 2, 4, 2 ** 22 + 64), (8, 2 ** 30 + 1, 4, 64)]:
         assert ws(G, M, N, K) == 0, (G, M, N, K)

@@ -222,10 +222,10 @@ def test_grouped_f8_tile_forms(counts, N, K):
 
 
 @pytest.mark.parametrize("fmt,act", [("q4", "f32"), ("q8", "bf16"), ("f8", "f8")])
-@pytest.mark.parametrize("M", [6, 300])
-def test_grouped_long_rows(fmt, act, M):
-    # K = 28928: past the few-row form, and two K segments of the tiles.
-    K, N, G = 28928, 40, 2
+@pytest.mark.parametrize("M,K", [(6, 28928), (300, 28928), (40, 14336), (40, 14592)])
+def test_grouped_long_rows(fmt, act, M, K):
+    # K = 14336 is the few-row form's longest; two and more K segments of the tiles.
+    N, G = 40, 2
     off, _ = split([M - 2, 2])
     a, av = activations(act, M, K, 13)
     w, wv = weights(fmt, G, N, K, 99)
