@@ -588,6 +588,16 @@ __device__ __forceinline__ void gemm_split_body(
                 for (int q = 0; q < 4; ++q)
                     red[(wq * 64 + ms * (CN * 4) + ns * 4 + q) * 64 + lane] = acc[ms][ns][q];
     }
+    // GROUPED: the tile's rows of y and their exponents, fetched at once (2048
+    // tokens, 2 of 8 experts, 14336 x 4096, Q4_0 with bfloat16: 832 us when each
+    // is read as its row is stored, 780 so).
+    [[maybe_unused]] int2 *rows = reinterpret_cast<int2 *>(&lds.b[0][0]);
+    if constexpr (GROUPED) {
+        static_assert(sizeof(lds.b) >= kGemmBM * sizeof(int2), "a row and an exponent each");
+        const int r = tid - kSplitGemmThreads / 2;
+        if (r >= 0 && r < kGemmBM)
+            rows[r] = pos0 + r < pos1 ? int2{group_row(gr, pos0 + r), row_exp[m0 + r]} : int2{-1, 0};
+    }
     __syncthreads();
     if (kg == 0) {
         // Lane (li, g) of tile (ms, ns) holds rows 4g..4g+3 of column li.
@@ -603,11 +613,11 @@ __device__ __forceinline__ void gemm_split_body(
             for (int q = 0; q < 4; ++q) {
                 const int m = mb + ms * 16 + q;
                 if constexpr (GROUPED) {
-                    const int pos = pos0 + (m - m0), row = pos < pos1 ? group_row(gr, pos) : -1;
-                    if (row < 0)
+                    const int2 to = rows[m - m0];
+                    if (to.x < 0)
                         continue;
-                    const int pe = row_exp[m];
-                    float *yr = y + (size_t)row * (size_t)N + nb;
+                    const int pe = to.y;
+                    float *yr = y + (size_t)to.x * (size_t)N + nb;
 #pragma unroll
                     for (int ns = 0; ns < CN; ++ns) {
                         float v = acc[ms][ns][q] + red[(wq * 64 + ms * (CN * 4) + ns * 4 + q) * 64 + lane];

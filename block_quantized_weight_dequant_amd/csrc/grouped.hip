@@ -125,14 +125,17 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
 }
 
 // ---------------------------------------------------------------------------
-// Few rows a group: bound by the bytes of the weights. Workgroup (x, e) takes
-// 16 CT weight rows of group e past the group's rows, 16 R at a time. Its four
-// wavefronts deal the row's chunks of 8 blocks (256 elements: 144 or 272
-// bytes, whole 16-byte pieces) among themselves; each stages its own chunk's
-// raw bytes in its own LDS by 16-byte direct loads, one chunk ahead, and so
-// waits only for its own loads, never for the others. A row of a staged chunk
-// is 36 or 68 dwords, 4 mod 32, so the sixteen rows an operand read touches lie
-// in different banks. The activation operands of a chunk go from L2 to
+// Few rows a group: bound by the bytes of the weights. Workgroup (x, t) takes
+// 16 CT weight rows past one pass, up to 16 R rows of a group: a long group's
+// passes run side by side and share its weights in L2 (487 tokens, 2 of 32
+// experts unevenly, 1882 x 320: 37 us with one workgroup for all of a group's
+// passes, 27 so). Its four wavefronts deal the row's chunks of 8 blocks (256
+// elements: 144 or 272 bytes, whole 16-byte pieces; the last one may be short)
+// among themselves; each stages its own chunk's raw bytes in its own LDS by
+// 16-byte direct loads (rows need dword alignment only: K % 64 == 0), one chunk
+// ahead, and so waits only for its own loads, never for the others. A row of a
+// staged chunk is 36 or 68 dwords, 4 mod 32, so the sixteen rows an operand read
+// touches lie in different banks. The activation operands of a chunk go from L2 to
 // registers (they are the wavefront's own: no other reads that chunk), once
 // for all 16 CT weight rows. The partial tiles are added through LDS. Four
 // wavefronts, so that two workgroups share a compute unit and one streams while
@@ -160,7 +163,45 @@ struct FewLds {
         u32x4 w[kFewWaves][2][FewGeom<F, CT>::kStage];
         f32x4 red[kFewWaves][R * CT][64];
     };
+    int row[64], exp[64];   // of the 16 R rows
 };
+
+// Pass t over the groups one after another, 16 R rows a pass (the last of a
+// group shorter): its group, its positions from lo on (hi: the group's end) and
+// its first 16-row tile. M <= 32 G here: the sums stay small whatever the lists
+// hold.
+struct FewPass {
+    int e, lo, hi, tile;
+};
+
+__device__ __forceinline__ FewPass find_pass(const Groups &gr, int t, int R)
+{
+    const int lane = threadIdx.x & 63;
+    int passes = 0, tiles = 0;   // of the groups before base
+    for (int base = 0; base < gr.G; base += 64) {
+        int lo = 0, hi = 0;
+        if (base + lane < gr.G)
+            group_bounds(gr, base + lane, lo, hi);
+        const int mine = (hi - lo + 15) / 16, my_passes = (mine + R - 1) / R;
+        int st = mine, sp = my_passes;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int vt = __shfl_up(st, d), vp = __shfl_up(sp, d);
+            if (lane >= d)
+                st += vt, sp += vp;
+        }
+        const uint64_t past = __ballot(passes + sp > t);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int k = t - passes - __builtin_amdgcn_readlane(sp - my_passes, l);
+            return {base + l, __builtin_amdgcn_readlane(lo, l) + k * 16 * R, __builtin_amdgcn_readlane(hi, l),
+                    tiles + __builtin_amdgcn_readlane(st - mine, l) + k * R};
+        }
+        passes += __builtin_amdgcn_readlane(sp, 63);
+        tiles += __builtin_amdgcn_readlane(st, 63);
+    }
+    return {-1, 0, 0, 0};
+}
 
 template <class F, bool HO, int CT, int R>
 __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__restrict__ ops,
@@ -172,16 +213,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     using G = FewGeom<F, CT>;
     constexpr int TERMS = HO ? 1 : 2;
     __shared__ FewLds<F, HO, CT, R> lds;
-    const int e = blockIdx.y;
-    int lo, hi;
-    group_bounds(gr, e, lo, hi);
-    if (lo >= hi)
+    const FewPass at = find_pass(gr, blockIdx.y, R);
+    if (at.e < 0 || at.tile >= gr.tiles)
         return;
-    int tile = group_tiles_before(gr, e, 16);
+    const int e = at.e, lo = at.lo, hi = at.hi, tile = at.tile;
+    const int subs = min(min(R, (hi - lo + 15) / 16), gr.tiles - tile);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, g = lane >> 4;
-    const int nblk = K >> 5, chunks = K / (32 * kFewBlocks);
+    const int nblk = K >> 5, chunks = (nblk + kFewBlocks - 1) / kFewBlocks;
     const int n0 = blockIdx.x * G::kRows;
     const uint32_t row_bytes = (uint32_t)nblk * F::kBytes;
     const int wrows = min(G::kRows, N - n0);
@@ -196,6 +236,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
         const int row = t / G::kPieces;
         off[j] = (uint32_t)min(row, wrows - 1) * row_bytes + 16u * (uint32_t)(t - row * G::kPieces);
     }
+    // M <= 32 G rows here, and gr.tiles tiles of 16 exponents.
+    const __amdgpu_buffer_rsrc_t orders = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)gr.order, (short)0, gr.order ? gr.M * 4 : 0, kBufferRsrcWord3);
+    const __amdgpu_buffer_rsrc_t exps = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)row_exp, (short)0, gr.tiles * 64, kBufferRsrcWord3);
     const uint32_t magic = magic_vgpr<F>();
     auto issue = [&](int c, int buf) __attribute__((always_inline)) {
 #pragma unroll
@@ -206,93 +251,99 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     const f16x8 scale = {sc, sc, sc, sc, sc, sc, sc, sc};
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
 
-    // (Right lists end at gr.tiles by themselves.)
-    for (; lo < hi && tile < gr.tiles; lo += 16 * R, tile += R) {
-        const int subs = min(min(R, (hi - lo + 15) / 16), gr.tiles - tile);
-        f32x4 acc[R][CT];
+    f32x4 acc[R][CT];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-                acc[r][ct] = zero4;
-        const int last = chunks - 1;
-        if (wave < chunks) {
-            issue(wave, 0);
-            int buf = 0;
-            for (int c = wave; c < chunks; c += kFewWaves, buf ^= 1) {
-                // This chunk's operands, then the next chunk's bytes: waiting for
-                // the operands leaves those in flight. Past the last chunk the
-                // last one is read again, into the buffer nobody reads.
-                f16x8 aop[R][TERMS][kFewBlocks];
+        for (int ct = 0; ct < CT; ++ct)
+            acc[r][ct] = zero4;
+    // The rows of y and their exponents arrive while the weights stream (37
+    // tokens, 2 of 8 experts, 14336 x 4096, Q4_0: 96 us when they are read one
+    // by one behind the last chunk, 93 so).
+    if (wave == 0) {
+        const uint32_t i = (uint32_t)lane * 4u;
+        if (gr.order)
+            load4_to_lds(orders, lds.row, i, lo * 4);
+        load4_to_lds(exps, lds.exp, lane < 16 * subs ? i : 0u, tile * 64);
+    }
+    const int last = chunks - 1;
+    if (wave < chunks) {
+        issue(wave, 0);
+        int buf = 0;
+        // This chunk's operands, then the next chunk's bytes: waiting for
+        // the operands leaves those in flight. Past the last chunk the
+        // last one is read again, into the buffer nobody reads.
+        auto chunk = [&](auto full_c, int c) __attribute__((always_inline)) {
+            constexpr bool full = decltype(full_c)::value;
+            const int left = nblk - c * kFewBlocks;   // blocks of a short last chunk
+            f16x8 aop[R][TERMS][kFewBlocks];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const u32x4 *src = ops + ((size_t)(tile + min(r, subs - 1)) * nblk + c * kFewBlocks) * (TERMS * 64) + lane;
+            for (int r = 0; r < R; ++r) {
+                const u32x4 *src = ops + ((size_t)(tile + min(r, subs - 1)) * nblk + c * kFewBlocks) * (TERMS * 64) + lane;
 #pragma unroll
-                    for (int b = 0; b < kFewBlocks; ++b)
+                for (int b = 0; b < kFewBlocks; ++b)
 #pragma unroll
-                        for (int h = 0; h < TERMS; ++h)
-                            aop[r][h][b] = bitcast<f16x8>(src[(b * TERMS + h) * 64]);
-                }
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));   // the other buffer has been read
-                issue(min(c + kFewWaves, last), buf ^ 1);
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(G::kLoads));
-                asm volatile("" ::: "memory");
-                const uint32_t *base = reinterpret_cast<const uint32_t *>(lds.w[wave][buf]) + li * (G::kRowBytes / 4);
-                auto block = [&](auto b_c) __attribute__((always_inline)) {
-                    constexpr int b = decltype(b_c)::value;
+                    for (int h = 0; h < TERMS; ++h)
+                        aop[r][h][b] = bitcast<f16x8>(src[((full ? b : min(b, left - 1)) * TERMS + h) * 64]);
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));   // the other buffer has been read
+            issue(min(c + kFewWaves, last), buf ^ 1);
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(G::kLoads));
+            asm volatile("" ::: "memory");
+            const uint32_t *base = reinterpret_cast<const uint32_t *>(lds.w[wave][buf]) + li * (G::kRowBytes / 4);
+            unroll<kFewBlocks>([&](auto b_c) __attribute__((always_inline)) {
+                constexpr int b = decltype(b_c)::value;
+                if (!full && b >= left)
+                    return;
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const uint32_t *row = base + ct * 16 * (G::kRowBytes / 4);
-                        uint32_t x[F::kQsDwords];
-                        read_qs<F, b>(row, g, x);
-                        const float d = f16_bits_to_f32(read_d_bits<F, b>(row));
-                        const f16x8 q = F::decode(x, magic);
+                for (int ct = 0; ct < CT; ++ct) {
+                    const uint32_t *row = base + ct * 16 * (G::kRowBytes / 4);
+                    uint32_t x[F::kQsDwords];
+                    read_qs<F, b>(row, g, x);
+                    const float d = f16_bits_to_f32(read_d_bits<F, b>(row));
+                    const f16x8 q = F::decode(x, magic);
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            f32x4 s = zero4;
-                            if constexpr (!HO)
-                                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][1][b], q * scale, s, 0, 0, 0);
-                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][0][b], q, s, 0, 0, 0);
+                    for (int r = 0; r < R; ++r) {
+                        f32x4 s = zero4;
+                        if constexpr (!HO)
+                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][1][b], q * scale, s, 0, 0, 0);
+                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(aop[r][0][b], q, s, 0, 0, 0);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[r][ct][i] = fmaf(d, s[i], acc[r][ct][i]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            acc[r][ct][i] = fmaf(d, s[i], acc[r][ct][i]);
                     }
-                };
-                block(std::integral_constant<int, 0>{});
-                block(std::integral_constant<int, 1>{});
-                block(std::integral_constant<int, 2>{});
-                block(std::integral_constant<int, 3>{});
-                block(std::integral_constant<int, 4>{});
-                block(std::integral_constant<int, 5>{});
-                block(std::integral_constant<int, 6>{});
-                block(std::integral_constant<int, 7>{});
-            }
+                }
+            });
+            buf ^= 1;
+        };
+        for (int c = wave; c < chunks; c += kFewWaves) {
+            if (c < chunks - 1 || nblk % kFewBlocks == 0)
+                chunk(std::true_type{}, c);
+            else
+                chunk(std::false_type{}, c);
         }
-        // Every load has landed before its LDS serves the partial tiles.
-        ring_barrier<0>();
+    }
+    // Every load has landed before its LDS serves the partial tiles.
+    ring_barrier<0>();
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-                lds.red[wave][r * CT + ct][lane] = acc[r][ct];
-        __syncthreads();
-        for (int i = wave; i < R * CT; i += kFewWaves) {
-            const int r = i / CT, ct = i % CT, n = n0 + ct * 16 + li;
-            f32x4 v = lds.red[0][i][lane];
+        for (int ct = 0; ct < CT; ++ct)
+            lds.red[wave][r * CT + ct][lane] = acc[r][ct];
+    __syncthreads();
+    for (int i = wave; i < R * CT; i += kFewWaves) {
+        const int r = i / CT, ct = i % CT, n = n0 + ct * 16 + li;
+        f32x4 v = lds.red[0][i][lane];
 #pragma unroll
-            for (int s = 1; s < kFewWaves; ++s)
-                v += lds.red[s][i][lane];
+        for (int s = 1; s < kFewWaves; ++s)
+            v += lds.red[s][i][lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at = lo + 16 * r + 4 * g + q;
-                const int row = at < hi && r < subs ? group_row(gr, at) : -1;
-                if (row >= 0 && n < N)
-                    y[(size_t)row * (size_t)N + n] = ldexpf(v[q], -row_exp[(size_t)(tile + r) * 16 + 4 * g + q]);
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int j = 16 * r + 4 * g + q, row = gr.order ? lds.row[j] : lo + j;
+            if (r < subs && lo + j < hi && (unsigned)row < (unsigned)gr.M && n < N)
+                y[(size_t)row * (size_t)N + n] = ldexpf(v[q], -lds.exp[j]);
         }
-        __syncthreads();
     }
 }
 
@@ -342,7 +393,7 @@ static hipError_t launch_few(const u32x4 *ops, const int *row_exp, const uint8_t
                              int N, int K, const Groups &gr, hipStream_t s)
 {
     static_assert(sizeof(FewLds<F, BF, CT, R>) <= (size_t)kLdsBytes, "the stages fit in LDS");
-    return launch_kernel(k_grouped_few<F, BF, CT, R>, dim3((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)gr.G),
+    return launch_kernel(k_grouped_few<F, BF, CT, R>, dim3((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)q4v::group_row_tiles(gr.G, gr.M, 16 * R)),
                          dim3(64 * kFewWaves), 0, s, ops, row_exp, w, y, N, K, gr);
 }
 

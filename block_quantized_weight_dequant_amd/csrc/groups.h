@@ -87,22 +87,6 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
     return {-1, 0, 0, 0, 0, 0};
 }
 
-// Row tiles of bm rows in the groups before group e, by one wavefront; at most
-// gr.tiles.
-__device__ __forceinline__ int group_tiles_before(const Groups &gr, int e, int bm)
-{
-    int sum = 0;
-    for (int i = threadIdx.x & 63; i < e; i += 64) {
-        int lo, hi;
-        group_bounds(gr, i, lo, hi);
-        sum = min(sum + (hi - lo + bm - 1) / bm, gr.tiles);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        sum = min(sum + __shfl_xor(sum, d), gr.tiles);
-    return sum;
-}
-
 // Workgroups go to the eight XCDs in turn: tile index of workgroup L such that
 // each XCD takes runs of eight consecutive tiles (which share weight columns
 // in its L2) without the total being known.

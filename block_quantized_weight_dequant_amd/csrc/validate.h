@@ -183,13 +183,12 @@ inline long long group_row_tiles(long long G, long long M, long long bm)
 }
 
 // The grouped product's form. few: 16-row tiles streamed past the weights, for
-// groups of at most 32 rows on average; it needs 16-byte aligned weight rows
-// (K % 256 == 0) and keeps a wavefront's chain of block partials at 112 or
-// fewer (K <= 14336: 448 blocks dealt to four), as the GEMM's segments do.
-// Otherwise 128-row tiles of the GEMM's split kernel.
+// groups of at most 32 rows on average; it keeps a wavefront's chain of block
+// partials at 112 or fewer (K <= 14336: 448 blocks dealt to four), as the GEMM's
+// segments do. Otherwise 128-row tiles of the GEMM's split kernel.
 inline bool grouped_few(int G, int M, int K)
 {
-    return K % 256 == 0 && K <= 14336 && (long long)M <= 32LL * G;
+    return K <= 14336 && (long long)M <= 32LL * G;
 }
 
 // Up to 8 rows are multiplied in place, each by the streaming GEMV kernel with

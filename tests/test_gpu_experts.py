@@ -152,6 +152,9 @@ CASES = [
     ([200, 129], 257, 1088, 2, 0),
     ([30, 20, 25], 40, 512, 1, 0),
     ([1] * 70, 20, 256, 1, 0),
+    ([33, 0, 2, 15], 70, 704, 1, 2),
+    ([0] * 20 + [90] + [1] * 10, 130, 1088, 2, 1),
+    ([7, 30], 300, 64, 1, 0),
     ([0] * 100 + [9] + [0] * 30 + [4], 40, 512, 1, 0),
 ]
 
