@@ -168,8 +168,8 @@ struct FewLds {
 
 // Pass t over the groups one after another, 16 R rows a pass (the last of a
 // group shorter): its group, its positions from lo on (hi: the group's end) and
-// its first 16-row tile. M <= 32 G here: the sums stay small whatever the lists
-// hold.
+// its first 16-row tile. At most 2^15 tiles a group here: the sums stay small
+// whatever the lists hold.
 struct FewPass {
     int e, lo, hi, tile;
 };
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
         const int row = t / G::kPieces;
         off[j] = (uint32_t)min(row, wrows - 1) * row_bytes + 16u * (uint32_t)(t - row * G::kPieces);
     }
-    // M <= 32 G rows here, and gr.tiles tiles of 16 exponents.
+    // At most 2^19 rows here, and gr.tiles tiles of 16 exponents.
     const __amdgpu_buffer_rsrc_t orders = __builtin_amdgcn_make_buffer_rsrc(
         (void *)gr.order, (short)0, gr.order ? gr.M * 4 : 0, kBufferRsrcWord3);
     const __amdgpu_buffer_rsrc_t exps = __builtin_amdgcn_make_buffer_rsrc(
@@ -404,11 +404,11 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     if (q4v::grouped_in_place(gr.M, N, K, F::kBytes, BF ? 2 : 4))
         return gemv_rows_line_aligned<F>(w, K) ? launch_grouped_gemv<F, BF, true>(a, w, y, N, K, gr, s)
                                                : launch_grouped_gemv<F, BF, false>(a, w, y, N, K, gr, s);
-    const bool few = q4v::grouped_few(gr.G, gr.M, K);
+    const bool few = q4v::grouped_few(gr.G, gr.M, N, K);
     const int bm = few ? 16 : 128, nblk = K >> 5;
     const long long tiles = q4v::group_row_tiles(gr.G, gr.M, bm);
     int *row_exp = static_cast<int *>(workspace);
-    u32x4 *ops = reinterpret_cast<u32x4 *>(static_cast<char *>(workspace) + q4v::grouped_exp_bytes(gr.G, gr.M, K));
+    u32x4 *ops = reinterpret_cast<u32x4 *>(static_cast<char *>(workspace) + q4v::grouped_exp_bytes(gr.G, gr.M, N, K));
     const long long groups = tiles * (bm / 16);
     const int part = prep_part_blocks(groups, nblk, 1);
     hipError_t e = launch_kernel(few ? k_grouped_prep<F, BF, 16> : k_grouped_prep<F, BF, 128>,
@@ -422,7 +422,7 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
         const long long hit = gr.G < gr.M ? gr.G : gr.M;
         const bool two = gr.M > 16LL * hit;   // more than 16 rows a group on average
         constexpr int CTL = F::kBytes == kQ8Bytes ? 2 : 4;
-        if (hit * N >= 512LL * 16 * CTL)
+        if (q4v::grouped_passes(gr.G, gr.M, two ? 2 : 1) * N >= 512LL * 16 * CTL)
             return two ? launch_few<F, BF, CTL, 2>(ops, row_exp, w, y, N, K, gr, s)
                        : launch_few<F, BF, CTL, 1>(ops, row_exp, w, y, N, K, gr, s);
         return launch_few<F, BF, 1, 1>(ops, row_exp, w, y, N, K, gr, s);
@@ -448,7 +448,7 @@ hipError_t launch_gemm_grouped(WeightFormat fmt, bool bf16, const void *a, const
                                const int *offsets, const int *order, int share, float *y, int G,
                                int M, int N, int K, void *workspace, hipStream_t s)
 {
-    const int bm = q4v::grouped_few(G, M, K) ? 16 : 128;
+    const int bm = q4v::grouped_few(G, M, N, K) ? 16 : 128;
     const Groups gr = {offsets, order, G, M, share, (int)q4v::group_row_tiles(G, M, bm)};
     if (fmt == WeightFormat::kQ8_0)
         return bf16 ? launch_grouped_f<FmtQ8_0, true>(a, w, y, N, K, gr, workspace, s)

@@ -317,11 +317,11 @@ size_t grouped_workspace_bytes(int G, int M, int N, int K, size_t block_bytes, s
     if (check_group_shape(G, M, N, K, 64, 1 << 22, 1) != Q4_OK || M == 0 || N == 0 ||
         grouped_in_place(M, N, K, block_bytes, a_elem))
         return 0;
-    const int bm = grouped_few(G, M, K) ? 16 : 128;
+    const int bm = grouped_few(G, M, N, K) ? 16 : 128;
     size_t n = (size_t)group_row_tiles(G, M, bm) * (size_t)bm;   // below 2^39
     if (!mul_ok(n, (size_t)K, &n) || !mul_ok(n, a_elem, &n))
         return SIZE_MAX;
-    const size_t e = grouped_exp_bytes(G, M, K);
+    const size_t e = grouped_exp_bytes(G, M, N, K);
     return n > SIZE_MAX - e ? SIZE_MAX : n + e;
 }
 

@@ -182,13 +182,31 @@ inline long long group_row_tiles(long long G, long long M, long long bm)
     return M / bm + (G < M ? G : M);
 }
 
-// The grouped product's form. few: 16-row tiles streamed past the weights, for
-// groups of at most 32 rows on average; it keeps a wavefront's chain of block
-// partials at 112 or fewer (K <= 14336: 448 blocks dealt to four), as the GEMM's
-// segments do. Otherwise 128-row tiles of the GEMM's split kernel.
-inline bool grouped_few(int G, int M, int K)
+// Passes of the grouped product's few-row form over its 16 R rows at a time,
+// where the sizes of the groups (min(G, M) at most) are not known: a group ends
+// within a pass, half filled on average.
+inline long long grouped_passes(long long G, long long M, int R)
 {
-    return K <= 14336 && (long long)M <= 32LL * G;
+    const long long hit = G < M ? G : M, n = M / (16 * R) + hit / 2;
+    return n > hit ? n : hit;
+}
+
+// The grouped product's form. few: passes of up to 32 rows streamed past 64
+// weight rows each. Otherwise 128 x 256 tiles of the GEMM's split kernel. By
+// their times with the chip full and, where there are not enough of them for
+// that, alone, in us at K = 4096 with bfloat16 activations (f32: 1.8 times each):
+// a tile 1/3, at least 45; a pass 1/19 (256 tokens, 2 of 8 experts: 1024 x 1024
+// 15.6 us by passes and 24.7 by tiles, 2048 x 2048 28 and 36, 4096 x 4096 70 and
+// 59). few keeps a wavefront's chain of block partials at 112 or fewer (K <=
+// 14336: 448 blocks dealt to four), as the GEMM's segments do, and its passes
+// within a grid's second dimension.
+inline bool grouped_few(int G, int M, int N, int K)
+{
+    if (K > 14336 || M > 1 << 19)
+        return false;
+    const long long hit = G < M ? G : M, half = M / 128 + hit / 2, tm = half > hit ? half : hit;
+    const long long tiles = tm * (((long long)N + 255) / 256), passes = grouped_passes(G, M, 2) * (((long long)N + 63) / 64);
+    return passes * 3 <= 19 * (tiles > 135 ? tiles : 135);
 }
 
 // Up to 8 rows are multiplied in place, each by the streaming GEMV kernel with
@@ -202,9 +220,9 @@ inline bool grouped_in_place(int M, int N, int K, size_t block_bytes, size_t a_e
 // element (two of f32 activations, one of bfloat16). 0 in place, and for invalid
 // or empty shapes; SIZE_MAX on overflow.
 size_t grouped_workspace_bytes(int G, int M, int N, int K, size_t block_bytes, size_t a_elem);
-inline size_t grouped_exp_bytes(int G, int M, int K)
+inline size_t grouped_exp_bytes(int G, int M, int N, int K)
 {
-    const int bm = grouped_few(G, M, K) ? 16 : 128;
+    const int bm = grouped_few(G, M, N, K) ? 16 : 128;
     return ((size_t)group_row_tiles(G, M, bm) * (size_t)bm * 4 + 255) / 256 * 256;
 }
 

@@ -509,10 +509,10 @@ int q8_gemm_grouped_bf16(const uint16_t *a, const void *w_q, size_t w_bytes, con
  * q4_gemm_grouped_workspace_bytes and its kin — the row exponents and operands
  * of the groups' row tiles. 0 (NULL allowed) for M <= 8 rows where K % 256 == 0
  * and one W[e] and one row of a are below 2^31 bytes: those are multiplied in
- * place. Else, with bm = 16 when K <= 14336 and M <= 32 G, else 128, and R =
- * (M / bm + min(G, M)) * bm rows: R * 4 bytes padded to 256, then R * K * 4
- * (f32) or R * K * 2 (bfloat16). 0 for invalid or empty shapes, SIZE_MAX on
- * overflow. Pure functions of their arguments.
+ * place. Else, with row tiles of bm = 16 or 128 rows, as the library chooses for
+ * the shape, and R = (M / bm + min(G, M)) * bm rows: R * 4 bytes padded to 256,
+ * then R * K * 4 (f32) or R * K * 2 (bfloat16). 0 for invalid or empty shapes,
+ * SIZE_MAX on overflow. Pure functions of their arguments.
  */
 size_t q4_gemm_grouped_workspace_bytes(int G, int M, int N, int K);
 size_t q4_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K);

@@ -67,7 +67,10 @@ def test_grouped_workspace_bytes(f, act):
     assert ws(8, 2, big, 256) == 0
     assert ws(8, 2, big + 1, 256) == pad(2 * 16 * 4) + 2 * 16 * 256 * e
     assert ws(8, 256, 64, 4096) == pad(24 * 16 * 4) + 24 * 16 * 4096 * e
-    assert ws(8, 257, 64, 4096) == pad(10 * 128 * 4) + 10 * 128 * 4096 * e
+    assert ws(8, 257, 14336, 4096) == pad(24 * 16 * 4) + 24 * 16 * 4096 * e
+    assert ws(8, 400, 14336, 4096) == pad(11 * 128 * 4) + 11 * 128 * 4096 * e     # more rows of many columns: 128-row tiles
+    assert ws(8, 400, 64, 4096) == pad(33 * 16 * 4) + 33 * 16 * 4096 * e          # of few columns
+    assert ws(1, 2 ** 19 + 128, 64, 64) == pad(4098 * 128 * 4) + 4098 * 128 * 64 * e
     assert ws(8, 2, 64, 64) == pad(2 * 16 * 4) + 2 * 16 * 64 * e                  # K % 256 != 0: not in place
     assert ws(8, 9, 64, 14336) == pad(8 * 16 * 4) + 8 * 16 * 14336 * e
     assert ws(8, 9, 64, 14592) == pad(8 * 128 * 4) + 8 * 128 * 14592 * e          # past 112 blocks a wavefront: 128-row tiles
