@@ -421,8 +421,9 @@ static hipError_t launch_few(const u32x4 *ops, const int *row_exp, const uint8_t
                              int N, int K, const Groups &gr, hipStream_t s)
 {
     static_assert(sizeof(FewLds<F, BF, CT, R>) <= (size_t)kLdsBytes, "the stages fit in LDS");
-    return launch_kernel(k_grouped_few<F, BF, CT, R>, dim3((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)q4v::group_row_tiles(gr.G, gr.M, 16 * R)),
-                         dim3(64 * kFewWaves), 0, s, ops, row_exp, w, y, N, K, gr);
+    const dim3 grid((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)q4v::group_row_tiles(gr.G, gr.M, 16 * R));
+    return launch_kernel(k_grouped_few<F, BF, CT, R>, grid, dim3(64 * kFewWaves), 0, s, ops, row_exp, w, y, N,
+                         K, gr);
 }
 
 template <class F, bool BF>
