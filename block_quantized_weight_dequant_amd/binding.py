@@ -129,32 +129,33 @@ def _load_library():
 
 lib = _load_library()
 
+import torch  # noqa: E402  (loaded above, before libq4.so)
+
 
 def _addr(x) -> int:
     """Device address of a tensor argument (an int is taken as an address).
     Host tensors are refused here: the kernels would fault on a host pointer."""
     if x is None:
         return 0
+    if getattr(x, "is_cuda", False):
+        return x.data_ptr()
     if isinstance(x, int):
         return x
-    if not getattr(x, "is_cuda", False):
-        raise ValueError("expected a device (cuda) tensor, got one on %s" % getattr(x, "device", type(x)))
-    return int(x.data_ptr())
+    raise ValueError("expected a device (cuda) tensor, got one on %s" % getattr(x, "device", type(x)))
 
 
 def _nbytes(x) -> int:
-    return int(x.numel() * x.element_size())
+    return x.nbytes
 
 
 def _stream(stream) -> int:
     if stream is None:
         # Before PyTorch has initialised the GPU its current stream is the
-        # default one. The raw handle costs 0.3 us a call, against 3.5 us
+        # default one. The raw handle costs 0.2 us a call, against 3.5 us
         # through a torch.cuda.Stream object.
-        import torch
         if not torch.cuda.is_initialized():
             return 0
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
