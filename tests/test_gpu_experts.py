@@ -370,6 +370,42 @@ def test_expert_layer_eager_and_captured(T, E, k, H, D):
         check_grouped("f8", cap["y"].float().cpu().numpy().astype(np.float64), ref, P, there, H, "down")
 
 
+@pytest.mark.parametrize("fmt,act", FORMS)
+@pytest.mark.parametrize("T,N,K", [(3, 300, 512), (37, 520, 1088), (300, 2048, 512)])
+def test_grouped_calls_on_several_streams_at_once(fmt, act, T, N, K):
+    # Each call has its own workspace, from the allocator's pool of the stream it
+    # runs on; the weights, lists and activations are shared.
+    E, k = 6, 2
+    S = T * k
+    a, _ = activations(act, T, K, 31)
+    w, _ = weights(fmt, E, N, K, 700)
+    rng = np.random.default_rng(T)
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].reshape(-1)
+    off = to_dev(np.searchsorted(np.sort(ids), np.arange(E + 1)).astype(np.int32))
+    order = to_dev(np.argsort(ids, kind="stable").astype(np.int32))
+    if fmt == "f8":
+        args = [to_dev(t) for t in (a[0], a[1], w[0], w[1])]
+        f, dtype = q4.f8_gemm_grouped, torch.bfloat16
+    else:
+        args = [to_dev(a), to_dev(w)]
+        f, dtype = getattr(q4, fmt + "_gemm_grouped" + ("_bf16" if act == "bf16" else "")), torch.float32
+    y = torch.empty(S, N, dtype=dtype, device=DEV)
+    f(*args, off, order, y, E, S, N, K, share=k)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(3)], []
+    for i in range(9):
+        s, out = streams[i % 3], torch.zeros(S, N, dtype=dtype, device=DEV)
+        s.wait_stream(torch.cuda.current_stream())
+        if i % 2:
+            with torch.cuda.stream(s):
+                f(*args, off, order, out, E, S, N, K, share=k)
+        else:
+            f(*args, off, order, out, E, S, N, K, share=k, stream=s)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, y) for out in outs)
+
+
 @pytest.mark.parametrize("fmt,act", [("q4", "bf16"), ("q8", "f32")])
 @pytest.mark.parametrize("T", [3, 200])
 def test_routed_block_quantized_products_captured(fmt, act, T):
