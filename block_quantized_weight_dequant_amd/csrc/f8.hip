@@ -720,18 +720,19 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     };
 
     // The pipeline. Step s multiplies stage s mod NS. Its weight operands, its
-    // first activation operand and its scales are in registers when it begins.
-    // At kTurn every wavefront has read the last of the stage (the wait and the
-    // barrier) and the next stage has landed: the step's last column of tiles
-    // runs from registers while each weight operand that it has used is read
-    // again from the next stage, and the loads of step s + NS begin to fill the
-    // stage just left; they are spread into the next step, since a burst of
-    // them from every wavefront at once stalls the issue of all. No step begins by waiting for LDS. Tile t's FMAs follow
-    // matrix instruction t + kLag, when its result is ready. The group barriers
-    // keep that order; the empty asm keeps the FMAs where they are written.
-    // The last kLag tiles' FMAs of a step run in the next one (kCarry), which
-    // then begins with matrix instructions; not in the large form, whose
-    // registers are all taken, and where they are a sixteenth of the tiles.
+    // first activation operand and its scales are in registers when it begins, so
+    // no step begins by waiting for LDS. At kTurn every wavefront has read the
+    // last of the stage (the wait and the barrier) and the next stage has landed:
+    // the step's last column of tiles runs from registers while each weight
+    // operand that it has used is read again from the next stage, and the loads
+    // of step s + NS begin to fill the stage just left; they are spread into the
+    // next step, since a burst of them from every wavefront at once stalls the
+    // issue of all. Tile t's FMAs follow matrix instruction t + kLag, when its
+    // result is ready. The group barriers keep that order; the empty asm keeps
+    // the FMAs where they are written. The last kLag tiles' FMAs of a step run in
+    // the next one (kCarry), which then begins with matrix instructions; not in
+    // the large form, whose registers are all taken, and where they are a
+    // sixteenth of the tiles.
     constexpr int kLag = 2, kRing = 4;
     constexpr bool kCarry = S::kTiles < 32;
     static_assert(S::kTiles % kRing == 0 && S::TN >= kLag, "results of two steps do not meet");
