@@ -7,6 +7,7 @@
 // ceil(K / 128)] (one per 128 x 128 tile), all row-major; a row's last block
 // may be short.
 #include <algorithm>
+#include <climits>
 
 #include "device_common.h"
 #include "groups.h"
@@ -461,15 +462,18 @@ __device__ __forceinline__ void rows_tile(const F8Product &p, const uint8_t *__r
     }
 }
 
+// Workgroup (x, t): weight rows 16 x .., activation rows 16 RG t ...
 template <class S>
 __global__ __launch_bounds__(S::kThreads) void k_f8_rows(F8Product p)
 {
     __shared__ RowsLds<S> lds;
+    const int m0 = blockIdx.y * (16 * S::RG), rows = min(16 * S::RG, p.M - m0);
+    p.a += (size_t)m0 * (size_t)p.K;
+    p.a_s += (size_t)m0 * (size_t)p.Kb;
     auto at = [&](int r) __attribute__((always_inline)) {
-        const int m = r < p.M ? r : -1;
-        return int2{m, m};
+        return r < rows ? int2{r, m0 + r} : int2{-1, -1};
     };
-    rows_tile<S>(p, p.w, p.w_s + (size_t)(blockIdx.x >> 3) * (size_t)p.Kb, (uint32_t)p.M, blockIdx.x * 16, at, lds);
+    rows_tile<S>(p, p.w, p.w_s + (size_t)(blockIdx.x >> 3) * (size_t)p.Kb, (uint32_t)rows, blockIdx.x * 16, at, lds);
 }
 
 // The same over groups: workgroup (x, e) takes 16 weight rows of group e past
@@ -933,7 +937,8 @@ template <class S>
 static hipError_t launch_rows(const F8Product &p, hipStream_t st)
 {
     static_assert(sizeof(RowsLds<S>) <= 160 * 1024, "the rings fit in LDS");
-    return launch_kernel(k_f8_rows<S>, dim3((unsigned)(((long long)p.N + 15) / 16)), dim3(S::kThreads), 0, st, p);
+    const dim3 grid((unsigned)(((long long)p.N + 15) / 16), (unsigned)((p.M + 16LL * S::RG - 1) / (16 * S::RG)));
+    return launch_kernel(k_f8_rows<S>, grid, dim3(S::kThreads), 0, st, p);
 }
 
 template <class S>
@@ -965,17 +970,23 @@ static long long tile_cost(long long tiles_m, int N, int round)
     return (tiles_m * (((long long)N + S::BN - 1) / S::BN) + 255) / 256 * round;
 }
 
-// For `groups` groups with tiles_m(bm) row tiles of bm rows in all; rg: the
-// row groups of the few-row form, 0 if the groups are too long for it.
-template <class TilesM>
-static Form choose_form(long long groups, int rg, int N, TilesM tiles_m)
+// Rounds of the few-row form: `passes` times N / 16 workgroups, rg row groups each.
+static long long rows_cost(long long passes, int N, int rg)
 {
-    constexpr int kRowsRound[] = {0, 11, 12, 14, 19};
+    constexpr int kRound[] = {0, 11, 12, 14, 19};
+    return (passes * (((long long)N + 15) / 16) + 255) / 256 * kRound[rg];
+}
+
+// Over tiles_m(bm) row tiles of bm rows in all, of `groups` weight matrices;
+// rows: the cost of the few-row form.
+template <class TilesM>
+static Form choose_form(long long groups, long long rows, int N, TilesM tiles_m)
+{
     const long long cost[] = {tile_cost<TileQuarter>(tiles_m(64), N, 25), tile_cost<TileHalf>(tiles_m(64), N, 40),
                               tile_cost<TileSmall>(tiles_m(128), N, 70), tile_cost<TileWide>(tiles_m(128), N, 110),
                               tile_cost<TileLarge>(tiles_m(256), N, 190)};
     const long long least = *std::min_element(cost, cost + 5);
-    if (rg && (groups * (((long long)N + 15) / 16) + 255) / 256 * kRowsRound[rg] <= least)
+    if (rows <= least)
         return kRows;
     int i = 4;
     while (cost[i] > std::max(least, groups * N / 430))
@@ -987,8 +998,18 @@ hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, 
                           uint16_t *y, int M, int N, int K, hipStream_t st)
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
-    const int rg = M <= 64 ? (M + 15) / 16 : 0;
-    switch (choose_form(1, rg, N, [&](int bm) { return ((long long)M + bm - 1) / bm; })) {
+    // Row groups of the few-row form: the fewest at the least cost, so that few
+    // weight rows spread over more workgroups (64 x 1024 x 4096: 7.3 us by one
+    // pass of four row groups, 5.2 by four of one; 128 x 256 x 7168: 11.4 us in
+    // quarter tiles, 5.0 so).
+    int rg = 0;
+    long long rows = 0;
+    for (int i = 1; i <= 4; ++i) {
+        const long long passes = (M + 16LL * i - 1) / (16 * i), c = rows_cost(passes, N, i);
+        if (passes <= 65535 && (!rg || c < rows))
+            rg = i, rows = c;
+    }
+    switch (choose_form(1, rg ? rows : LLONG_MAX, N, [&](int bm) { return ((long long)M + bm - 1) / bm; })) {
     case kRows:
         return rg == 1 ? launch_rows<Rows1>(p, st) : rg == 2 ? launch_rows<Rows2>(p, st)
              : rg == 3 ? launch_rows<Rows3>(p, st) : launch_rows<Rows4>(p, st);
@@ -1022,7 +1043,8 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
     // half filled on average.
     const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit;
     const int rg = mean <= 8 ? 1 : mean <= 16 ? 2 : mean <= 32 ? 4 : 0;
-    switch (choose_form(hit, rg, N, [&](int bm) { return std::max(hit, M / bm + hit / 2); })) {
+    const long long rows = rg ? rows_cost(hit, N, rg) : LLONG_MAX;
+    switch (choose_form(hit, rows, N, [&](int bm) { return std::max(hit, M / bm + hit / 2); })) {
     case kRows:
         return rg == 1 ? launch_rows_grouped<Rows1>(p, gr, st) : rg == 2 ? launch_rows_grouped<Rows2>(p, gr, st)
              : launch_rows_grouped<Rows4>(p, gr, st);

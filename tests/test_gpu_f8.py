@@ -145,10 +145,11 @@ def test_values_past_a_short_block_do_not_count():
 
 
 @pytest.mark.parametrize("M,N,K", [(4096, 4100, 160), (3900, 4096, 1056), (1000, 4104, 288), (300, 14401, 672),
-                                   (700, 4100, 1312), (520, 4096, 32), (70, 14400, 1056), (100, 14402, 416), (64, 14336, 1184)])
+                                   (700, 4100, 1312), (520, 4096, 32), (70, 14400, 1056), (100, 14402, 416), (64, 14336, 1184),
+                                   (140, 3900, 416), (130, 2002, 1312), (250, 3008, 160)])
 def test_product_large_tiles(M, N, K):
-    # Enough rows and columns for each form of larger tiles (256 x 256, 256 x
-    # 128, 128 x 128, 128 x 64); the reference in f64 on the card.
+    # Enough rows and columns for each form of tiles (256 x 256, 256 x 128, 128 x
+    # 128, 128 x 64, 64 x 64); the reference in f64 on the card.
     g = torch.Generator(device=DEV).manual_seed(3)
     x, v = torch.randn(M, K, generator=g, device=DEV), torch.randn(N, K, generator=g, device=DEV)
     a, a_s = torch.empty(M, K, dtype=torch.uint8, device=DEV), torch.empty(M, pl.blocks(K), device=DEV)
