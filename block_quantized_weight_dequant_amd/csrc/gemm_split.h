@@ -513,8 +513,8 @@ __device__ __forceinline__ void gemm_split_body(
         // barrier ending step p the loads issued after the last one pair p + 2
         // needs may still be in flight: ring_in_flight counts them, one count
         // for even and one for odd p (near the end, where fewer are issued, the
-        // barrier waits for everything). The last step reads stages no load is
-        // writing any more, and discards what it read.
+        // barrier waits for everything). What the last step reads is discarded;
+        // the loads that it leaves in flight are waited for before the epilogue.
         constexpr int kInFlightEven = ring_in_flight(0, DA, LB, NAK, NBK);
         constexpr int kInFlightOdd = ring_in_flight(1, DA, LB, NAK, NBK);
         static_assert(kInFlightEven < 64 && kInFlightOdd < 64, "vmcnt counts to 63");
@@ -573,8 +573,12 @@ __device__ __forceinline__ void gemm_split_body(
     else
         run_group(std::integral_constant<int, 1>{});
 
-    // Group 1 hands its partial tile to group 0 through LDS (every load has
-    // landed and every wavefront has passed the last barrier):
+    // The last steps' reloads may still be on their way (a counted barrier
+    // leaves them in flight, and K group 1, which issued none, cannot wait for
+    // them): they land before any of the rings' LDS is written below.
+    ring_barrier<0>();
+
+    // Group 1 hands its partial tile to group 0 through LDS:
     // [wavefront of the group][value][lane].
     float *red = reinterpret_cast<float *>(&lds.a[0][0]);
     static_assert(sizeof(lds.a) >= 4 * 64 * 64 * sizeof(float), "reduction buffer");
