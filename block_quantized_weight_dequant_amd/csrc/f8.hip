@@ -73,14 +73,15 @@ struct Eight {
             // first to within a unit in the last place, the second to the
             // nearest (Markstein's theorem). No intermediate leaves the normal
             // range here but where the quotient is far below the smallest
-            // code, and no quotient rounds past 448. Five operations an
-            // element; a division takes about twice that.
+            // code, and no quotient rounds past 448. The remainder of -0 is
+            // +0, which would lose its sign: the quotient takes x's. Six
+            // operations an element; a division takes about twice that.
             const float r = 1.0f / s;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float q0 = v[i] * r;
                 const float q1 = fmaf(fmaf(-q0, s, v[i]), r, q0);
-                q[i] = fmaf(fmaf(-q1, s, v[i]), r, q1);
+                q[i] = __builtin_copysignf(fmaf(fmaf(-q1, s, v[i]), r, q1), v[i]);
             }
         } else {
 #pragma unroll

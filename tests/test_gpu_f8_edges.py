@@ -1,0 +1,44 @@
+"""Edges of the E4M3 quantizer on the GPU: signed zeros under scales of every
+size, against the plain form (plain_experts.py), bit for bit."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import plain_experts as pl  # noqa: E402
+from block_quantized_weight_dequant_amd import binding as q4  # noqa: E402
+from gpu_helpers import Guarded, f32_bits, to_dev  # noqa: E402
+
+
+def check_codes(x, block_rows, act):
+    M, K = x.shape
+    ref_q, ref_s = pl.quantize(x, block_rows)
+    q, s = Guarded(M * K, torch.uint8), Guarded(ref_s.size, torch.float32)
+    if act == "bf16":
+        bits = pl.bf16_bits(x)
+        assert np.array_equal(pl.bf16_value(bits).reshape(M, K), x)
+        q4.f8_quantize_bf16(to_dev(bits.view(np.int16)), q.view, s.view, M, K, block_rows)
+    else:
+        q4.f8_quantize(to_dev(x), q.view, s.view, M, K, block_rows)
+    torch.cuda.synchronize()
+    assert np.array_equal(f32_bits(s.host()), f32_bits(ref_s).reshape(-1))
+    assert np.array_equal(q.host().reshape(M, K), ref_q)
+    assert q.guards_intact() and s.guards_intact()
+    return ref_q
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 1.0, 2.0 ** 60, 2.0 ** 100])
+def test_quantize_keeps_the_sign_of_zero(block_rows, act, scale):
+    # -0 / s is -0, code 0x80, whatever the scale; so is a negative quotient
+    # that rounds to zero.
+    rng = np.random.default_rng(9)
+    x = rng.choice(np.float32([1.0, -0.5, 0.0, -0.0, 2.0 ** -20, -2.0 ** -20]), (9, 160)) * np.float32(scale)
+    x[:, 0] = scale
+    q = check_codes(x.astype(np.float32), block_rows, act)
+    assert (q == 0x80).any() and (q == 0).any()
