@@ -23,7 +23,9 @@ constexpr float kE4M3Max = 448.0f;
 // ---------------------------------------------------------------------------
 // Quantize. Per block: s = max|x| / 448 in f32, code = the E4M3 value nearest
 // to x / s (ties to even), the quotient rounded once to f32 and clamped to
-// +-448 (it can pass that only where s is subnormal); s == 0 stores zeros.
+// +-448; s == 0 stores zeros. s is rounded, so the largest quotient is often a
+// step past 448 (448 + 2^-15, one ordinary maximum in twelve), and farther only
+// where s is subnormal.
 // Bound by the bytes of x: 16 lanes share a block of a row, eight elements
 // each, so a wavefront reads four blocks (2 KB of f32) and writes 512 bytes
 // of codes in whole lines, and the maximum crosses 16 lanes in four DPP moves.
@@ -73,7 +75,8 @@ struct Eight {
             // first to within a unit in the last place, the second to the
             // nearest (Markstein's theorem). No intermediate leaves the normal
             // range here but where the quotient is far below the smallest
-            // code, and no quotient rounds past 448. The remainder of -0 is
+            // code. No clamp: 448 + 2^-15 at most, which the conversion rounds
+            // to 448 as it rounds all below 464. The remainder of -0 is
             // +0, which would lose its sign: the quotient takes x's. Six
             // operations an element; a division takes about twice that.
             const float r = 1.0f / s;

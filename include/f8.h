@@ -42,8 +42,10 @@ extern "C" {
  *               not overlap (Q4_ERR_ALIAS).
  * Per block: scale = max|x| / 448, rounded to f32; code = the E4M3 value
  * nearest to x / scale, ties to even, where the quotient is first rounded to
- * f32 and clamped to [-448, 448] (it passes 448 only for a subnormal scale).
- * A block whose scale is 0 stores codes 0. Bit-exact.
+ * f32 and clamped to [-448, 448] (the scale is rounded, so the largest quotient
+ * can be a step of f32 past 448; farther only for a subnormal scale). -0 and
+ * negative quotients that round to zero are 0x80. A block whose scale is 0
+ * stores codes 0. Bit-exact.
  */
 int f8_quantize(const float *x, int M, int K, int block_rows, void *q, size_t q_bytes, float *s,
                 size_t s_elems, void *stream);

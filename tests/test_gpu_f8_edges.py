@@ -1,5 +1,5 @@
 """Edges of the E4M3 quantizer on the GPU: signed zeros under scales of every
-size, against the plain form (plain_experts.py), bit for bit."""
+size and quotients a step past 448, against the plain form (plain_experts.py), bit for bit."""
 import numpy as np
 import pytest
 
@@ -42,3 +42,18 @@ def test_quantize_keeps_the_sign_of_zero(block_rows, act, scale):
     x[:, 0] = scale
     q = check_codes(x.astype(np.float32), block_rows, act)
     assert (q == 0x80).any() and (q == 0).any()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_of_maxima_a_step_past_448(block_rows):
+    # max / s in f32, s = max / 448 in f32, can be 448 + 2^-15 for ordinary
+    # scales: it is still the code of 448.
+    v = np.random.default_rng(10).uniform(1, 8, 4096).astype(np.float32)
+    v = np.concatenate([np.float32([1.921268, 3.9120002]), v])
+    past = v / (v / np.float32(448)) > 448
+    assert past[:2].all() and past.sum() > 100
+    v = v[past][:101]
+    x = np.zeros((101 * block_rows, 128), dtype=np.float32)
+    x[::block_rows, 3], x[::block_rows, 77] = v, -v
+    q = check_codes(x, block_rows, "f32")
+    assert (q[::block_rows, 3] == 0x7E).all() and (q[::block_rows, 77] == 0xFE).all()
