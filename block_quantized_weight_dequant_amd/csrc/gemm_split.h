@@ -2,6 +2,7 @@
 // plain GEMM (gemm.hip) and the products grouped by expert (grouped.hip).
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "device_common.h"
@@ -232,6 +233,9 @@ constexpr int ring_in_flight(int par, int da, int lb, int na, int nb)
     }
     return n;
 }
+
+// In row_exp, GROUPED: a tile row whose row of y another one stores.
+constexpr int kNotStored = INT_MIN;
 
 // One K segment of the product: ahl points at the operands of block kb0 of
 // the first row tile (a row tile holds nblk_row blocks of operands) and w at
@@ -600,7 +604,8 @@ __device__ __forceinline__ void gemm_split_body(
         static_assert(sizeof(lds.b) >= kGemmBM * sizeof(int2), "a row and an exponent each");
         const int r = tid - kSplitGemmThreads / 2;
         if (r >= 0 && r < kGemmBM)
-            rows[r] = pos0 + r < pos1 ? int2{group_row(gr, pos0 + r), row_exp[m0 + r]} : int2{-1, 0};
+            rows[r] = pos0 + r < pos1 && row_exp[m0 + r] != kNotStored
+                          ? int2{group_row(gr, pos0 + r), row_exp[m0 + r]} : int2{-1, 0};
     }
     __syncthreads();
     if (kg == 0) {

@@ -30,7 +30,8 @@ template <class F, bool BF, int BM>
 __global__ __launch_bounds__(64 * kPrepWaves) void k_grouped_prep(const void *__restrict__ a,
                                                                 Groups gr, int *__restrict__ row_exp,
                                                                 u32x4 *__restrict__ ops, int K,
-                                                                int part_blocks)
+                                                                int part_blocks, int *__restrict__ claims,
+                                                                int N)
 {
     __shared__ int s_p[16], s_row[16];
     __shared__ u32x4 s_tile[kPrepWaves][16 * 9];
@@ -53,8 +54,11 @@ __global__ __launch_bounds__(64 * kPrepWaves) void k_grouped_prep(const void *__
     if (lane == 0) {
         s_p[wave] = p;
         s_row[wave] = r;
-        if (blockIdx.y == 0)
+        if (blockIdx.y == 0) {
             row_exp[(size_t)t * BM + sub * 16 + wave] = p;
+            if (claims && r >= 0)
+                claims[(size_t)r * (size_t)N] = t * BM + sub * 16 + wave;
+        }
     }
     __syncthreads();
     // A unit is 128 bytes of each row. Eight lanes read a row's, whole lines,
@@ -125,6 +129,22 @@ __global__ __launch_bounds__(64 * kPrepWaves) void k_grouped_prep(const void *__
                 dst[SUBS * 64] = bitcast<u32x4>(lo);
         }
     }
+}
+
+// Where K is cut into segments, every launch after the first adds to y, so a row
+// that the lists name more than once must be one tile row's alone. Each tile
+// row leaves its number in its row of y in the preparation (the first element,
+// until the product stores there), and those whose number is not the one that
+// stayed are marked in row_exp: 4.6 us beside products of some hundred. Which
+// one stays is left open. Workgroup t: tile t.
+__global__ __launch_bounds__(kGemmBM) void k_grouped_resolve(Groups gr, const int *__restrict__ claims, int N,
+                                                            int *__restrict__ row_exp)
+{
+    const GroupTile gt = find_group_tile(gr, blockIdx.x, kGemmBM, 1);
+    const int p = gt.lo + gt.mt * kGemmBM + (int)threadIdx.x, j = (int)(blockIdx.x * kGemmBM + threadIdx.x);
+    const int r = gt.e >= 0 && p < gt.hi ? group_row(gr, p) : -1;
+    if (r >= 0 && claims[(size_t)r * (size_t)N] != j)
+        row_exp[j] = kNotStored;
 }
 
 template <class F, bool HO>
@@ -440,9 +460,11 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     u32x4 *ops = reinterpret_cast<u32x4 *>(static_cast<char *>(workspace) + q4v::grouped_exp_bytes(gr.G, gr.M, N, K));
     const long long groups = tiles * (bm / 16);
     const int part = prep_part_blocks(groups, nblk, BF ? 2 : 1);
+    const KSegments sg = few ? KSegments{1, nblk} : k_segments(nblk, 2);
+    int *claims = sg.n > 1 ? reinterpret_cast<int *>(y) : nullptr;
     hipError_t e = launch_kernel(few ? k_grouped_prep<F, BF, 16> : k_grouped_prep<F, BF, 128>,
                                  dim3((unsigned)groups, (unsigned)((nblk + part - 1) / part)),
-                                 dim3(64 * kPrepWaves), 0, s, a, gr, row_exp, ops, K, part);
+                                 dim3(64 * kPrepWaves), 0, s, a, gr, row_exp, ops, K, part, claims, N);
     if (e != hipSuccess)
         return e;
     if (few) {
@@ -460,7 +482,12 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     const long long grid = group_grid(gr.G, gr.M, kGemmBM, tn);
     if (grid > 0x7fffffffLL)
         return hipErrorInvalidValue;
-    const KSegments sg = k_segments(nblk, 2);
+    if (claims) {
+        e = launch_kernel(k_grouped_resolve, dim3((unsigned)tiles), dim3(kGemmBM), 0, s, gr,
+                          (const int *)claims, N, row_exp);
+        if (e != hipSuccess)
+            return e;
+    }
     for (int i = 0; i < sg.n; ++i) {
         const int kb0 = i * sg.len, nb = min(sg.len, nblk - kb0);
         e = launch_kernel(k_gemm_split_grouped<F, BF>, dim3((unsigned)grid), dim3(kSplitGemmThreads),
