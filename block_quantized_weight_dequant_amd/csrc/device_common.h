@@ -96,7 +96,9 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void *dst
 }
 
 // Launch a kernel and return the runtime's verdict on this launch alone. Each
-// argument is first converted to the kernel's own parameter type.
+// argument is first converted to the kernel's own parameter type. A grid
+// dimension holds fewer than 2^32 threads; past that the runtime can launch a
+// part of the grid and report success, so it is refused here.
 template <typename Kernel, typename Tuple, size_t... I>
 inline hipError_t launch_tuple(Kernel kernel, dim3 grid, dim3 block, size_t lds_bytes,
                                hipStream_t stream, Tuple &vals, std::index_sequence<I...>)
@@ -111,9 +113,26 @@ inline hipError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block
                                 hipStream_t stream, Args &&...args)
 {
     static_assert(sizeof...(Params) == sizeof...(Args), "argument count");
+    if ((uint64_t)grid.x * block.x > UINT32_MAX || (uint64_t)grid.y * block.y > UINT32_MAX ||
+        (uint64_t)grid.z * block.z > UINT32_MAX)
+        return hipErrorInvalidConfiguration;
     std::tuple<std::decay_t<Params>...> vals(std::forward<Args>(args)...);
     return launch_tuple(kernel, grid, block, lds_bytes, stream, vals,
                         std::index_sequence_for<Params...>{});
+}
+
+// A grid of any number of workgroups in x, 2^31 threads a launch (a multiple of
+// 64 workgroups): the kernel's last parameter is the index of its first one.
+template <typename... Params, typename... Args>
+inline hipError_t launch_parts(void (*kernel)(Params...), long long blocks, unsigned blocks_y,
+                               unsigned threads, hipStream_t stream, Args &&...args)
+{
+    const long long part = (1LL << 31) / threads / 64 * 64;
+    hipError_t e = hipSuccess;
+    for (long long first = 0; first < blocks && e == hipSuccess; first += part)
+        e = launch_kernel(kernel, dim3((unsigned)(blocks - first < part ? blocks - first : part), blocks_y),
+                          dim3(threads), 0, stream, args..., (int)first);
+    return e;
 }
 
 }  // namespace q4k

@@ -468,36 +468,37 @@ __device__ __forceinline__ void rows_tile(const F8Product &p, const uint8_t *__r
 
 // Workgroup (x, t): weight rows 16 x .., activation rows 16 RG t ...
 template <class S>
-__global__ __launch_bounds__(S::kThreads) void k_f8_rows(F8Product p)
+__global__ __launch_bounds__(S::kThreads) void k_f8_rows(F8Product p, int first)
 {
     __shared__ RowsLds<S> lds;
+    const int x = first + (int)blockIdx.x;
     const int m0 = blockIdx.y * (16 * S::RG), rows = min(16 * S::RG, p.M - m0);
     p.a += (size_t)m0 * (size_t)p.K;
     p.a_s += (size_t)m0 * (size_t)p.Kb;
     auto at = [&](int r) __attribute__((always_inline)) {
         return r < rows ? int2{r, m0 + r} : int2{-1, -1};
     };
-    rows_tile<S>(p, p.w, p.w_s + (size_t)(blockIdx.x >> 3) * (size_t)p.Kb, (uint32_t)rows, blockIdx.x * 16, at, lds);
+    rows_tile<S>(p, p.w, p.w_s + (size_t)(x >> 3) * (size_t)p.Kb, (uint32_t)rows, x * 16, at, lds);
 }
 
 // The same over groups: workgroup (x, e) takes 16 weight rows of group e past
 // the group's rows, 16 RG at a time.
 template <class S>
-__global__ __launch_bounds__(S::kThreads) void k_f8_rows_grouped(F8Product p, Groups gr)
+__global__ __launch_bounds__(S::kThreads) void k_f8_rows_grouped(F8Product p, Groups gr, int first)
 {
     __shared__ RowsLds<S> lds;
-    const int e = blockIdx.y;
+    const int e = blockIdx.y, x = first + (int)blockIdx.x;
     int lo, hi;
     group_bounds(gr, e, lo, hi);
     const uint8_t *w = p.w + (size_t)e * (size_t)p.N * (size_t)p.K;
-    const float *w_s = p.w_s + ((size_t)e * (size_t)p.Nb + (size_t)(blockIdx.x >> 3)) * (size_t)p.Kb;
+    const float *w_s = p.w_s + ((size_t)e * (size_t)p.Nb + (size_t)(x >> 3)) * (size_t)p.Kb;
     const uint32_t a_rows = (uint32_t)((gr.M - 1) / gr.share + 1);
     for (; lo < hi; lo += 16 * S::RG) {
         auto at = [&](int r) __attribute__((always_inline)) {
             const int y = lo + r < hi ? group_row(gr, lo + r) : -1;
             return int2{y < 0 ? -1 : y / gr.share, y};
         };
-        rows_tile<S>(p, w, w_s, a_rows, blockIdx.x * 16, at, lds);
+        rows_tile<S>(p, w, w_s, a_rows, x * 16, at, lds);
         __syncthreads();   // the partial tiles are read before the next rows' loads
     }
 }
@@ -581,9 +582,9 @@ struct TileOrder {
     int nx, rn, rm;
 };
 
-__device__ __forceinline__ bool tile_of(const TileOrder &o, int &nt, int &mt)
+__device__ __forceinline__ bool tile_of(const TileOrder &o, int L, int &nt, int &mt)
 {
-    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int x = L & 7, i = L >> 3;
     const int xn = x % o.nx, xm = x / o.nx;
     const int strip = i / (8 * o.rn), h = min(8, o.rm - 8 * strip), r = i - strip * 8 * o.rn;
     nt = xn * o.rn + r / h;
@@ -592,7 +593,7 @@ __device__ __forceinline__ bool tile_of(const TileOrder &o, int &nt, int &mt)
 }
 
 template <class S, bool GROUPED>
-__global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, TileOrder order)
+__global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr, TileOrder order, int first)
 {
     __shared__ TileLds<S> lds;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -601,7 +602,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
     const uint8_t *w = p.w;
     const float *w_s = p.w_s;
     if constexpr (GROUPED) {
-        const GroupTile g = find_group_tile(gr, xcd_runs(blockIdx.x), S::BM, order.tn);
+        const GroupTile g = find_group_tile(gr, xcd_runs(first + (int)blockIdx.x), S::BM, order.tn);
         if (g.e < 0)
             return;
         mt = g.mt, nt = g.nt;
@@ -613,7 +614,7 @@ __global__ __launch_bounds__(S::kThreads) void k_f8_tile(F8Product p, Groups gr,
             lds.row[tid] = tid < rows ? group_row(gr, lo + tid) : -1;
         __syncthreads();
     } else {
-        if (!tile_of(order, nt, mt))
+        if (!tile_of(order, first + (int)blockIdx.x, nt, mt))
             return;
         rows = min(S::BM, p.M - mt * S::BM);
     }
@@ -933,23 +934,22 @@ static hipError_t launch_tiles(const F8Product &p, hipStream_t st)
     }
     if (best * 8 > 0x7fffffffLL)
         return hipErrorInvalidValue;
-    return launch_kernel(k_f8_tile<S, false>, dim3((unsigned)(best * 8)), dim3(S::kThreads), 0, st, p,
-                         Groups{nullptr, nullptr, 0, 0, 1, 0}, o);
+    return launch_parts(k_f8_tile<S, false>, best * 8, 1, S::kThreads, st, p,
+                        Groups{nullptr, nullptr, 0, 0, 1, 0}, o);
 }
 
 template <class S>
 static hipError_t launch_rows(const F8Product &p, hipStream_t st)
 {
     static_assert(sizeof(RowsLds<S>) <= 160 * 1024, "the rings fit in LDS");
-    const dim3 grid((unsigned)(((long long)p.N + 15) / 16), (unsigned)((p.M + 16LL * S::RG - 1) / (16 * S::RG)));
-    return launch_kernel(k_f8_rows<S>, grid, dim3(S::kThreads), 0, st, p);
+    return launch_parts(k_f8_rows<S>, ((long long)p.N + 15) / 16,
+                        (unsigned)((p.M + 16LL * S::RG - 1) / (16 * S::RG)), S::kThreads, st, p);
 }
 
 template <class S>
 static hipError_t launch_rows_grouped(const F8Product &p, const Groups &gr, hipStream_t st)
 {
-    return launch_kernel(k_f8_rows_grouped<S>, dim3((unsigned)(((long long)p.N + 15) / 16), (unsigned)gr.G),
-                         dim3(S::kThreads), 0, st, p, gr);
+    return launch_parts(k_f8_rows_grouped<S>, ((long long)p.N + 15) / 16, (unsigned)gr.G, S::kThreads, st, p, gr);
 }
 
 // Which kernel. A form costs its rounds of 256 workgroups times a round's time
@@ -1030,10 +1030,9 @@ static hipError_t launch_grouped_tiles(const F8Product &p, const Groups &gr, hip
 {
     const long long tn = ((long long)p.N + S::BN - 1) / S::BN;
     const long long grid = group_grid(gr.G, gr.M, S::BM, tn);
-    if (grid > 0x7fffffffLL)
+    if (grid > kMaxGroupTiles)
         return hipErrorInvalidValue;
-    return launch_kernel(k_f8_tile<S, true>, dim3((unsigned)grid), dim3(S::kThreads), 0, st, p, gr,
-                         TileOrder{(int)tn, 0, 0, 0, 0});
+    return launch_parts(k_f8_tile<S, true>, grid, 1, S::kThreads, st, p, gr, TileOrder{(int)tn, 0, 0, 0, 0});
 }
 
 hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w,

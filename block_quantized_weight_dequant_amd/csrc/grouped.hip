@@ -31,13 +31,13 @@ __global__ __launch_bounds__(64 * kPrepWaves) void k_grouped_prep(const void *__
                                                                 Groups gr, int *__restrict__ row_exp,
                                                                 u32x4 *__restrict__ ops, int K,
                                                                 int part_blocks, int *__restrict__ claims,
-                                                                int N)
+                                                                int N, int first)
 {
     __shared__ int s_p[16], s_row[16];
     __shared__ u32x4 s_tile[kPrepWaves][16 * 9];
     constexpr int SUBS = BM / 16, TERMS = BF ? 1 : 2;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int t = blockIdx.x / SUBS, sub = blockIdx.x % SUBS;
+    const int x = first + (int)blockIdx.x, t = x / SUBS, sub = x % SUBS;
     const GroupTile gt = find_group_tile(gr, t, BM, 1);
     const int p0 = gt.lo + gt.mt * BM + sub * 16;
     if (gt.e < 0 || p0 >= gt.hi)
@@ -150,10 +150,11 @@ __global__ __launch_bounds__(kGemmBM) void k_grouped_resolve(Groups gr, const in
 template <class F, bool HO>
 __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
     const u32x4 *__restrict__ ahl, const uint8_t *__restrict__ w, float *__restrict__ y, int N,
-    int nblk_row, int nblk, int tiles_n, const int *__restrict__ row_exp, int accumulate, Groups gr)
+    int nblk_row, int nblk, int tiles_n, const int *__restrict__ row_exp, int accumulate, Groups gr,
+    int first)
 {
     __shared__ SplitLds<F, HO> lds;
-    const GroupTile gt = find_group_tile(gr, xcd_runs(blockIdx.x), kGemmBM, tiles_n);
+    const GroupTile gt = find_group_tile(gr, xcd_runs(first + (int)blockIdx.x), kGemmBM, tiles_n);
     if (gt.e < 0 || gt.before + gt.mt >= gr.tiles)
         return;
     if constexpr (HO) {
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
                                                               const int *__restrict__ row_exp,
                                                               const uint8_t *__restrict__ w,
                                                               float *__restrict__ y, int N, int K,
-                                                              Groups gr)
+                                                              Groups gr, int first)
 {
     using G = FewGeom<F, CT>;
     constexpr int TERMS = HO ? 1 : 2;
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_grouped_few(const u32x4 *__r
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, g = lane >> 4;
     const int nblk = K >> 5, chunks = (nblk + kFewBlocks - 1) / kFewBlocks;
-    const int n0 = blockIdx.x * G::kRows;
+    const int n0 = (first + (int)blockIdx.x) * G::kRows;
     const uint32_t row_bytes = (uint32_t)nblk * F::kBytes;
     const int wrows = min(G::kRows, N - n0);
     // At most 64 rows of 14336 elements: the offsets are far below 2^31.
@@ -441,9 +442,9 @@ static hipError_t launch_few(const u32x4 *ops, const int *row_exp, const uint8_t
                              int N, int K, const Groups &gr, hipStream_t s)
 {
     static_assert(sizeof(FewLds<F, BF, CT, R>) <= (size_t)kLdsBytes, "the stages fit in LDS");
-    const dim3 grid((unsigned)((N + 16LL * CT - 1) / (16 * CT)), (unsigned)q4v::group_row_tiles(gr.G, gr.M, 16 * R));
-    return launch_kernel(k_grouped_few<F, BF, CT, R>, grid, dim3(64 * kFewWaves), 0, s, ops, row_exp, w, y, N,
-                         K, gr);
+    return launch_parts(k_grouped_few<F, BF, CT, R>, (N + 16LL * CT - 1) / (16 * CT),
+                        (unsigned)q4v::group_row_tiles(gr.G, gr.M, 16 * R), 64 * kFewWaves, s, ops, row_exp, w, y,
+                        N, K, gr);
 }
 
 template <class F, bool BF>
@@ -462,9 +463,9 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     const int part = prep_part_blocks(groups, nblk, BF ? 2 : 1);
     const KSegments sg = few ? KSegments{1, nblk} : k_segments(nblk, 2);
     int *claims = sg.n > 1 ? reinterpret_cast<int *>(y) : nullptr;
-    hipError_t e = launch_kernel(few ? k_grouped_prep<F, BF, 16> : k_grouped_prep<F, BF, 128>,
-                                 dim3((unsigned)groups, (unsigned)((nblk + part - 1) / part)),
-                                 dim3(64 * kPrepWaves), 0, s, a, gr, row_exp, ops, K, part, claims, N);
+    hipError_t e = launch_parts(few ? k_grouped_prep<F, BF, 16> : k_grouped_prep<F, BF, 128>, groups,
+                                (unsigned)((nblk + part - 1) / part), 64 * kPrepWaves, s, a, gr, row_exp,
+                                ops, K, part, claims, N);
     if (e != hipSuccess)
         return e;
     if (few) {
@@ -480,7 +481,7 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     }
     const long long tn = ((long long)N + kGemmBN - 1) / kGemmBN;
     const long long grid = group_grid(gr.G, gr.M, kGemmBM, tn);
-    if (grid > 0x7fffffffLL)
+    if (grid > kMaxGroupTiles)
         return hipErrorInvalidValue;
     if (claims) {
         e = launch_kernel(k_grouped_resolve, dim3((unsigned)tiles), dim3(kGemmBM), 0, s, gr,
@@ -490,10 +491,10 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     }
     for (int i = 0; i < sg.n; ++i) {
         const int kb0 = i * sg.len, nb = min(sg.len, nblk - kb0);
-        e = launch_kernel(k_gemm_split_grouped<F, BF>, dim3((unsigned)grid), dim3(kSplitGemmThreads),
-                          0, s, (const u32x4 *)(ops + (size_t)kb0 * slab_ops<BF>()),
-                          w + (size_t)kb0 * F::kBytes, y, N, nblk, nb, (int)tn,
-                          (const int *)row_exp, i > 0 ? 1 : 0, gr);
+        e = launch_parts(k_gemm_split_grouped<F, BF>, grid, 1, kSplitGemmThreads, s,
+                         (const u32x4 *)(ops + (size_t)kb0 * slab_ops<BF>()),
+                         w + (size_t)kb0 * F::kBytes, y, N, nblk, nb, (int)tn,
+                         (const int *)row_exp, i > 0 ? 1 : 0, gr);
         if (e != hipSuccess)
             return e;
     }

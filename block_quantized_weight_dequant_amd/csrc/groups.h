@@ -58,9 +58,11 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
         int lo = 0, hi = 0;
         if (base + lane < gr.G)
             group_bounds(gr, base + lane, lo, hi);
-        // A right list has fewer tiles than any grid has workgroups (2^23 of 512
-        // threads); a wrong one is cut there, where the sums cannot overflow.
-        const int tiles = (int)min((long long)((hi - lo + bm - 1) / bm) * tiles_n, 1LL << 23);
+        // A group of a grid has at most 2^24 tiles (M <= 2^30 rows of one column
+        // tile in tiles of 64; with more columns y, and before it this card's
+        // memory, ends sooner). The cut keeps the sums of overlapping groups
+        // from overflowing.
+        const int tiles = (int)min((long long)((hi - lo + bm - 1) / bm) * tiles_n, 1LL << 24);
         int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -68,7 +70,7 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
             if (lane >= d)
                 sum += v;
         }
-        const uint64_t past = __ballot(run + sum > t);
+        const uint64_t past = __ballot((unsigned)run + (unsigned)sum > (unsigned)t);
         if (past) {
             const int l = __builtin_ctzll(past);
             GroupTile g;
@@ -82,7 +84,7 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
             g.before = first / tiles_n;
             return g;
         }
-        run = min(run + __builtin_amdgcn_readlane(sum, 63), 1 << 30);
+        run = (int)min((unsigned)run + (unsigned)__builtin_amdgcn_readlane(sum, 63), 1u << 30);
     }
     return {-1, 0, 0, 0, 0, 0};
 }
@@ -92,7 +94,9 @@ __device__ __forceinline__ GroupTile find_group_tile(const Groups &gr, int t, in
 // in its L2) without the total being known.
 __device__ __forceinline__ int xcd_runs(int L) { return (L & ~63) | ((L & 7) << 3) | ((L >> 3) & 7); }
 
-// Grid that covers every tile of at most M rows in G groups, whole runs.
+// Grid that covers every tile of at most M rows in G groups, whole runs; at most
+// kMaxGroupTiles of them can be told apart.
+constexpr long long kMaxGroupTiles = 1LL << 30;
 inline long long group_grid(long long G, long long M, long long bm, long long tiles_n)
 {
     return (q4v::group_row_tiles(G, M, bm) * tiles_n + 63) / 64 * 64;
