@@ -46,6 +46,7 @@
 // The slot order of the operands and the decode of the weight bytes are the
 // format's (formats.h); where the decode leaves a factor 2^kHiLog2 on slots
 // 4..7 (Q4_0), the activations of those slots carry 2^-kHiLog2.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <type_traits>
@@ -552,13 +553,37 @@ static bool gemm_f32_splits(int M, int N, int K)
     return q4v::gemm_splits_activations(K) && (long long)M * N < (1LL << 31);
 }
 
+// Rows that one run of launches takes: a grid dimension holds fewer than 2^32
+// threads, and the preparations use 64 for a row, or one for four elements
+// where bfloat16 or Q8_0 activations are written as f32 (per_quad).
+static int gemm_rows_at_once(int M, int K, bool per_quad)
+{
+    if (M < (1 << 26) - kGemmBM && (!per_quad || (long long)M * K <= (1LL << 34) - 1024))
+        return M;
+    const long long rows = std::min(1LL << 25, (1LL << 33) / K);
+    return (int)(rows >= kGemmBM ? rows / kGemmBM * kGemmBM : rows);   // K < 2^31: at least 4
+}
+
+// launch(r0, rows) over the rows of a call, one run after another: each writes
+// the workspace that it reads.
+template <class Fn>
+static hipError_t by_rows(int M, int K, bool per_quad, Fn launch)
+{
+    const int rows = gemm_rows_at_once(M, K, per_quad);
+    hipError_t e = hipSuccess;
+    for (long long r0 = 0; r0 < M && e == hipSuccess; r0 += rows)
+        e = launch((size_t)r0, (int)std::min((long long)rows, M - r0));
+    return e;
+}
+
 hipError_t launch_gemm(WeightFormat fmt, const float *a, const uint8_t *w, float *y, int M, int N,
                        int K, void *workspace, hipStream_t s)
 {
     const bool split = gemm_f32_splits(M, N, K);
-    if (fmt == WeightFormat::kQ8_0)
-        return launch_gemm_f<FmtQ8_0>(a, w, y, M, N, K, workspace, s, split);
-    return launch_gemm_f<FmtQ4_0>(a, w, y, M, N, K, workspace, s, split);
+    return by_rows(M, K, false, [&](size_t r0, int rows) {
+        const auto f = fmt == WeightFormat::kQ8_0 ? launch_gemm_f<FmtQ8_0> : launch_gemm_f<FmtQ4_0>;
+        return f(a + r0 * (size_t)K, w, y + r0 * (size_t)N, rows, N, K, workspace, s, split);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -653,9 +678,10 @@ hipError_t launch_gemm_noalloc(WeightFormat fmt, const float *a, const uint8_t *
 hipError_t launch_gemm_bf16(WeightFormat fmt, const uint16_t *a, const uint8_t *w, float *y, int M,
                             int N, int K, void *workspace, hipStream_t s)
 {
-    if (fmt == WeightFormat::kQ8_0)
-        return launch_gemm_bf16_f<FmtQ8_0>(a, w, y, M, N, K, workspace, s);
-    return launch_gemm_bf16_f<FmtQ4_0>(a, w, y, M, N, K, workspace, s);
+    return by_rows(M, K, true, [&](size_t r0, int rows) {
+        const auto f = fmt == WeightFormat::kQ8_0 ? launch_gemm_bf16_f<FmtQ8_0> : launch_gemm_bf16_f<FmtQ4_0>;
+        return f(a + r0 * (size_t)K, w, y + r0 * (size_t)N, rows, N, K, workspace, s);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -845,9 +871,10 @@ static hipError_t launch_gemm_q8a_f(const uint8_t *aq, const uint8_t *w, float *
 hipError_t launch_gemm_q8a(WeightFormat fmt, const uint8_t *a_q, const uint8_t *w, float *y, int M,
                            int N, int K, void *workspace, hipStream_t s)
 {
-    if (fmt == WeightFormat::kQ8_0)
-        return launch_gemm_q8a_f<FmtQ8_0>(a_q, w, y, M, N, K, workspace, s);
-    return launch_gemm_q8a_f<FmtQ4_0>(a_q, w, y, M, N, K, workspace, s);
+    return by_rows(M, K, true, [&](size_t r0, int rows) {
+        const auto f = fmt == WeightFormat::kQ8_0 ? launch_gemm_q8a_f<FmtQ8_0> : launch_gemm_q8a_f<FmtQ4_0>;
+        return f(a_q + r0 * ((size_t)(K / 32) * kQ8Bytes), w, y + r0 * (size_t)N, rows, N, K, workspace, s);
+    });
 }
 
 }  // namespace q4k

@@ -54,7 +54,8 @@ extern "C" {
 #define Q4_ERR_SIZE 3   /* a byte or element count disagrees with the shape, or overflows size_t */
 #define Q4_ERR_ALIGN 4  /* a pointer is not 16-byte aligned */
 #define Q4_ERR_ALIAS 5  /* an output overlaps an input */
-#define Q4_ERR_LAUNCH 6 /* the HIP runtime refused the launch */
+#define Q4_ERR_LAUNCH 6 /* the HIP runtime refused the launch, or it needs a grid of 2^32 threads or more
+                         * (some 2^27 columns on the GEMVs' general kernels, 2^30 on the GEMMs) */
 #define Q4_ERR_WORKSPACE 7 /* a GEMM workspace is smaller than its *_gemm_workspace_bytes */
 
 /* Largest number of activation rows q4_gemv and q8_gemv accept. */

@@ -1,0 +1,51 @@
+"""GEMMs past the threads of one launch (2^26 rows, 64 threads each in the
+preparation): every output written, and sampled ones right."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import oracle  # noqa: E402
+from block_quantized_weight_dequant_amd import binding  # noqa: E402
+from block_quantized_weight_dequant_amd import workloads as wl  # noqa: E402
+from gpu_helpers import DEV, assert_within_tolerance, to_dev, weight_blob  # noqa: E402
+
+M, N = 2 ** 26 + 40, 16
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16", "q8_0"])
+@pytest.mark.parametrize("K", [64, 32])          # the split path, the general kernel
+def test_gemm_of_2_26_rows(act, K):
+    blob = weight_blob("q8_0", N, K, 90)
+    T = 5000                                     # distinct rows, repeated
+    rows = torch.from_numpy(np.arange(M, dtype=np.int64) % T).to(DEV)
+    y = torch.full((M, N), float("nan"), device=DEV)
+    if act == "q8_0":
+        small = oracle.q8_0_quantize(wl.activations_f32(91, T, K))
+        values = oracle.q8_0_dequant(small).reshape(T, K)
+        a = to_dev(small.reshape(T, -1))[rows]
+        binding.q8_gemm_q8a(a, to_dev(blob), y, M, N, K)
+    elif act == "bf16":
+        small = wl.activations_bf16(91, T, K)
+        values = oracle.bf16_to_f32(small).reshape(T, K)
+        a = to_dev(small.view(np.int16).reshape(T, K))[rows]
+        binding.q8_gemm_bf16(a, to_dev(blob), y, M, N, K)
+    else:
+        values = wl.activations_f32(91, T, K)
+        a = to_dev(values)[rows]
+        binding.q8_gemm_ws(a, to_dev(blob), y, M, N, K)
+    torch.cuda.synchronize()
+    del a
+    w = oracle.q8_0_dequant(blob).reshape(N, K).astype(np.float64)
+    ref, bound = values.astype(np.float64) @ w.T, np.abs(values).astype(np.float64) @ np.abs(w).T
+    first = y[:T].cpu().numpy()
+    assert_within_tolerance(first, ref, bound, act)
+    # Equal rows are equal bits, wherever they stand.
+    whole = M // T * T
+    assert bool((y[:whole].reshape(-1, T, N) == y[:T]).all()) and bool((y[whole:] == y[:M - whole]).all())
+    del y, rows
+    torch.cuda.empty_cache()
