@@ -7,9 +7,9 @@
 // ceil(K / 128)] (one per 128 x 128 tile), all row-major; a row's last block
 // may be short.
 #include <algorithm>
-#include <climits>
 
 #include "device_common.h"
+#include "f8_forms.h"
 #include "groups.h"
 #include "launch.h"
 
@@ -952,75 +952,25 @@ static hipError_t launch_rows_grouped(const F8Product &p, const Groups &gr, hipS
     return launch_parts(k_f8_rows_grouped<S>, ((long long)p.N + 15) / 16, (unsigned)gr.G, S::kThreads, st, p, gr);
 }
 
-// Which kernel. A form costs its rounds of 256 workgroups times a round's time
-// per block of K, in 10 ns on MI355X (beside some 4 us a call): few rows by
-// their row groups with the weights streaming, tiles with the chip full. Few
-// rows are taken where they cost no more than the cheapest tile, else the
-// largest tile that costs no more than that, or than the weights' bytes take at
-// 5.5 TB/s: where those bound the call the larger tiles stream them better (37
-// tokens, 2 of 8 experts of 14336 x 4096: wide 113 us, half 119; 512 tokens, 8 of
-// 128 of 1536 x 2048: wide 87, quarter 96). M x N x K by few rows and by quarter
-// tiles, weights in cache: 64 x 4096 x 4096 9.2 and 9.7 us, 16 x 8192 x 8192 13.9
-// and 14.2, 1 x 14336 x 4096 16.5 and 11.7, 32 x 14336 x 4096 20.1 and 12.4
-// (weights from HBM: 24.9 and 16.1). By quarter, half and small tiles: 256 x 4096
-// x 4096 11.4, 15.9 and 18.3 us, 512 x 4096 x 4096 19.7, 17.1 and 21.5, 1001 x
-// 4096 x 4096 35.8, 26.6 and 21.7. By small, wide and large ones: 1001 x 4096 x
-// 4096 21, 28 and 46 us, 2048 x 14336 x 4096 163, 149 and 129.
-enum Form { kRows, kQuarter, kHalf, kSmall, kWide, kLarge };
-
+// f8_forms.h prices the tiles by their sides.
 template <class S>
-static long long tile_cost(long long tiles_m, int N, int round)
-{
-    return (tiles_m * (((long long)N + S::BN - 1) / S::BN) + 255) / 256 * round;
-}
-
-// Rounds of the few-row form: `passes` times N / 16 workgroups, rg row groups each.
-static long long rows_cost(long long passes, int N, int rg)
-{
-    constexpr int kRound[] = {0, 11, 12, 14, 19};
-    return (passes * (((long long)N + 15) / 16) + 255) / 256 * kRound[rg];
-}
-
-// Over tiles_m(bm) row tiles of bm rows in all, of `groups` weight matrices;
-// rows: the cost of the few-row form.
-template <class TilesM>
-static Form choose_form(long long groups, long long rows, int N, TilesM tiles_m)
-{
-    const long long cost[] = {tile_cost<TileQuarter>(tiles_m(64), N, 25), tile_cost<TileHalf>(tiles_m(64), N, 40),
-                              tile_cost<TileSmall>(tiles_m(128), N, 70), tile_cost<TileWide>(tiles_m(128), N, 110),
-                              tile_cost<TileLarge>(tiles_m(256), N, 190)};
-    const long long least = *std::min_element(cost, cost + 5);
-    if (rows <= least)
-        return kRows;
-    int i = 4;
-    while (cost[i] > std::max(least, groups * N / 430))
-        --i;
-    return (Form)(kQuarter + i);
-}
+constexpr bool sides(q4v::F8Form f) { return q4v::kF8Tiles[f - q4v::kF8Quarter].bn == S::BN && q4v::kF8Tiles[f - q4v::kF8Quarter].bm == S::BM; }
+static_assert(sides<TileQuarter>(q4v::kF8Quarter) && sides<TileHalf>(q4v::kF8Half) && sides<TileSmall>(q4v::kF8Small) &&
+                  sides<TileWide>(q4v::kF8Wide) && sides<TileLarge>(q4v::kF8Large), "one list of sides");
 
 hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, const float *w_s,
                           uint16_t *y, int M, int N, int K, hipStream_t st)
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
-    // Row groups of the few-row form: the fewest at the least cost, so that few
-    // weight rows spread over more workgroups (64 x 1024 x 4096: 7.3 us by one
-    // pass of four row groups, 5.2 by four of one; 128 x 256 x 7168: 11.4 us in
-    // quarter tiles, 5.0 so).
-    int rg = 0;
-    long long rows = 0;
-    for (int i = 1; i <= 4; ++i) {
-        const long long passes = (M + 16LL * i - 1) / (16 * i), c = rows_cost(passes, N, i);
-        if (passes <= 65535 && (!rg || c < rows))
-            rg = i, rows = c;
-    }
-    switch (choose_form(1, rg ? rows : LLONG_MAX, N, [&](int bm) { return ((long long)M + bm - 1) / bm; })) {
-    case kRows:
-        return rg == 1 ? launch_rows<Rows1>(p, st) : rg == 2 ? launch_rows<Rows2>(p, st)
-             : rg == 3 ? launch_rows<Rows3>(p, st) : launch_rows<Rows4>(p, st);
-    case kQuarter: return launch_tiles<TileQuarter>(p, st);
-    case kHalf: return launch_tiles<TileHalf>(p, st);
-    case kSmall: return launch_tiles<TileSmall>(p, st);
-    case kWide: return launch_tiles<TileWide>(p, st);
+    const q4v::F8Choice c = q4v::f8_form(M, N);
+    switch (c.form) {
+    case q4v::kF8Rows:
+        return c.rg == 1 ? launch_rows<Rows1>(p, st) : c.rg == 2 ? launch_rows<Rows2>(p, st)
+             : c.rg == 3 ? launch_rows<Rows3>(p, st) : launch_rows<Rows4>(p, st);
+    case q4v::kF8Quarter: return launch_tiles<TileQuarter>(p, st);
+    case q4v::kF8Half: return launch_tiles<TileHalf>(p, st);
+    case q4v::kF8Small: return launch_tiles<TileSmall>(p, st);
+    case q4v::kF8Wide: return launch_tiles<TileWide>(p, st);
     default: return launch_tiles<TileLarge>(p, st);
     }
 }
@@ -1041,20 +991,15 @@ hipError_t launch_f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint
 {
     const F8Product p = {a, a_s, w, w_s, y, M, N, K, (K + 127) / 128, (int)(((long long)N + 127) / 128)};
     const Groups gr = {offsets, order, G, M, share, 0};
-    // The host knows the mean size only. Few rows: with room for groups of twice
-    // the mean (longer ones take several passes). Tiles: a group ends within one,
-    // half filled on average.
-    const long long hit = G < M ? G : M, mean = (M + hit - 1) / hit;
-    const int rg = mean <= 8 ? 1 : mean <= 16 ? 2 : mean <= 32 ? 4 : 0;
-    const long long rows = rg ? rows_cost(hit, N, rg) : LLONG_MAX;
-    switch (choose_form(hit, rows, N, [&](int bm) { return std::max(hit, M / bm + hit / 2); })) {
-    case kRows:
-        return rg == 1 ? launch_rows_grouped<Rows1>(p, gr, st) : rg == 2 ? launch_rows_grouped<Rows2>(p, gr, st)
+    const q4v::F8Choice c = q4v::f8_form_grouped(G, M, N);
+    switch (c.form) {
+    case q4v::kF8Rows:
+        return c.rg == 1 ? launch_rows_grouped<Rows1>(p, gr, st) : c.rg == 2 ? launch_rows_grouped<Rows2>(p, gr, st)
              : launch_rows_grouped<Rows4>(p, gr, st);
-    case kQuarter: return launch_grouped_tiles<TileQuarter>(p, gr, st);
-    case kHalf: return launch_grouped_tiles<TileHalf>(p, gr, st);
-    case kSmall: return launch_grouped_tiles<TileSmall>(p, gr, st);
-    case kWide: return launch_grouped_tiles<TileWide>(p, gr, st);
+    case q4v::kF8Quarter: return launch_grouped_tiles<TileQuarter>(p, gr, st);
+    case q4v::kF8Half: return launch_grouped_tiles<TileHalf>(p, gr, st);
+    case q4v::kF8Small: return launch_grouped_tiles<TileSmall>(p, gr, st);
+    case q4v::kF8Wide: return launch_grouped_tiles<TileWide>(p, gr, st);
     default: return launch_grouped_tiles<TileLarge>(p, gr, st);
     }
 }

@@ -469,14 +469,11 @@ static hipError_t launch_grouped_f(const void *a, const uint8_t *w, float *y, in
     if (e != hipSuccess)
         return e;
     if (few) {
-        // Weight rows of a workgroup: as many as leave two workgroups for each
-        // compute unit (more of them share one pass over the operands).
-        const long long hit = gr.G < gr.M ? gr.G : gr.M;
-        const bool two = gr.M > 16LL * hit;   // more than 16 rows a group on average
         constexpr int CTL = F::kBytes == kQ8Bytes ? 2 : 4;
-        if (q4v::grouped_passes(gr.G, gr.M, two ? 2 : 1) * N >= 512LL * 16 * CTL)
-            return two ? launch_few<F, BF, CTL, 2>(ops, row_exp, w, y, N, K, gr, s)
-                       : launch_few<F, BF, CTL, 1>(ops, row_exp, w, y, N, K, gr, s);
+        const q4v::FewShape fs = q4v::grouped_few_shape(gr.G, gr.M, N, F::kBytes);
+        if (fs.ct == CTL)
+            return fs.r == 2 ? launch_few<F, BF, CTL, 2>(ops, row_exp, w, y, N, K, gr, s)
+                             : launch_few<F, BF, CTL, 1>(ops, row_exp, w, y, N, K, gr, s);
         return launch_few<F, BF, 1, 1>(ops, row_exp, w, y, N, K, gr, s);
     }
     const long long tn = ((long long)N + kGemmBN - 1) / kGemmBN;

@@ -209,6 +209,19 @@ inline bool grouped_few(int G, int M, int N, int K)
     return passes * 3 <= 19 * (tiles > 135 ? tiles : 135);
 }
 
+// A few-row workgroup's weight rows, in 16s, and the rows of its pass: as many
+// weight rows as leave two workgroups for each compute unit (more of them share
+// one pass over the operands), 32 rows where groups have more than 16 on
+// average.
+struct FewShape {
+    int ct, r;
+};
+inline FewShape grouped_few_shape(int G, int M, int N, size_t block_bytes)
+{
+    const int r = M > 16LL * (G < M ? G : M) ? 2 : 1, wide = block_bytes == 34 ? 2 : 4;
+    return grouped_passes(G, M, r) * N >= 512LL * 16 * wide ? FewShape{wide, r} : FewShape{1, 1};
+}
+
 // Up to 8 rows are multiplied in place, each by the streaming GEMV kernel with
 // its group's matrix, where that kernel takes the shape: no workspace.
 inline bool grouped_in_place(int M, int N, int K, size_t block_bytes, size_t a_elem)
