@@ -75,7 +75,11 @@ int f8_dequant(const void *q, size_t q_bytes, const float *s, size_t s_elems, in
  * The first term is y's rounding to bfloat16 (at most half a step). The second
  * is the matrix core's: it adds eight products at a time and drops what is
  * below 2^-13 of the largest one's power of two. On normal data that is about
- * 2^-16 of the result, far below the first term. The blocks are added in f32.
+ * 2^-16 of the result, far below the first term. The blocks are added in f32,
+ * each times a_s w_s, which is formed in f32: below 2^-126 it is a multiple of
+ * 2^-149, and the bound is 2^-150 (sum over k of the codes' |a w| + K / 64) +
+ * 2^-134 wider; from 2^128 on its block counts as infinite, or NaN where the
+ * codes' sum is 0. f8_quantize makes such scales of values near f32's ends only.
  */
 int f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, size_t w_bytes, const float *w_s,
             uint16_t *y, int M, int N, int K, void *stream);

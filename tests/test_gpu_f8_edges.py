@@ -57,3 +57,24 @@ def test_quantize_of_maxima_a_step_past_448(block_rows):
     x[::block_rows, 3], x[::block_rows, 77] = v, -v
     q = check_codes(x, block_rows, "f32")
     assert (q[::block_rows, 3] == 0x7E).all() and (q[::block_rows, 77] == 0xFE).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 100, 160), (40, 4096, 160), (140, 3900, 288), (520, 4096, 160), (975, 8200, 160)])
+def test_product_of_scales_below_the_normal_range(M, N, K):
+    # a_s w_s of 2^-145 to 2^-135: formed in f32, a multiple of 2^-149 (off by
+    # 2^-150 at most), so each block is off by 2^-150 of its codes' sum more.
+    # Each of the blocks' additions and y's rounding to bfloat16 add half a step
+    # below the normal range: 2^-150 a block, 2^-134.
+    rng = np.random.default_rng(M)
+    a = pl.e4m3_encode(rng.normal(size=(M, K)).astype(np.float32) * 100)
+    w = pl.e4m3_encode(rng.normal(size=(N, K)).astype(np.float32) * 100)
+    a_s = np.exp2(rng.uniform(-72, -68, (M, pl.blocks(K)))).astype(np.float32)
+    w_s = np.exp2(rng.uniform(-73, -67, (pl.blocks(N), pl.blocks(K)))).astype(np.float32)
+    ref, P = pl.product(a, a_s, w, w_s)
+    C = np.abs(pl.e4m3_decode(a)) @ np.abs(pl.e4m3_decode(w)).T
+    y = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    q4.f8_gemm(to_dev(a), to_dev(a_s), to_dev(w), to_dev(w_s), y, M, N, K)
+    torch.cuda.synchronize()
+    tol = pl.product_tolerance(ref, P, K) + 2.0 ** -150 * (1.01 * C + 2 * pl.blocks(K)) + 2.0 ** -134
+    got = y.double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol).all() and (got != 0).mean() > 0.9
