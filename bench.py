@@ -608,6 +608,7 @@ def bench_rw_ceiling(torch, groups, read_words, write_words, steps, warmup, reps
 EXPERT_ROWS = [
     ("f8_quantize_bf16_2048x4096", "quantize", dict(M=2048, K=4096, rows=1, act="bf16")),
     ("f8_quantize_tiles_14336x4096", "quantize", dict(M=14336, K=4096, rows=128, act="f32")),
+    ("f8_dequant_tiles_14336x4096", "dequant", dict(M=14336, K=4096, rows=128)),
     ("f8_gemv_1x4096x4096", "f8", dict(M=1, N=4096, K=4096)),
     ("f8_gemv_8x14336x4096", "f8", dict(M=8, N=14336, K=4096)),
     ("f8_gemm_40x4096x14336", "f8", dict(M=40, N=4096, K=14336)),
@@ -619,8 +620,17 @@ EXPERT_ROWS = [
     ("q4_grouped_f32_1_2of8_4096x4096", "grouped", dict(fmt="q4_0", act="f32", T=1, E=8, k=2, N=4096, K=4096)),
     ("q4_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
     ("q8_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
+    ("q4_grouped_f32_37_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="f32", T=37, E=8, k=2, N=14336, K=4096)),
+    ("q8_grouped_f32_37_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="f32", T=37, E=8, k=2, N=14336, K=4096)),
+    ("q4_grouped_bf16_512_8of128_1536x2048", "grouped", dict(fmt="q4_0", act="bf16", T=512, E=128, k=8, N=1536, K=2048)),
     ("q4_grouped_bf16_2048_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="bf16", T=2048, E=8, k=2, N=14336, K=4096)),
+    ("q8_grouped_bf16_2048_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="bf16", T=2048, E=8, k=2, N=14336, K=4096)),
+    ("q4_grouped_f32_2048_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="f32", T=2048, E=8, k=2, N=14336, K=4096)),
+    ("q8_grouped_f32_2048_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="f32", T=2048, E=8, k=2, N=14336, K=4096)),
+    ("q4_grouped_bf16_2048_2of8_4096x14336", "grouped", dict(fmt="q4_0", act="bf16", T=2048, E=8, k=2, N=4096, K=14336)),
+    ("f8_grouped_1_2of8_4096x4096", "grouped", dict(fmt="f8", act="f8", T=1, E=8, k=2, N=4096, K=4096)),
     ("f8_grouped_37_2of8_14336x4096", "grouped", dict(fmt="f8", act="f8", T=37, E=8, k=2, N=14336, K=4096)),
+    ("f8_grouped_512_8of128_1536x2048", "grouped", dict(fmt="f8", act="f8", T=512, E=128, k=8, N=1536, K=2048)),
     ("f8_grouped_2048_2of8_14336x4096", "grouped", dict(fmt="f8", act="f8", T=2048, E=8, k=2, N=14336, K=4096)),
 ]
 
@@ -658,6 +668,9 @@ def bench_expert(torch, q4, name, kind, steps, warmup, reps, profile, M=0, N=0, 
             f, x = (q4.f8_quantize_bf16, x.bfloat16()) if act == "bf16" else (q4.f8_quantize, x)
             q, s = torch.empty(M * K, dtype=torch.uint8, **dev), torch.empty(-(-M // rows), kb, **dev)
             return (lambda: f(x, q, s, M, K, rows)), M * K * (x.element_size() + 1) + s.numel() * 4, 0
+        if kind == "dequant":
+            (q, s), out = e4m3(normal(M, K), rows), torch.empty(M * K, **dev)
+            return (lambda: q4.f8_dequant(q, s, out, M, K, rows)), M * K * 5 + s.numel() * 4, 0
         if kind == "f8":
             (a, a_s), (w, w_s) = e4m3(normal(M, K), 1), e4m3(normal(N, K), 128)
             y = torch.empty(M, N, dtype=torch.bfloat16, **dev)

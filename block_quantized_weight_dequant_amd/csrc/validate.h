@@ -194,12 +194,18 @@ inline long long grouped_passes(long long G, long long M, int R)
 // The grouped product's form. few: passes of up to 32 rows streamed past 64
 // weight rows each. Otherwise 128 x 256 tiles of the GEMM's split kernel. By
 // their times with the chip full and, where there are not enough of them for
-// that, alone, in us at K = 4096 with bfloat16 activations (f32: 1.8 times each):
-// a tile 1/3, at least 45; a pass 1/19 (256 tokens, 2 of 8 experts: 1024 x 1024
-// 15.6 us by passes and 24.7 by tiles, 2048 x 2048 28 and 36, 4096 x 4096 70 and
-// 59). few keeps a wavefront's chain of block partials at 112 or fewer (K <=
-// 14336: 448 blocks dealt to four), as the GEMM's segments do, and its passes
-// within a grid's second dimension.
+// that, alone, in us at K = 4096 with bfloat16 activations: a tile 1/3, at least
+// 45; a pass 1/19. f32 activations and Q8_0 weights make both longer by much the
+// same, so one rule serves all four. 256 tokens, 2 of 8 experts, N x K by passes
+// and by tiles, us:
+//               Q4_0 f32   Q4_0 bf16   Q8_0 f32   Q8_0 bf16
+//   1024 x 1024   20  29     15  23      20  30     16  24
+//   2560 x 4096   61  71     46  52      71  76     52  57
+//   4096 x 4096   95  79     72  55     110  86     81  60
+//   8192 x 4096  150 147    114  97     213 168    159 114
+// few keeps a wavefront's chain of block partials at 112 or fewer (K <= 14336:
+// 448 blocks dealt to four), as the GEMM's segments do, and its passes within a
+// grid's second dimension.
 inline bool grouped_few(int G, int M, int N, int K)
 {
     if (K > 14336 || M > 1 << 19)
@@ -239,10 +245,10 @@ inline size_t grouped_exp_bytes(int G, int M, int N, int K)
     return ((size_t)group_row_tiles(G, M, bm) * (size_t)bm * 4 + 255) / 256 * 256;
 }
 
-// Sizes, then pointers, of a grouped product: a (a_bytes in all, and a_s of
-// a_s_bytes, 0 if there is none), w (w_want bytes asked, w_bytes given), w_s,
-// offsets [G + 1], order [M] (may be NULL), y of y_bytes. Shapes are checked
-// before, by check_group_shape.
+// Pointers of a grouped product: a (a_bytes in all, and a_s of a_s_bytes, 0 if
+// there is none), w, w_s, offsets [G + 1], order [M] (may be NULL), y of y_bytes.
+// Shapes are checked before, by check_group_shape, and the caller compares
+// w_bytes with what the shape asks.
 int check_group_shape(int G, int M, int N, int K, int k_unit, int k_max, int share);
 struct GroupedArgs {
     const void *a;
