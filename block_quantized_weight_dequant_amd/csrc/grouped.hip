@@ -192,9 +192,10 @@ __global__ __launch_bounds__(kSplitGemmThreads) void k_gemm_split_grouped(
 // 154 -> 128 us, Q4_0 with f32 activations 118 -> 106, 100 tokens of bfloat16
 // 134 -> 124). Also measured, and no faster (90-100 us of Q4_0, bfloat16):
 // persistent workgroups with the loads running on into the next tile, three
-// stages, loads spread between the blocks' decodes. The decode (14 vector
-// instructions a matrix instruction) and the streaming each take about 60 us
-// alone, and 3 TB/s is what the decode GEMV of 8 rows reaches on this shape.
+// stages, loads spread between the blocks' decodes. Of its 73 us the bytes
+// need 56 and the decode's issue (14 vector instructions a matrix instruction,
+// 917504 of these) some 22: what is left is latency, with two wavefronts a SIMD
+// (74 KB of LDS a workgroup) to hide it.
 constexpr int kFewWaves = 4, kFewBlocks = 8;
 
 template <class F, int CT>

@@ -192,9 +192,9 @@ inline long long grouped_passes(long long G, long long M, int R)
 }
 
 // The grouped product's form. few: passes of up to 32 rows streamed past 64
-// weight rows each. Otherwise 128 x 256 tiles of the GEMM's split kernel. By
+// weight rows each. Otherwise the GEMM's split kernel, its 128 x 128 tiles in pairs. By
 // their times with the chip full and, where there are not enough of them for
-// that, alone, in us at K = 4096 with bfloat16 activations: a tile 1/3, at least
+// that, alone, in us at K = 4096 with bfloat16 activations: a pair 1/3, at least
 // 45; a pass 1/19. f32 activations and Q8_0 weights make both longer by much the
 // same, so one rule serves all four. 256 tokens, 2 of 8 experts, N x K by passes
 // and by tiles, us:
