@@ -93,14 +93,17 @@ __global__ __launch_bounds__(kDequantThreads) void k_dequant(const uint8_t *__re
 hipError_t launch_dequant(WeightFormat fmt, const uint8_t *w, size_t n_blocks, float *out,
                           hipStream_t s)
 {
-    const size_t n_quads = n_blocks * 8;
-    const size_t per_wg = kDequantThreads * kQuadsPerThread;
-    const size_t grid = (n_quads + per_wg - 1) / per_wg;
-    if (grid > 0x7fffffffu)
-        return hipErrorInvalidValue;
-    return launch_kernel(fmt == WeightFormat::kQ8_0 ? k_dequant<FmtQ8_0> : k_dequant<FmtQ4_0>,
-                         dim3((unsigned)grid), dim3(kDequantThreads), 0, s, w,
-                         reinterpret_cast<float4 *>(out), n_quads);
+    // 2^29 blocks (2^31 threads) a launch: a grid holds fewer than 2^32.
+    constexpr size_t part = (size_t)1 << 29, per_wg = kDequantThreads * kQuadsPerThread;
+    const size_t bytes = fmt == WeightFormat::kQ8_0 ? kQ8Bytes : kQ4Bytes;
+    hipError_t e = hipSuccess;
+    for (size_t b0 = 0; b0 < n_blocks && e == hipSuccess; b0 += part) {
+        const size_t n_quads = (n_blocks - b0 < part ? n_blocks - b0 : part) * 8;
+        e = launch_kernel(fmt == WeightFormat::kQ8_0 ? k_dequant<FmtQ8_0> : k_dequant<FmtQ4_0>,
+                          dim3((unsigned)((n_quads + per_wg - 1) / per_wg)), dim3(kDequantThreads), 0, s,
+                          w + b0 * bytes, reinterpret_cast<float4 *>(out + b0 * 32), n_quads);
+    }
+    return e;
 }
 
 }  // namespace q4k

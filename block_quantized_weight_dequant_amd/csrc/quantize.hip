@@ -214,27 +214,31 @@ __global__ __launch_bounds__(256) void k_quantize_q4_0(const float *__restrict__
 }
 
 // R = kQuantLaneBlocks when that still gives kQuantMinGrid workgroups, else 1.
+// At most 2^23 workgroups (2^31 threads) a launch: a grid holds fewer than 2^32.
 static hipError_t launch_quant(void (*k4)(const float *, uint8_t *, size_t),
-                               void (*k1)(const float *, uint8_t *, size_t), const float *x,
-                               size_t n_blocks, uint8_t *out, hipStream_t s)
+                               void (*k1)(const float *, uint8_t *, size_t), size_t block_bytes,
+                               const float *x, size_t n_blocks, uint8_t *out, hipStream_t s)
 {
     const size_t wide = 32 * (size_t)kQuantLaneBlocks;
     const bool wide_launch = (n_blocks + wide - 1) / wide >= kQuantMinGrid;
-    const size_t per = wide_launch ? wide : 32;
-    const size_t grid = (n_blocks + per - 1) / per;
-    if (grid > 0x7fffffffu)
-        return hipErrorInvalidValue;
-    return launch_kernel(wide_launch ? k4 : k1, dim3((unsigned)grid), dim3(256), 0, s, x, out, n_blocks);
+    const size_t per = wide_launch ? wide : 32, part = per << 23;
+    hipError_t e = hipSuccess;
+    for (size_t b0 = 0; b0 < n_blocks && e == hipSuccess; b0 += part) {
+        const size_t nb = n_blocks - b0 < part ? n_blocks - b0 : part;
+        e = launch_kernel(wide_launch ? k4 : k1, dim3((unsigned)((nb + per - 1) / per)), dim3(256), 0, s,
+                          x + b0 * 32, out + b0 * block_bytes, nb);
+    }
+    return e;
 }
 
 hipError_t launch_q8_quantize(const float *x, size_t n_blocks, uint8_t *out, hipStream_t s)
 {
-    return launch_quant(k_quantize_q8_0<kQuantLaneBlocks>, k_quantize_q8_0<1>, x, n_blocks, out, s);
+    return launch_quant(k_quantize_q8_0<kQuantLaneBlocks>, k_quantize_q8_0<1>, kQ8Bytes, x, n_blocks, out, s);
 }
 
 hipError_t launch_q4_quantize(const float *x, size_t n_blocks, uint8_t *out, hipStream_t s)
 {
-    return launch_quant(k_quantize_q4_0<kQuantLaneBlocks>, k_quantize_q4_0<1>, x, n_blocks, out, s);
+    return launch_quant(k_quantize_q4_0<kQuantLaneBlocks>, k_quantize_q4_0<1>, kQ4Bytes, x, n_blocks, out, s);
 }
 
 }  // namespace q4k

@@ -49,3 +49,33 @@ def test_gemm_of_2_26_rows(act, K):
     assert bool((y[:whole].reshape(-1, T, N) == y[:T]).all()) and bool((y[whole:] == y[:M - whole]).all())
     del y, rows
     torch.cuda.empty_cache()
+
+
+ROW = 2 ** 20                    # elements, repeated
+
+
+def same_rows(t, what):
+    for r0 in range(0, t.shape[0], 4096):
+        assert bool((t[r0:r0 + 4096] == t[0]).all()), (what, r0)
+
+
+@pytest.mark.parametrize("fmt", ["q4", "q8"])
+def test_codecs_of_2_35_elements(fmt):
+    # 2^32 threads of the quantizers and the decodes (128 GiB of f32).
+    rows, row_bytes = 2 ** 15 + 1, ROW // 32 * (18 if fmt == "q4" else 34)
+    x0 = wl.activations_f32(92, 1, ROW).reshape(-1)
+    x = torch.empty(rows, ROW, device=DEV)
+    x[:] = to_dev(x0)
+    q = torch.zeros(rows, row_bytes, dtype=torch.uint8, device=DEV)
+    getattr(binding, fmt + "_quantize")(x, q)
+    torch.cuda.synchronize()
+    ref = getattr(oracle, fmt + "_0_quantize")(x0)
+    assert np.array_equal(q[0].cpu().numpy(), ref)
+    same_rows(q, "codes")
+    x.fill_(float("nan"))
+    getattr(binding, fmt + "_dequant")(q, x)
+    torch.cuda.synchronize()
+    assert np.array_equal(x[0].cpu().numpy(), getattr(oracle, fmt + "_0_dequant")(ref).reshape(-1))
+    same_rows(x, "values")
+    del x, q
+    torch.cuda.empty_cache()
