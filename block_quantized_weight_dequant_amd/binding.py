@@ -30,6 +30,12 @@ Q4_GEMM_SCRATCH_BYTES = 64 << 20
 Q4_MAX_EXPERTS = 1024
 Q4_MAX_TOP_K = 32
 Q4_MAX_SLOTS = 1 << 30
+Q4_NORM_MAX_K = 32768
+Q4_ROUTE_MAX_GROUPS = 64
+Q4_ACT_SILU = 0
+Q4_ACT_GELU = 1
+Q4_SCORE_SOFTMAX = 0
+Q4_SCORE_SIGMOID = 1
 SIZE_MAX = 2 ** 64 - 1
 
 #: Every symbol include/q4.h declares.
@@ -42,13 +48,14 @@ EXPORTS = ("q4_abi_version", "q4_status_string", "q4_dequant", "q4_gemv", "q4_ge
            "q4_gemv_prepare", "q4_gemv_prepared", "q8_gemv_prepare_bytes", "q8_gemv_prepare",
            "q8_gemv_prepared", "q4_gemv_q8a", "q8_gemv_q8a", "q4_gemm_q8a",
            "q4_gemm_q8a_workspace_bytes", "q8_gemm_q8a", "q8_gemm_q8a_workspace_bytes",
-           "q4_route", "q4_route_workspace_bytes") + tuple(
+           "q4_route", "q4_route_workspace_bytes", "q4_route_groups") + tuple(
                f + "_gemm_grouped" + act + ws for f in ("q4", "q8") for act in ("", "_bf16")
-               for ws in ("", "_workspace_bytes"))
+               for ws in ("", "_workspace_bytes")) + tuple(
+               f + op + act for f in ("q4", "q8") for op in ("_norm", "_act") for act in ("", "_bf16"))
 
 #: Every symbol include/f8.h declares.
 F8_EXPORTS = ("f8_quantize", "f8_quantize_bf16", "f8_dequant", "f8_gemm", "f8_gemv",
-              "f8_gemm_grouped")
+              "f8_gemm_grouped", "f8_norm", "f8_norm_bf16", "f8_act", "f8_act_bf16")
 F8_BLOCK = 128
 F8_MAX_K = 4194304
 
@@ -118,6 +125,16 @@ def _load_library():
         getattr(lib, name).argtypes = [P, P, sz, P, P, i32, P, i32, i32, i32, i32, P, sz, P]
         getattr(lib, name + "_workspace_bytes").restype = sz
         getattr(lib, name + "_workspace_bytes").argtypes = [i32, i32, i32, i32]
+    f32 = ctypes.c_float
+    lib.q4_route_groups.restype = i32
+    lib.q4_route_groups.argtypes = [P, P] + [i32] * 8 + [f32, P, P, P, P, P, sz, P]
+    for act in ("", "_bf16"):
+        for op, head in (("_norm", [P, P, i32, P, P, P, f32]), ("_act", [P, P, i32, i32])):
+            extra = [P] if op == "_norm" else []
+            getattr(lib, "q4" + op + act).restype = getattr(lib, "q8" + op + act).restype = i32
+            getattr(lib, "q4" + op + act).argtypes = head + [P, i32, i32, i32, P]
+            getattr(lib, "q8" + op + act).argtypes = head + extra + [P, sz, i32, i32, P]
+            getattr(lib, "f8" + op + act).argtypes = head + extra + [P, sz, P, sz, i32, i32, P]
     for name in F8_EXPORTS:
         getattr(lib, name).restype = i32
     lib.f8_quantize.argtypes = lib.f8_quantize_bf16.argtypes = [P, i32, i32, i32, P, sz, P, sz, P]
@@ -610,6 +627,203 @@ def q8_gemm_grouped_bf16(a, w_q, offsets, order, y, G: int, M: int, N: int, K: i
     """As q4_gemm_grouped_bf16 over Q8_0 matrices."""
     _gemm_grouped("q8_gemm_grouped_bf16", a, w_q, offsets, order, y, G, M, N, K, share, workspace,
                   workspace_bytes, w_bytes, stream)
+
+
+def q4_route_groups(logits, bias, ids, weights, offsets, order, T: int, E: int, top_k: int,
+                    score: int = Q4_SCORE_SIGMOID, n_groups: int = 1, top_groups: int = 1,
+                    group_best: int = 1, renorm: bool = True, scale: float = 1.0, workspace=None,
+                    workspace_bytes=None, stream=None) -> None:
+    """Router with scores, a bias and groups: the top_k experts by s + ``bias``
+    (f32 [E], or None) among the best ``top_groups`` of ``n_groups`` groups of
+    neighbouring experts, s the sigmoid or softmax scores of ``logits``; weights
+    scale * s, over their sum with ``renorm``. Outputs and workspace as q4_route."""
+    ws = workspace
+    if ws is None:
+        need = int(lib.q4_route_workspace_bytes(int(T), int(E), int(top_k)))
+        if need:
+            ws = _scratch(need, stream, ids)
+    if workspace_bytes is not None:
+        wsb = int(workspace_bytes)
+    else:
+        wsb = _nbytes(ws) if ws is not None and not isinstance(ws, int) else 0
+    slots = T * top_k
+    _check(lib.q4_route_groups(_array(logits, T * E, _F32), _array(bias, E, _F32), T, E, top_k, score,
+                               n_groups, top_groups, group_best, bool(renorm), scale,
+                               _array(ids, slots, _I32), _array(weights, slots, _F32),
+                               _array(offsets, E + 1, _I32), _array(order, slots, _I32), _addr(ws),
+                               wsb, _stream_for(stream, logits)), "q4_route_groups")
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+
+
+def _array(x, n: int, dtypes) -> int:
+    """Address of a dense device tensor of n elements of one of ``dtypes`` (or of
+    None, or of a plain address): the kernels go by the sizes given beside it."""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    if not x.is_cuda or x.dtype not in dtypes or x.numel() != n or not x.is_contiguous():
+        raise ValueError("expected a dense device tensor of %d elements of %s, got %s" % (
+            n, " or ".join(map(str, dtypes)), _what(x)))
+    return x.data_ptr()
+
+
+def _what(x) -> str:
+    return "%s of %s on %s, strides %s" % (tuple(x.shape), x.dtype, x.device, x.stride())
+
+
+def _stream_for(stream, x) -> int:
+    """_stream, where the work is x's: without a ``stream`` its device has to be
+    the current one, whose stream is taken."""
+    if stream is None and getattr(x, "is_cuda", False) and x.get_device() != torch._C._cuda_getDevice():
+        raise ValueError("the tensors are on %s, which is not the current device: make it current, or "
+                         "pass a stream" % x.device)
+    return _stream(stream)
+
+
+def _values(y, n: int):
+    """Address of f32 or bfloat16 values, and whether they are bfloat16."""
+    bf16 = not isinstance(y, int) and y is not None and y.dtype in _BF16
+    return _array(y, n, _BF16 if bf16 else _F32), bf16
+
+
+def _norm_inputs(x, gamma, M, K, dtypes, residual, sum, weights, share, eps):
+    n = M * K
+    return (_array(x, n * share, dtypes), _array(weights, M * share, _F32), share,
+            _array(residual, n, dtypes), _array(sum, n, dtypes), _array(gamma, K, _F32), eps)
+
+
+def q4_norm(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+            share: int = 1, y_bf16=None, stream=None) -> None:
+    """The residual's addition and the root-mean-square norm: h = ``residual`` +
+    sum_j weights[m, j] x[m share + j], written to ``sum`` (which may be
+    ``residual``), and ``y`` = h / sqrt(mean(h^2) + eps) * gamma in f32 or
+    bfloat16, by y's type (of an address: ``y_bf16``). ``x`` [M * share, K],
+    ``residual`` and ``sum`` [M, K] f32; ``weights`` [M, share] as q4_route writes
+    them, a weight of 0 leaving its row out; ``gamma`` [K] f32."""
+    at, bf16 = _values(y, M * K)
+    _check(lib.q4_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps), at,
+                       bf16 if y_bf16 is None else bool(y_bf16), M, K, _stream_for(stream, x)), "q4_norm")
+
+
+def q4_norm_bf16(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+                 share: int = 1, y_bf16=None, stream=None) -> None:
+    """As q4_norm with ``x``, ``residual`` and ``sum`` in bfloat16."""
+    at, bf16 = _values(y, M * K)
+    _check(lib.q4_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps), at,
+                            bf16 if y_bf16 is None else bool(y_bf16), M, K, _stream_for(stream, x)),
+           "q4_norm_bf16")
+
+
+def q8_norm(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+            share: int = 1, y=None, stream=None) -> None:
+    """q4_norm with the result as Q8_0 blocks in the uint8 tensor ``out_q``, and in
+    f32 in ``y`` as well where that is given."""
+    nb = M * (K // 32) * 34
+    _check(lib.q8_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps),
+                       _array(y, M * K, _F32), _array(out_q, nb, _BYTES), nb, M, K,
+                       _stream_for(stream, x)), "q8_norm")
+
+
+def q8_norm_bf16(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+                 share: int = 1, y=None, stream=None) -> None:
+    """As q8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
+    nb = M * (K // 32) * 34
+    _check(lib.q8_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps),
+                            _array(y, M * K, _BF16), _array(out_q, nb, _BYTES), nb, M, K,
+                            _stream_for(stream, x)), "q8_norm_bf16")
+
+
+def f8_norm(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+            share: int = 1, y=None, stream=None) -> None:
+    """q4_norm with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
+    columns, ``s`` [M, ceil(K / 128)], and in f32 in ``y`` as well where that is
+    given."""
+    ns = M * -(-K // 128)
+    _check(lib.f8_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps),
+                       _array(y, M * K, _F32), _array(q, M * K, _BYTES), M * K, _array(s, ns, _F32), ns,
+                       M, K, _stream_for(stream, x)), "f8_norm")
+
+
+def f8_norm_bf16(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
+                 share: int = 1, y=None, stream=None) -> None:
+    """As f8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
+    ns = M * -(-K // 128)
+    _check(lib.f8_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps),
+                            _array(y, M * K, _BF16), _array(q, M * K, _BYTES), M * K,
+                            _array(s, ns, _F32), ns, M, K, _stream_for(stream, x)), "f8_norm_bf16")
+
+
+def _halves(gate, up, M, K, dtypes, ld):
+    """Addresses and row distance of [M, K] views whose rows are dense."""
+    if isinstance(gate, int):
+        return gate, 0 if up is None else up, K if ld is None else ld
+    for t in (gate, up):
+        if t is not None and (not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != M
+                              or t.shape[1] != K or t.stride(1) != 1
+                              or (M > 1 and t.stride(0) != gate.stride(0))):
+            raise ValueError("expected [%d, %d] device tensors of %s with dense rows at the same distance, "
+                             "got %s" % (M, K, " or ".join(map(str, dtypes)), _what(t)))
+    return gate.data_ptr(), 0 if up is None else up.data_ptr(), gate.stride(0) if M > 1 else K
+
+
+def q4_act(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=None, ld=None, stream=None) -> None:
+    """The gated activation y = f(gate) * up, f SiLU or GELU (tanh form), in f32 or
+    bfloat16 by y's type. ``gate`` and ``up`` are f32 [M, K] views with dense
+    rows, the halves of one product's rows or two products' results (of
+    addresses: ``ld`` elements a row); ``up`` may be None."""
+    at, bf16 = _values(y, M * K)
+    g, u, ld = _halves(gate, up, M, K, _F32, ld)
+    _check(lib.q4_act(g, u, ld, act, at, bf16 if y_bf16 is None else bool(y_bf16), M, K,
+                      _stream_for(stream, gate)), "q4_act")
+
+
+def q4_act_bf16(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=None, ld=None,
+                stream=None) -> None:
+    """As q4_act with ``gate`` and ``up`` in bfloat16."""
+    at, bf16 = _values(y, M * K)
+    g, u, ld = _halves(gate, up, M, K, _BF16, ld)
+    _check(lib.q4_act_bf16(g, u, ld, act, at, bf16 if y_bf16 is None else bool(y_bf16), M, K,
+                           _stream_for(stream, gate)), "q4_act_bf16")
+
+
+def _q8_act(entry, gate, up, out_q, M, K, act, dtypes, ld, stream) -> None:
+    nb = M * (K // 32) * 34
+    g, u, ld = _halves(gate, up, M, K, dtypes, ld)
+    _check(getattr(lib, entry)(g, u, ld, act, _array(out_q, nb, _BYTES), nb, M, K,
+                               _stream_for(stream, gate)), entry)
+
+
+def q8_act(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
+    """q4_act with the result as Q8_0 blocks in the uint8 tensor ``out_q``."""
+    _q8_act("q8_act", gate, up, out_q, M, K, act, _F32, ld, stream)
+
+
+def q8_act_bf16(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
+    """As q8_act with ``gate`` and ``up`` in bfloat16."""
+    _q8_act("q8_act_bf16", gate, up, out_q, M, K, act, _BF16, ld, stream)
+
+
+def _f8_act(entry, gate, up, q, s, M, K, act, dtypes, ld, stream) -> None:
+    ns = M * -(-K // 128)
+    g, u, ld = _halves(gate, up, M, K, dtypes, ld)
+    _check(getattr(lib, entry)(g, u, ld, act, _array(q, M * K, _BYTES), M * K, _array(s, ns, _F32), ns,
+                               M, K, _stream_for(stream, gate)), entry)
+
+
+def f8_act(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
+    """q4_act with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
+    columns, ``s`` [M, ceil(K / 128)]."""
+    _f8_act("f8_act", gate, up, q, s, M, K, act, _F32, ld, stream)
+
+
+def f8_act_bf16(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
+    """As f8_act with ``gate`` and ``up`` in bfloat16."""
+    _f8_act("f8_act_bf16", gate, up, q, s, M, K, act, _BF16, ld, stream)
 
 
 def raw_status(entry: str, *args) -> int:

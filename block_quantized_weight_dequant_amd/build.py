@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libq4.so")
 PROBE_LIB = os.path.join(PKG, "libq4probe.so")
 
 SOURCES = ["abi.cpp", "validate.cpp", "dequant.hip", "quantize.hip", "gemv.hip", "gemm.hip", "f8.hip",
-           "route.hip", "grouped.hip"]
+           "route.hip", "grouped.hip", "norm.hip", "act.hip"]
 PROBE_SOURCES = ["probe/stream_read.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

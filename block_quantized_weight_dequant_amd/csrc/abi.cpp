@@ -466,12 +466,31 @@ Q4_EXPORT int q4_route(const float *logits, int T, int E, int top_k, int renorm,
                        size_t workspace_bytes, void *stream)
 {
     bool empty = false;
-    int st = q4v::check_route(logits, T, E, top_k, ids, weights, offsets, order, workspace,
+    int st = q4v::check_route(logits, nullptr, T, E, top_k, ids, weights, offsets, order, workspace,
                               workspace_bytes, q4v::route_workspace_bytes(T, E, top_k), &empty);
     if (st != Q4_OK || empty)
         return st;
     return launched(q4k::launch_route(logits, ids, weights, offsets, order, workspace, T, E, top_k,
                                       renorm != 0, as_stream(stream)));
+}
+
+Q4_EXPORT int q4_route_groups(const float *logits, const float *bias, int T, int E, int top_k, int score,
+                              int n_groups, int top_groups, int group_best, int renorm, float scale,
+                              int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = q4v::check_route_groups(E, top_k, score, n_groups, top_groups, group_best, scale);
+    if (st != Q4_OK)
+        return st;
+    bool empty = false;
+    st = q4v::check_route(logits, bias, T, E, top_k, ids, weights, offsets, order, workspace,
+                          workspace_bytes, q4v::route_workspace_bytes(T, E, top_k), &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    const q4k::RouteGroups g = {bias, score == Q4_SCORE_SIGMOID, renorm != 0, n_groups, top_groups,
+                                group_best, scale};
+    return launched(q4k::launch_route_groups(logits, g, ids, weights, offsets, order, workspace, T, E,
+                                             top_k, as_stream(stream)));
 }
 
 static int gemm_grouped(q4k::WeightFormat fmt, size_t block_bytes, bool bf16, const void *a,
@@ -576,4 +595,129 @@ Q4_EXPORT int f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t 
         return st;
     return launched(q4k::launch_f8_gemm_grouped(a, a_s, w, w_s, offsets, order, share, y, G, M, N, K,
                                                 as_stream(stream)));
+}
+
+// The norms: `out` says the form's pointers and sizes.
+static int norm(bool bf16, q4k::RowForm form, const q4v::RowsOut &out, const void *x, const float *weights,
+                int share, const void *residual, void *sum, const float *gamma, float eps, void *dense,
+                void *y, float *s, int M, int K, void *stream)
+{
+    const q4v::NormCheck c = {x, weights, share, residual, sum, gamma, eps, dense, out, M, K, bf16 ? 2u : 4u};
+    bool empty = false;
+    int st = q4v::check_norm(c, &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    const q4k::NormArgs a = {x, weights, share, residual, sum, gamma, eps, dense, {y, s}, M, K};
+    return launched(q4k::launch_norm(bf16, form, a, as_stream(stream)));
+}
+
+static int norm_values(bool bf16, const void *x, const float *weights, int share, const void *residual,
+                       void *sum, const float *gamma, float eps, void *y, int y_bf16, int M, int K, void *stream)
+{
+    return norm(bf16, y_bf16 ? q4k::RowForm::kBf16 : q4k::RowForm::kF32, {y, y_bf16 ? 2u : 4u, false, 0, nullptr, 0},
+                x, weights, share, residual, sum, gamma, eps, nullptr, y, nullptr, M, K, stream);
+}
+
+Q4_EXPORT int q4_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+                      const float *gamma, float eps, void *y, int y_bf16, int M, int K, void *stream)
+{
+    return norm_values(false, x, weights, share, residual, sum, gamma, eps, y, y_bf16, M, K, stream);
+}
+
+Q4_EXPORT int q4_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                           uint16_t *sum, const float *gamma, float eps, void *y, int y_bf16, int M, int K,
+                           void *stream)
+{
+    return norm_values(true, x, weights, share, residual, sum, gamma, eps, y, y_bf16, M, K, stream);
+}
+
+Q4_EXPORT int q8_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+                      const float *gamma, float eps, float *y, void *out_q, size_t out_bytes, int M, int K,
+                      void *stream)
+{
+    return norm(false, q4k::RowForm::kQ8_0, {out_q, 0, false, out_bytes, nullptr, 0}, x, weights, share, residual,
+                sum, gamma, eps, y, out_q, nullptr, M, K, stream);
+}
+
+Q4_EXPORT int q8_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                           uint16_t *sum, const float *gamma, float eps, uint16_t *y, void *out_q,
+                           size_t out_bytes, int M, int K, void *stream)
+{
+    return norm(true, q4k::RowForm::kQ8_0, {out_q, 0, false, out_bytes, nullptr, 0}, x, weights, share, residual,
+                sum, gamma, eps, y, out_q, nullptr, M, K, stream);
+}
+
+Q4_EXPORT int f8_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+                      const float *gamma, float eps, float *y, void *q, size_t q_bytes, float *s,
+                      size_t s_elems, int M, int K, void *stream)
+{
+    return norm(false, q4k::RowForm::kE4M3, {q, 0, true, q_bytes, s, s_elems}, x, weights, share, residual, sum,
+                gamma, eps, y, q, s, M, K, stream);
+}
+
+Q4_EXPORT int f8_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                           uint16_t *sum, const float *gamma, float eps, uint16_t *y, void *q, size_t q_bytes,
+                           float *s, size_t s_elems, int M, int K, void *stream)
+{
+    return norm(true, q4k::RowForm::kE4M3, {q, 0, true, q_bytes, s, s_elems}, x, weights, share, residual, sum,
+                gamma, eps, y, q, s, M, K, stream);
+}
+
+static int act_rows(bool bf16, q4k::RowForm form, const q4v::RowsOut &out, const void *gate, const void *up, int ld,
+                    int act, void *y, float *s, int M, int K, void *stream)
+{
+    const q4v::ActCheck c = {gate, up, ld, act, out, M, K, bf16 ? 2u : 4u};
+    bool empty = false;
+    int st = q4v::check_act(c, &empty);
+    if (st != Q4_OK || empty)
+        return st;
+    const q4k::ActArgs a = {gate, up, ld, act, {y, s}, M, K};
+    return launched(q4k::launch_act(bf16, form, a, as_stream(stream)));
+}
+
+static int act_values(bool bf16, const void *gate, const void *up, int ld, int act, void *y, int y_bf16, int M,
+                      int K, void *stream)
+{
+    return act_rows(bf16, y_bf16 ? q4k::RowForm::kBf16 : q4k::RowForm::kF32,
+                    {y, y_bf16 ? 2u : 4u, false, 0, nullptr, 0}, gate, up, ld, act, y, nullptr, M, K, stream);
+}
+
+Q4_EXPORT int q4_act(const float *gate, const float *up, int ld, int act, void *y, int y_bf16, int M, int K,
+                     void *stream)
+{
+    return act_values(false, gate, up, ld, act, y, y_bf16, M, K, stream);
+}
+
+Q4_EXPORT int q4_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *y, int y_bf16, int M,
+                          int K, void *stream)
+{
+    return act_values(true, gate, up, ld, act, y, y_bf16, M, K, stream);
+}
+
+Q4_EXPORT int q8_act(const float *gate, const float *up, int ld, int act, void *out_q, size_t out_bytes, int M,
+                     int K, void *stream)
+{
+    return act_rows(false, q4k::RowForm::kQ8_0, {out_q, 0, false, out_bytes, nullptr, 0}, gate, up, ld, act, out_q,
+                    nullptr, M, K, stream);
+}
+
+Q4_EXPORT int q8_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *out_q,
+                          size_t out_bytes, int M, int K, void *stream)
+{
+    return act_rows(true, q4k::RowForm::kQ8_0, {out_q, 0, false, out_bytes, nullptr, 0}, gate, up, ld, act, out_q,
+                    nullptr, M, K, stream);
+}
+
+Q4_EXPORT int f8_act(const float *gate, const float *up, int ld, int act, void *q, size_t q_bytes, float *s,
+                     size_t s_elems, int M, int K, void *stream)
+{
+    return act_rows(false, q4k::RowForm::kE4M3, {q, 0, true, q_bytes, s, s_elems}, gate, up, ld, act, q, s, M, K,
+                    stream);
+}
+
+Q4_EXPORT int f8_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *q, size_t q_bytes,
+                          float *s, size_t s_elems, int M, int K, void *stream)
+{
+    return act_rows(true, q4k::RowForm::kE4M3, {q, 0, true, q_bytes, s, s_elems}, gate, up, ld, act, q, s, M, K,
+                    stream);
 }

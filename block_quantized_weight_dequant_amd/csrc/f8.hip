@@ -12,13 +12,12 @@
 #include "f8_forms.h"
 #include "groups.h"
 #include "launch.h"
+#include "rows_out.h"
 
 namespace q4k {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-
-constexpr float kE4M3Max = 448.0f;
 
 // ---------------------------------------------------------------------------
 // Quantize. Per block: s = max|x| / 448 in f32, code = the E4M3 value nearest
@@ -29,9 +28,6 @@ constexpr float kE4M3Max = 448.0f;
 // Bound by the bytes of x: 16 lanes share a block of a row, eight elements
 // each, so a wavefront reads four blocks (2 KB of f32) and writes 512 bytes
 // of codes in whole lines, and the maximum crosses 16 lanes in four DPP moves.
-
-__device__ __forceinline__ float f32_of(float v) { return v; }
-__device__ __forceinline__ float f32_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 template <class T>
 struct Eight {
@@ -68,48 +64,11 @@ struct Eight {
     }
     __device__ __forceinline__ u32x2 codes(float s) const
     {
-        float q[8];
-        if (s >= 0x1p-90f && s <= 0x1p90f) {
-            // The correctly rounded quotient from the correctly rounded
-            // reciprocal: each step takes the exact remainder (an FMA), the
-            // first to within a unit in the last place, the second to the
-            // nearest (Markstein's theorem). No intermediate leaves the normal
-            // range here but where the quotient is far below the smallest
-            // code. No clamp: 448 + 2^-15 at most, which the conversion rounds
-            // to 448 as it rounds all below 464. The remainder of -0 is
-            // +0, which would lose its sign: the quotient takes x's. Six
-            // operations an element; a division takes about twice that.
-            const float r = 1.0f / s;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q0 = v[i] * r;
-                const float q1 = fmaf(fmaf(-q0, s, v[i]), r, q0);
-                q[i] = __builtin_copysignf(fmaf(fmaf(-q1, s, v[i]), r, q1), v[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                q[i] = s == 0.0f ? 0.0f : fminf(fmaxf(v[i] / s, -kE4M3Max), kE4M3Max);
-        }
-        u32x2 r;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int x = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
-            r[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], x, true);
-        }
-        return r;
+        uint32_t w[2];
+        e4m3_codes(v, s, w);
+        return (u32x2){w[0], w[1]};
     }
 };
-
-// Largest over each 16 lanes, in every one of them.
-__device__ __forceinline__ float max16(float v)
-{
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));    // quad_perm 1,0,3,2
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));    // quad_perm 2,3,0,1
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));   // row_half_mirror
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));   // row_mirror
-    return v;
-}
 
 // One scale per 128 columns of a row: 16 blocks per 256-thread workgroup, one a
 // thread group (2048 x 4096 bfloat16: 6.4 us, 3.9 TB/s; two or four blocks in
@@ -129,7 +88,7 @@ __global__ __launch_bounds__(256) void k_f8_quantize_rows(const T *__restrict__ 
     Eight<T> v;
     v.load(x + at);
     v.clear_if(!in);
-    const float sc = max16(v.amax()) / kE4M3Max;
+    const float sc = lanes_max<16>(v.amax()) / kE4M3Max;
     if (in)
         *reinterpret_cast<u32x2 *>(q + at) = v.codes(sc);
     if (p == 0)
@@ -162,7 +121,7 @@ __global__ __launch_bounds__(256) void k_f8_quantize_tiles(const T *__restrict__
         v[i].clear_if(!col_in || row0 + 16 * i >= M);
         m = fmaxf(m, v[i].amax());
     }
-    m = max16(m);
+    m = lanes_max<16>(m);
     m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
     if ((tid & 63) == 0)

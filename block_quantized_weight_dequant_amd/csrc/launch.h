@@ -72,6 +72,46 @@ hipError_t launch_f8_gemm(const uint8_t *a, const float *a_s, const uint8_t *w, 
 // The router. workspace: q4v::route_workspace_bytes(T, E, top_k) bytes.
 hipError_t launch_route(const float *logits, int *ids, float *weights, int *offsets, int *order,
                         void *workspace, int T, int E, int top_k, bool renorm, hipStream_t st);
+// The router with scores, a bias and groups of experts; the same workspace.
+struct RouteGroups {
+    const float *bias;   // [E], or null
+    bool sigmoid, renorm;
+    int n_groups, top_groups, group_best;
+    float scale;
+};
+hipError_t launch_route_groups(const float *logits, const RouteGroups &g, int *ids, float *weights,
+                               int *offsets, int *order, void *workspace, int T, int E, int top_k,
+                               hipStream_t st);
+// A row of results in the form that the next product reads.
+enum class RowForm { kF32, kBf16, kQ8_0, kE4M3 };
+struct RowOut {
+    void *y;    // values, blocks or codes
+    float *s;   // E4M3: the scales
+};
+// The norm of the residual stream. x, residual, sum and dense in f32 or bfloat16
+// (bf16); weights, residual, sum and dense may be null, sum may be residual.
+struct NormArgs {
+    const void *x;
+    const float *weights;
+    int share;
+    const void *residual;
+    void *sum;
+    const float *gamma;
+    float eps;
+    void *dense;
+    RowOut out;
+    int M, K;
+};
+hipError_t launch_norm(bool bf16, RowForm form, const NormArgs &a, hipStream_t st);
+// The gated activation. gate and up in f32 or bfloat16, rows ld elements apart; up
+// may be null.
+struct ActArgs {
+    const void *gate, *up;
+    int ld, act;
+    RowOut out;
+    int M, K;
+};
+hipError_t launch_act(bool bf16, RowForm form, const ActArgs &a, hipStream_t st);
 // The grouped products over Q4_0 and Q8_0 weights: f32 or bfloat16 (bf16)
 // activations; order may be null. workspace: q4v::grouped_workspace_bytes.
 hipError_t launch_gemm_grouped(WeightFormat fmt, bool bf16, const void *a, const uint8_t *w,

@@ -1,0 +1,188 @@
+// The residual's addition and the root-mean-square norm before a product:
+//   h = residual + sum_j w_j x_j,  y = h / sqrt(mean(h^2) + eps) * gamma,
+// with y in the form the product reads (rows_out.h) and h as the next residual.
+//
+// Bound by bytes when there are many rows and by latency when there are few, so
+// a row is read once: RW wavefronts hold it in registers, V 16-byte pieces a
+// lane, between the sum of its squares and its results. Wavefront w's lane l
+// takes pieces (i RW + w) 64 + l, so that a wavefront reads whole lines.
+//
+// The experts' rows are added in f64 (products of two f32 are exact there, so h
+// is the exact sum rounded once but for sums that cancel past 2^-53), and so are
+// the squares: two full-rate f64 operations an element, a fortieth of the time
+// its bytes take, and the result does not depend on the order of the sums but in
+// one row of some 10^7.
+#include "f64.h"
+#include "launch.h"
+#include "rows_out.h"
+
+namespace q4k {
+
+template <class T, RowForm O, bool COMBINE, int RW, int V>
+__global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, double inv_k, int first)
+{
+    constexpr int P = kPiece<T>, ROWS = RW < 4 ? 4 / RW : 1;
+    __shared__ double part[ROWS][RW];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int w = wave % RW, slot = wave / RW;
+    const long long want = ((long long)blockIdx.x + first) * ROWS + slot;
+    const size_t row = (size_t)(want < a.M ? want : a.M - 1);   // the last rows' spare wavefronts write nothing
+    const bool live = want < a.M;
+
+    const T *x = static_cast<const T *>(a.x) + row * (size_t)a.share * (size_t)a.K;
+    // Without a residual its loads repeat x's: unconditional loads stay in flight together.
+    const T *res = a.residual ? static_cast<const T *>(a.residual) + row * (size_t)a.K : x;
+    int col[V];
+    bool in[V];
+    float h[V][P], gamma[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = ((i * RW + w) * 64 + lane) * P;
+        in[i] = c < a.K;
+        col[i] = in[i] ? c : 0;
+    }
+    if constexpr (COMBINE) {
+        double acc[V][P];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float r[P];
+            load_piece(res + col[i], r);
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                acc[i][k] = a.residual ? (double)r[k] : 0.0;
+        }
+        const float *weights = a.weights ? a.weights + row * (size_t)a.share : nullptr;
+#pragma unroll 2
+        for (int j = 0; j < a.share; ++j) {
+            const float wj = weights ? weights[j] : 1.0f;
+            const T *xj = x + (size_t)j * (size_t)a.K;
+            float v[V][P];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                load_piece(xj + col[i], v[i]);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    acc[i][k] = fma((double)wj, (double)(wj == 0.0f ? 0.0f : v[i][k]), acc[i][k]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                h[i][k] = (float)acc[i][k];
+    } else {
+        float r[V][P];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            load_piece(x + col[i], h[i]);
+            load_piece(res + col[i], r[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                h[i][k] = a.residual ? h[i][k] + r[i][k] : h[i][k];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int q = 0; q < P / 4; ++q) {
+            const f32x4 g = *reinterpret_cast<const f32x4 *>(a.gamma + col[i] + 4 * q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                gamma[i][4 * q + k] = g[k];
+        }
+
+    double sq = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            h[i][k] = in[i] ? h[i][k] : 0.0f;
+            sq = fma((double)h[i][k], (double)h[i][k], sq);
+        }
+    sq = wave_sum_f64(sq);
+    if constexpr (RW > 1) {
+        if (lane == 0)
+            part[slot][w] = sq;
+        __syncthreads();
+        sq = part[slot][0];
+#pragma unroll
+        for (int k = 1; k < RW; ++k)
+            sq += part[slot][k];
+    }
+    const double ms = fma(sq, inv_k, (double)a.eps);
+    const float rstd = ms > 0.0 ? (float)rsqrt_f64(ms) : 0.0f;
+
+    if (a.sum && live) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (in[i])
+                store_piece(static_cast<T *>(a.sum) + row * (size_t)a.K + col[i], h[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+            h[i][k] = h[i][k] * rstd * gamma[i][k];
+        if (a.dense && live && in[i])
+            store_piece(static_cast<T *>(a.dense) + row * (size_t)a.K + col[i], h[i]);
+        put_piece<O>(a.out, a.K, h[i], in[i] && live, row, col[i]);
+    }
+}
+
+template <class T, RowForm O, bool COMBINE, int RW, int V>
+static hipError_t launch_rows(const NormArgs &a, hipStream_t st)
+{
+    constexpr int ROWS = RW < 4 ? 4 / RW : 1;
+    return launch_parts(k_norm<T, O, COMBINE, RW, V>, ((long long)a.M + ROWS - 1) / ROWS, 1, RW < 4 ? 256 : 64 * RW,
+                        st, a, 1.0 / a.K);
+}
+
+template <class T, RowForm O, bool COMBINE>
+static hipError_t launch_width(const NormArgs &a, hipStream_t st)
+{
+    const int waves = (a.K / kPiece<T> + 63) / 64;   // wavefronts of one piece a lane
+    if (waves <= 1)
+        return launch_rows<T, O, COMBINE, 1, 1>(a, st);
+    if (waves <= 2)
+        return launch_rows<T, O, COMBINE, 2, 1>(a, st);
+    if (waves <= 4)
+        return launch_rows<T, O, COMBINE, 4, 1>(a, st);
+    if (waves <= 8)
+        return launch_rows<T, O, COMBINE, 8, 1>(a, st);
+    if (waves <= 16)
+        return launch_rows<T, O, COMBINE, 16, 1>(a, st);
+    if (waves <= 32)
+        return launch_rows<T, O, COMBINE, 16, 2>(a, st);
+    if (waves <= 64)
+        return launch_rows<T, O, COMBINE, 16, 4>(a, st);
+    if constexpr (kPiece<T> == 4)
+        return launch_rows<T, O, COMBINE, 16, 8>(a, st);
+    return hipErrorInvalidValue;
+}
+
+template <class T, RowForm O>
+static hipError_t launch_form(const NormArgs &a, hipStream_t st)
+{
+    return a.share > 1 || a.weights ? launch_width<T, O, true>(a, st) : launch_width<T, O, false>(a, st);
+}
+
+template <class T>
+static hipError_t launch_type(RowForm form, const NormArgs &a, hipStream_t st)
+{
+    switch (form) {
+    case RowForm::kF32: return launch_form<T, RowForm::kF32>(a, st);
+    case RowForm::kBf16: return launch_form<T, RowForm::kBf16>(a, st);
+    case RowForm::kQ8_0: return launch_form<T, RowForm::kQ8_0>(a, st);
+    default: return launch_form<T, RowForm::kE4M3>(a, st);
+    }
+}
+
+hipError_t launch_norm(bool bf16, RowForm form, const NormArgs &a, hipStream_t st)
+{
+    return bf16 ? launch_type<uint16_t>(form, a, st) : launch_type<float>(form, a, st);
+}
+
+}  // namespace q4k

@@ -18,7 +18,13 @@
 // their rank from ballots over the bits of the expert (lanes with the same
 // expert, those before mine). Up to 64 tokens one workgroup does all of
 // it in one launch.
-#include "device_common.h"
+//
+// With scores, a bias and groups (q4_route_groups) the keys are f64, s + bias, and
+// so are the groups' sums: scores that differ in f32's last place would come out
+// in either order, and two f64 roundings almost never. s takes some 25 f64
+// operations an expert. A step of the selection then compares the keys' upper
+// halves, and the lower ones only where several experts share the largest.
+#include "f64.h"
 #include "launch.h"
 #include "validate.h"
 
@@ -120,10 +126,15 @@ __device__ __forceinline__ void route_tokens(const float *__restrict__ logits, i
     }
 }
 
+// W: keys of a wavefront's token in expert order, where groups are ranked.
+template <int W = 1>
 struct RouteLds {
-    int cursor[kMaxExperts];                      // next position of each expert
+    int cursor[kMaxExperts];                          // next position of each expert
     int part[kRouteWaves];
-    uint16_t waves[kRouteWaves][kMaxExperts];     // slots of a batch, by wavefront and expert
+    union {
+        uint16_t waves[kRouteWaves][kMaxExperts];     // slots of a batch, by wavefront and expert
+        double vals[kRouteWaves][W];                  // not needed any more when slots are placed
+    };
 };
 
 // Exclusive prefix sum over the workgroup's threads.
@@ -150,8 +161,8 @@ __device__ __forceinline__ int exclusive_scan(int v, int *part)
 // Place slots s0 .. s0 + n - 1, whose experts expert(0) .. expert(n - 1) are
 // (below E; bits: of an expert number). Thread e < E passes the first position
 // of its expert in `at`.
-template <class Fn>
-__device__ __forceinline__ void place(RouteLds &l, Fn expert, int s0, int n, int E, int bits, int at,
+template <class Lds, class Fn>
+__device__ __forceinline__ void place(Lds &l, Fn expert, int s0, int n, int E, int bits, int at,
                                       int *__restrict__ order)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -194,18 +205,15 @@ using q4v::route_chunk;
 using q4v::route_chunks;
 constexpr int kOneChunk = q4v::kRouteOneChunk;
 
-// counts: [chunks][E], or null when one workgroup does all of it.
-template <int V>
-__global__ __launch_bounds__(kRouteThreads) void k_route(const float *__restrict__ logits,
-                                                        int *__restrict__ ids,
-                                                        float *__restrict__ weights,
-                                                        int *__restrict__ offsets,
-                                                        int *__restrict__ order,
-                                                        int *__restrict__ counts, int T, int E,
-                                                        int top_k, int renorm, int chunk, int bits)
+// One workgroup's chunk: tokens(tok, n, to) chooses the experts of n tokens (the
+// second tok repeats another if n is 1) and leaves the choices of the u-th at
+// to(u). counts: [chunks][E], or null when one workgroup does all of it.
+template <class Lds, class Tokens>
+__device__ __forceinline__ void route_workgroup(Lds &l, uint16_t *s_ids, Tokens tokens,
+                                                int *__restrict__ offsets, int *__restrict__ order,
+                                                int *__restrict__ counts, int T, int E, int top_k,
+                                                int chunk, int bits)
 {
-    __shared__ RouteLds l;
-    __shared__ uint16_t s_ids[kOneChunk * kMaxTopK];   // at least two tokens a wavefront
     const int tid = threadIdx.x, wave = tid >> 6;
     if (tid < E)
         l.cursor[tid] = 0;
@@ -217,7 +225,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const float *__restrict
         auto to = [&](int u) __attribute__((always_inline)) {
             return s_ids + (counts ? (wave * 2 + u) * kMaxTopK : (tok[u] - t0) * top_k);
         };
-        route_tokens<V>(logits, E, top_k, renorm, ids, weights, tok, n, to);
+        tokens(tok, n, to);
         __builtin_amdgcn_wave_barrier();
         for (int u = 0; u < n; ++u)
             if ((tid & 63) < top_k)
@@ -238,6 +246,237 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const float *__restrict
     place(l, [&](int i) { return (int)s_ids[i]; }, 0, T * top_k, E, bits, at, order);
 }
 
+template <int V>
+__global__ __launch_bounds__(kRouteThreads) void k_route(const float *__restrict__ logits,
+                                                        int *__restrict__ ids,
+                                                        float *__restrict__ weights,
+                                                        int *__restrict__ offsets,
+                                                        int *__restrict__ order,
+                                                        int *__restrict__ counts, int T, int E,
+                                                        int top_k, int renorm, int chunk, int bits)
+{
+    __shared__ RouteLds<> l;
+    __shared__ uint16_t s_ids[kOneChunk * kMaxTopK];   // at least two tokens a wavefront
+    const auto tokens = [&](const int (&tok)[2], int n, auto to) __attribute__((always_inline)) {
+        route_tokens<V>(logits, E, top_k, renorm, ids, weights, tok, n, to);
+    };
+    route_workgroup(l, s_ids, tokens, offsets, order, counts, T, E, top_k, chunk, bits);
+}
+
+// An expert's place in the order of choice: larger first. 0 takes no part, 1 (a
+// masked expert) comes last; f64 keys, in two halves, are larger.
+struct Key {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Key f64_key(double v)
+{
+    const u32x2 b = bitcast<u32x2>(v + 0.0);   // -0 as +0
+    const uint32_t flip = (uint32_t)((int)b.y >> 31);
+    return {b.y ^ (flip | 0x80000000u), b.x ^ flip};
+}
+
+// What a wavefront keeps of its V experts lane + 64 i for all its tokens.
+template <int V>
+struct Experts {
+    float bias[V];
+    int bit[V];   // the first lane of the expert's group
+};
+
+// 2^lanes lanes rank a group's experts: as many as n_groups leave of the 64.
+template <int V, bool GROUPED>
+__device__ __forceinline__ Experts<V> load_experts(const RouteGroups &g, int E, int lanes)
+{
+    Experts<V> x;
+    const int size = E / g.n_groups;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = min((int)(threadIdx.x & 63) + 64 * i, E - 1);
+        x.bias[i] = g.bias ? g.bias[e] : 0.0f;
+        x.bit[i] = GROUPED ? (e / size) << lanes : 0;
+    }
+    return x;
+}
+
+// The groups of one token that can be chosen: bits at their first lanes. vals:
+// the wavefront's E keys in expert order, masked ones -inf.
+__device__ __forceinline__ uint64_t best_groups(const double *vals, const RouteGroups &g, int E, int lanes)
+{
+    const int lane = threadIdx.x & 63, size = E / g.n_groups, mine = lane >> lanes, step = 1 << lanes;
+    const double none = -__builtin_inf();
+    double first = none, second = none;
+    if (mine < g.n_groups)
+        for (int k = lane & (step - 1); k < size; k += step) {
+            const double v = vals[mine * size + k];
+            second = fmax(second, fmin(first, v));
+            first = fmax(first, v);
+        }
+    for (int d = 1; d < step; d <<= 1) {
+        const double f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+        second = fmax(fmin(first, f), fmax(second, s));
+        first = fmax(first, f);
+    }
+    const double score = g.group_best == 2 ? first + second : first;
+    int rank = 0;
+    for (int j = 0; j < g.n_groups; ++j) {
+        const double other = readlane_f64(score, j << lanes);
+        rank += other > score || (other == score && j < mine);
+    }
+    return __ballot(mine < g.n_groups && rank < g.top_groups);
+}
+
+// Tokens tok[0 .. U - 1] by one wavefront; lane j < top_k ends with choice j.
+template <int V, int U, bool GROUPED, class Ids>
+__device__ __forceinline__ void choose_tokens(const float *__restrict__ logits, const RouteGroups &g,
+                                              const Experts<V> &x, double *vals, int lanes, int E,
+                                              int top_k, int *__restrict__ ids,
+                                              float *__restrict__ weights, const int *tok, int n, Ids s_ids)
+{
+    const int lane = threadIdx.x & 63;
+    const float ninf = -__builtin_inff();
+    float v[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[u][i] = logits[(size_t)tok[u] * (size_t)E + min(lane + 64 * i, E - 1)];
+
+    double s[U][V], my_s[U];
+    Key key[U][V];
+    int my_id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        bool there[V];   // an expert, and not masked (NaN masks)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            there[i] = lane + 64 * i < E && v[u][i] > ninf;
+        if (g.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const double z = fmin(fmax((double)v[u][i], -700.0), 700.0);
+                s[u][i] = there[i] ? rcp_f64(1.0 + exp_f64(-z)) : 0.0;
+            }
+        } else {
+            uint32_t m = logit_key(ninf);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                m = max(m, there[i] ? logit_key(v[u][i]) : 0u);
+            const double mx = (double)key_logit(wave_max_u32(m));
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const double e = exp_f64(fmax((double)v[u][i] - mx, -700.0));
+                s[u][i] = there[i] ? e : 0.0;
+                sum += s[u][i];
+            }
+            const double r = rcp_f64(fmax(wave_sum_f64(sum), 0x1p-1000));
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                s[u][i] *= r;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const double k = s[u][i] + (double)x.bias[i];
+            there[i] = there[i] && x.bias[i] > ninf;
+            key[u][i] = there[i] ? f64_key(k) : Key{0u, lane + 64 * i < E ? 1u : 0u};
+            if (GROUPED && lane + 64 * i < E)
+                vals[lane + 64 * i] = there[i] ? k : -__builtin_inf();
+        }
+        if constexpr (GROUPED) {
+            __builtin_amdgcn_wave_barrier();
+            const uint64_t kept = best_groups(vals, g, E, lanes);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (!(kept >> x.bit[i] & 1))
+                    key[u][i] = {0u, 0u};
+        }
+        my_id[u] = 0;
+        my_s[u] = 0.0;
+    }
+
+    for (int j = 0; j < top_k; ++j) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t m = key[u][0].hi;
+#pragma unroll
+            for (int i = 1; i < V; ++i)
+                m = max(m, key[u][i].hi);
+            const uint32_t best = wave_max_u32(m);
+            uint64_t has[V];
+            int many = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                has[i] = __ballot(key[u][i].hi == best);
+                many += __popcll(has[i]);
+            }
+            if (many > 1) {
+                m = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    m = max(m, key[u][i].hi == best ? key[u][i].lo : 0u);
+                const uint32_t low = wave_max_u32(m);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    has[i] = __ballot(key[u][i].hi == best && key[u][i].lo == low);
+            }
+            // The lowest expert: the first i in which any lane has it, and there the lowest lane.
+            int id = -1;
+            double sel = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (id < 0 && has[i]) {
+                    const int l = __builtin_ctzll(has[i]);
+                    id = 64 * i + l;
+                    sel = readlane_f64(s[u][i], l);
+                    if (lane == l)
+                        key[u][i] = {0u, 0u};
+                }
+            if (lane == j) {
+                my_id[u] = id;
+                my_s[u] = best ? sel : 0.0;   // 0: masked
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const double total = wave_sum_f64(my_s[u]);
+        const double w = g.renorm ? (total > 0.0 ? my_s[u] * rcp_f64(total) : 0.0) : my_s[u];
+        if (u < n && lane < top_k) {
+            const size_t at = (size_t)tok[u] * (size_t)top_k + lane;
+            ids[at] = my_id[u];
+            weights[at] = (float)(w * (double)g.scale);
+            s_ids(u)[lane] = (uint16_t)my_id[u];
+        }
+    }
+}
+
+template <int V, bool GROUPED>
+__global__ __launch_bounds__(kRouteThreads) void k_route_groups(const float *__restrict__ logits,
+                                                               RouteGroups g, int lanes,
+                                                               int *__restrict__ ids,
+                                                               float *__restrict__ weights,
+                                                               int *__restrict__ offsets,
+                                                               int *__restrict__ order,
+                                                               int *__restrict__ counts, int T,
+                                                               int E, int top_k, int chunk, int bits)
+{
+    constexpr int U = V <= 4 ? 2 : 1;   // two tokens' keys and scores of 16 experts a lane do not fit the registers
+    __shared__ RouteLds<GROUPED ? 64 * V : 1> l;
+    __shared__ uint16_t s_ids[kOneChunk * kMaxTopK];
+    const Experts<V> x = load_experts<V, GROUPED>(g, E, lanes);
+    double *vals = l.vals[GROUPED ? threadIdx.x >> 6 : 0];
+    const auto tokens = [&](const int (&tok)[2], int n, auto to) __attribute__((always_inline)) {
+        if constexpr (U == 2) {
+            choose_tokens<V, 2, GROUPED>(logits, g, x, vals, lanes, E, top_k, ids, weights, tok, n, to);
+        } else {
+            for (int u = 0; u < n; ++u)
+                choose_tokens<V, 1, GROUPED>(logits, g, x, vals, lanes, E, top_k, ids, weights, tok + u, 1,
+                                             [&](int) __attribute__((always_inline)) { return to(u); });
+        }
+    };
+    route_workgroup(l, s_ids, tokens, offsets, order, counts, T, E, top_k, chunk, bits);
+}
+
 // Chunk c's slots to their places: thread (p, e) sums expert e's counts over
 // the chunks c' = p mod parts, all of them and those before c.
 __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__restrict__ ids,
@@ -247,7 +486,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
                                                               int top_k, int chunk, int chunks,
                                                               int bits)
 {
-    __shared__ RouteLds l;
+    __shared__ RouteLds<> l;
     __shared__ int sums[2][kRouteThreads];
     const int tid = threadIdx.x, c = blockIdx.x;
     const int width = 1 << bits, parts = kRouteThreads / width;   // E <= width <= 1024
@@ -282,23 +521,60 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
     place(l, [&](int i) { return ids[s0 + i]; }, s0, n, E, bits, first + before, order);
 }
 
+static int expert_bits(int E)
+{
+    int bits = 0;
+    while ((1 << bits) < E)
+        ++bits;
+    return bits;
+}
+
+// The second launch, where there is more than one chunk.
+static hipError_t launch_place(const int *ids, const int *counts, int *offsets, int *order, int T, int E,
+                               int top_k, hipStream_t st)
+{
+    const int chunk = route_chunk(T), chunks = route_chunks(T);
+    return launch_kernel(k_route_place, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, ids, counts,
+                         offsets, order, T, E, top_k, chunk, chunks, expert_bits(E));
+}
+
 hipError_t launch_route(const float *logits, int *ids, float *weights, int *offsets, int *order,
                         void *workspace, int T, int E, int top_k, bool renorm, hipStream_t st)
 {
     const int chunk = route_chunk(T), chunks = route_chunks(T);
     int *counts = chunks > 1 ? static_cast<int *>(workspace) : nullptr;
-    int bits = 0;
-    while ((1 << bits) < E)
-        ++bits;
     auto kernel = E <= 64 ? k_route<1> : E <= 128 ? k_route<2> : E <= 256 ? k_route<4> : k_route<16>;
     hipError_t e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, logits,
                                  ids, weights, offsets, order, counts, T, E, top_k, renorm ? 1 : 0,
-                                 chunk, bits);
+                                 chunk, expert_bits(E));
     if (e != hipSuccess || !counts)
         return e;
-    return launch_kernel(k_route_place, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st,
-                         (const int *)ids, (const int *)counts, offsets, order, T, E, top_k, chunk,
-                         chunks, bits);
+    return launch_place(ids, counts, offsets, order, T, E, top_k, st);
+}
+
+template <bool GROUPED>
+static auto groups_kernel(int E)
+{
+    return E <= 64 ? k_route_groups<1, GROUPED> : E <= 128 ? k_route_groups<2, GROUPED>
+         : E <= 256 ? k_route_groups<4, GROUPED> : k_route_groups<16, GROUPED>;
+}
+
+hipError_t launch_route_groups(const float *logits, const RouteGroups &g, int *ids, float *weights,
+                               int *offsets, int *order, void *workspace, int T, int E, int top_k,
+                               hipStream_t st)
+{
+    const int chunk = route_chunk(T), chunks = route_chunks(T);
+    int *counts = chunks > 1 ? static_cast<int *>(workspace) : nullptr;
+    int lanes = 6;
+    while (g.n_groups << lanes > 64)
+        --lanes;
+    auto kernel = g.top_groups < g.n_groups ? groups_kernel<true>(E) : groups_kernel<false>(E);
+    hipError_t e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, logits, g,
+                                 lanes, ids, weights, offsets, order, counts, T, E, top_k, chunk,
+                                 expert_bits(E));
+    if (e != hipSuccess || !counts)
+        return e;
+    return launch_place(ids, counts, offsets, order, T, E, top_k, st);
 }
 
 }  // namespace q4k

@@ -378,7 +378,18 @@ size_t route_workspace_bytes(int T, int E, int top_k)
     return route_chunks(T) > 1 ? (size_t)route_chunks(T) * (size_t)E * 4 : 0;
 }
 
-int check_route(const void *logits, int T, int E, int top_k, const void *ids, const void *weights,
+int check_route_groups(int E, int top_k, int score, int n_groups, int top_groups, int group_best,
+                       float scale)
+{
+    if ((score != Q4_SCORE_SOFTMAX && score != Q4_SCORE_SIGMOID) || n_groups < 1 ||
+        n_groups > Q4_ROUTE_MAX_GROUPS || E < 1 || E % n_groups != 0 || top_groups < 1 ||
+        top_groups > n_groups || group_best < 1 || group_best > 2 || group_best > E / n_groups ||
+        top_k > (long long)top_groups * (E / n_groups) || !(scale - scale == 0.0f))
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+int check_route(const void *logits, const void *bias, int T, int E, int top_k, const void *ids, const void *weights,
                 const void *offsets, const void *order, const void *ws, size_t ws_bytes, size_t need,
                 bool *empty)
 {
@@ -393,13 +404,13 @@ int check_route(const void *logits, int T, int E, int top_k, const void *ids, co
     if (!logits || !ids || !weights || !offsets || !order)
         return Q4_ERR_NULL;
     const size_t slots = (size_t)T * (size_t)top_k * 4;
-    const Span spans[6] = {{ids, slots}, {weights, slots}, {order, slots}, {offsets, (size_t)(E + 1) * 4},
-                           {logits, (size_t)T * (size_t)E * 4}, {ws, need}};
-    for (int i = 0; i < 5; ++i)
+    const Span spans[7] = {{ids, slots}, {weights, slots}, {order, slots}, {offsets, (size_t)(E + 1) * 4},
+                           {logits, (size_t)T * (size_t)E * 4}, {bias, bias ? (size_t)E * 4 : 0}, {ws, need}};
+    for (int i = 0; i < 6; ++i)
         if (!aligned16(spans[i].p))
             return Q4_ERR_ALIGN;
     for (int i = 0; i < 4; ++i)
-        for (int j = i + 1; j < 5; ++j)
+        for (int j = i + 1; j < 6; ++j)
             if (overlaps(spans[i], spans[j]))
                 return Q4_ERR_ALIAS;
     if (need == 0)
@@ -410,9 +421,92 @@ int check_route(const void *logits, int T, int E, int top_k, const void *ids, co
         return Q4_ERR_NULL;
     if (!aligned16(ws))
         return Q4_ERR_ALIGN;
-    for (int i = 0; i < 5; ++i)
-        if (overlaps(spans[i], spans[5]))
+    for (int i = 0; i < 6; ++i)
+        if (overlaps(spans[i], spans[6]))
             return Q4_ERR_ALIAS;
+    return Q4_OK;
+}
+
+// Sizes of the written rows: bytes of y, elements of s. Q4_ERR_SIZE where the
+// caller's counts say otherwise.
+static int rows_out_size(const RowsOut &o, int M, int K, size_t *y_bytes)
+{
+    const size_t n = (size_t)M * (size_t)K;   // both below 2^31
+    *y_bytes = o.y_elem ? n * o.y_elem : o.f8 ? n : n / 32 * 34;
+    if (!o.y_elem && o.bytes != *y_bytes)
+        return Q4_ERR_SIZE;
+    if (o.f8 && (o.s_elems != (size_t)M * f8_blocks(K) || o.s_elems >= ((size_t)1 << 31)))
+        return Q4_ERR_SIZE;
+    return Q4_OK;
+}
+
+int check_norm(const NormCheck &c, bool *empty)
+{
+    *empty = false;
+    if (c.M < 0 || c.K < 32 || c.K % 32 != 0 || c.K > Q4_NORM_MAX_K || c.share < 1 ||
+        c.share > Q4_MAX_TOP_K || (long long)c.M * c.share > Q4_MAX_SLOTS || !(c.eps >= 0.0f) ||
+        !(c.eps - c.eps == 0.0f))
+        return Q4_ERR_SHAPE;
+    size_t y_bytes = 0;
+    const int st = rows_out_size(c.out, c.M, c.K, &y_bytes);
+    if (st != Q4_OK)
+        return st;
+    if (c.M == 0) {
+        *empty = true;
+        return Q4_OK;
+    }
+    if (!c.x || !c.gamma || !c.out.y || (c.out.f8 && !c.out.s))
+        return Q4_ERR_NULL;
+    // Inputs, then outputs; an absent array is empty.
+    const size_t rows = (size_t)c.M * (size_t)c.K * c.elem;
+    const Span in[4] = {{c.x, rows * (size_t)c.share}, {c.gamma, (size_t)c.K * 4},
+                        {c.weights, c.weights ? (size_t)c.M * (size_t)c.share * 4 : 0},
+                        {c.residual, c.residual ? rows : 0}};
+    const Span out[4] = {{c.out.y, y_bytes}, {c.out.s, c.out.f8 ? c.out.s_elems * 4 : 0},
+                         {c.dense, c.dense ? rows : 0}, {c.sum, c.sum ? rows : 0}};
+    for (int i = 0; i < 4; ++i)
+        if (!aligned16(in[i].p) || !aligned16(out[i].p))
+            return Q4_ERR_ALIGN;
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlaps(out[i], in[j]) && !(i == 3 && j == 3 && c.sum == c.residual))
+                return Q4_ERR_ALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlaps(out[i], out[j]))
+                return Q4_ERR_ALIAS;
+    }
+    return Q4_OK;
+}
+
+int check_act(const ActCheck &c, bool *empty)
+{
+    *empty = false;
+    const int unit = 16 / (int)c.elem;
+    if (c.M < 0 || c.K < 32 || c.K % 32 != 0 || c.K > (1 << 22) || c.ld < c.K || c.ld % unit != 0 ||
+        (c.act != Q4_ACT_SILU && c.act != Q4_ACT_GELU))
+        return Q4_ERR_SHAPE;
+    size_t y_bytes = 0;
+    const int st = rows_out_size(c.out, c.M, c.K, &y_bytes);
+    if (st != Q4_OK)
+        return st;
+    if (c.M == 0) {
+        *empty = true;
+        return Q4_OK;
+    }
+    const size_t span = ((size_t)(c.M - 1) * (size_t)c.ld + (size_t)c.K) * c.elem;   // below 2^64
+    if (!c.gate || !c.out.y || (c.out.f8 && !c.out.s))
+        return Q4_ERR_NULL;
+    const Span in[2] = {{c.gate, span}, {c.up, c.up ? span : 0}};
+    const Span out[2] = {{c.out.y, y_bytes}, {c.out.s, c.out.f8 ? c.out.s_elems * 4 : 0}};
+    for (int i = 0; i < 2; ++i)
+        if (!aligned16(in[i].p) || !aligned16(out[i].p))
+            return Q4_ERR_ALIGN;
+    if (overlaps(out[0], out[1]))
+        return Q4_ERR_ALIAS;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (overlaps(out[i], in[j]))
+                return Q4_ERR_ALIAS;
     return Q4_OK;
 }
 

@@ -267,10 +267,13 @@ int check_grouped(const GroupedArgs &g);
 // The workspace against every span of g.
 int check_grouped_workspace(const GroupedArgs &g, size_t need, const void *ws, size_t ws_bytes);
 
-// q4_route.
-int check_route(const void *logits, int T, int E, int top_k, const void *ids, const void *weights,
+// q4_route, and q4_route_groups with its bias (may be NULL).
+int check_route(const void *logits, const void *bias, int T, int E, int top_k, const void *ids, const void *weights,
                 const void *offsets, const void *order, const void *ws, size_t ws_bytes, size_t need,
                 bool *empty);
+// q4_route_groups: its own arguments; check_route checks the others.
+int check_route_groups(int E, int top_k, int score, int n_groups, int top_groups, int group_best,
+                       float scale);
 // Tokens of a workgroup's chunk: up to kRouteOneChunk tokens one workgroup
 // does all; otherwise at least two for each of its 16 wavefronts, and at most
 // 256 chunks, over which every workgroup of the second launch adds.
@@ -284,6 +287,38 @@ inline int route_chunk(int T)
 }
 inline int route_chunks(int T) { return (T + route_chunk(T) - 1) / route_chunk(T); }
 size_t route_workspace_bytes(int T, int E, int top_k);
+
+// The form that the norm and the activation write: y_elem bytes a value (4 or 2),
+// or 0 for Q8_0 blocks (bytes: their size) or E4M3 codes (bytes, and s_elems
+// scales).
+struct RowsOut {
+    const void *y;
+    size_t y_elem;
+    bool f8;
+    size_t bytes;
+    const void *s;
+    size_t s_elems;
+};
+// The norms: elem bytes of x, residual, sum and dense.
+struct NormCheck {
+    const void *x, *weights;
+    int share;
+    const void *residual, *sum, *gamma;
+    float eps;
+    const void *dense;
+    RowsOut out;
+    int M, K;
+    size_t elem;
+};
+int check_norm(const NormCheck &c, bool *empty);
+struct ActCheck {
+    const void *gate, *up;
+    int ld, act;
+    RowsOut out;
+    int M, K;
+    size_t elem;
+};
+int check_act(const ActCheck &c, bool *empty);
 
 bool aligned16(const void *p);
 bool overlaps(Span a, Span b);

@@ -106,6 +106,31 @@ int f8_gemm_grouped(const uint8_t *a, const float *a_s, const uint8_t *w, size_t
                     const float *w_s, const int32_t *offsets, const int32_t *order, int share,
                     uint16_t *y, int G, int M, int N, int K, void *stream);
 
+/*
+ * f8_norm, f8_norm_bf16 — q4.h's q4_norm (q4_norm_bf16) with y as E4M3 codes and a
+ * scale for each 128 columns: what f8_quantize with block_rows 1 makes of its f32
+ * y, bit for bit.
+ *   q, q_bytes, s, s_elems  as f8_quantize (block_rows 1).
+ *   y         [M, K] f32 (f8_norm_bf16: bfloat16) as well, or NULL (for a router,
+ *             say).
+ */
+int f8_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+            const float *gamma, float eps, float *y, void *q, size_t q_bytes, float *s,
+            size_t s_elems, int M, int K, void *stream);
+int f8_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                 uint16_t *sum, const float *gamma, float eps, uint16_t *y, void *q, size_t q_bytes,
+                 float *s, size_t s_elems, int M, int K, void *stream);
+
+/*
+ * f8_act, f8_act_bf16 — q4.h's q4_act (q4_act_bf16) with y as E4M3 codes and a
+ * scale for each 128 columns: what f8_quantize with block_rows 1 makes of its f32
+ * y, bit for bit. q, q_bytes, s, s_elems as there.
+ */
+int f8_act(const float *gate, const float *up, int ld, int act, void *q, size_t q_bytes, float *s,
+           size_t s_elems, int M, int K, void *stream);
+int f8_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *q, size_t q_bytes,
+                float *s, size_t s_elems, int M, int K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,7 @@
 extern "C" {
 #endif
 
-#define Q4_ABI_VERSION 11
+#define Q4_ABI_VERSION 12
 
 #define Q4_OK 0
 #define Q4_ERR_NULL 1   /* a required pointer is NULL */
@@ -66,6 +66,18 @@ extern "C" {
 #define Q4_MAX_EXPERTS 1024
 #define Q4_MAX_TOP_K 32
 #define Q4_MAX_SLOTS 1073741824
+
+/* Widest row of the norms, and most groups of experts of q4_route_groups. */
+#define Q4_NORM_MAX_K 32768
+#define Q4_ROUTE_MAX_GROUPS 64
+
+/* Activations of q4_act and its kin: SiLU, and GELU in its tanh form. */
+#define Q4_ACT_SILU 0
+#define Q4_ACT_GELU 1
+
+/* Scores of q4_route_groups. */
+#define Q4_SCORE_SOFTMAX 0
+#define Q4_SCORE_SIGMOID 1
 
 /* Bytes of device memory each GPU holds for q4_gemm and q8_gemm (64 MiB). */
 #define Q4_GEMM_SCRATCH_BYTES 67108864u
@@ -460,6 +472,43 @@ int q4_route(const float *logits, int T, int E, int top_k, int renorm, int32_t *
 size_t q4_route_workspace_bytes(int T, int E, int top_k);
 
 /*
+ * q4_route_groups — q4_route with scores, a bias and groups of experts.
+ *   logits    [T, E] f32, as q4_route's.
+ *   score     Q4_SCORE_SIGMOID: s = 1 / (1 + exp(-logit)); Q4_SCORE_SOFTMAX: s =
+ *             the softmax over all E. A masked expert (-inf) has s = 0.
+ *   bias      [E] f32, or NULL for none. The experts are chosen by s + bias; the
+ *             weights come from s alone. -inf masks an expert for every token.
+ *   n_groups, top_groups, group_best  the experts form n_groups groups of
+ *             E / n_groups neighbours, and only those of the top_groups best
+ *             groups can be chosen: the ones with the largest sum of their
+ *             group_best (1 or 2) largest s + bias, the lowest group first among
+ *             equal sums. A group with fewer unmasked experts than group_best
+ *             ranks behind all others. top_groups == n_groups: no choice of groups.
+ *             1 <= top_groups <= n_groups <= Q4_ROUTE_MAX_GROUPS, E % n_groups == 0,
+ *             group_best <= E / n_groups, top_k <= top_groups * (E / n_groups).
+ *   renorm    non-zero: weights = scale * s / (the sum of s over the chosen
+ *             experts), 0 where that sum is 0; zero: weights = scale * s.
+ *   scale     a finite f32 (else Q4_ERR_SHAPE).
+ *   ids       [T, top_k] int32: the experts of the largest s + bias, in falling
+ *             order, the lowest expert first among equal ones. Masked experts
+ *             come last, in rising order, with weight 0.
+ *   T, E, top_k, weights, offsets, order, workspace: as q4_route, with
+ *             q4_route_workspace_bytes(T, E, top_k) bytes. Errors and their
+ *             order as q4_route.
+ * Scores, s + bias and the groups' sums are formed in f64 (each within 2^-49 of
+ * its largest term), so experts change places only where their s + bias agree to
+ * that; equal logits with equal biases give equal values. Logits more than 700
+ * below zero (softmax: below the largest) count as 700 below. Weights are
+ * rounded to f32 once. Deterministic. T == 0 is an empty problem. NaN logits and
+ * biases mask; logits of +inf give unspecified choices; ids, offsets and order
+ * stay a valid grouping.
+ */
+int q4_route_groups(const float *logits, const float *bias, int T, int E, int top_k, int score,
+                    int n_groups, int top_groups, int group_best, int renorm, float scale,
+                    int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * q4_gemm_grouped — products grouped by expert with ragged sizes: for every
  * group e and every row r that the list names for it,
  *   y[r, n] = sum_k a[r / share, k] dequant(W[e])[n, k].
@@ -544,6 +593,88 @@ int q8_quantize(const float *x, size_t n_elems, void *out_q, size_t out_bytes, v
  * Bit-exact and deterministic.
  */
 int q4_quantize(const float *x, size_t n_elems, void *out_q, size_t out_bytes, void *stream);
+
+/*
+ * q4_norm — the residual's addition and the root-mean-square norm before a
+ * product, for each of M rows:
+ *   h = residual + sum_{j < share} weights[m, j] x[m share + j],
+ *   y = h rstd gamma, rstd = 1 / sqrt(mean of h^2 + eps).
+ *   x         [M share, K] f32: the rows added to the residual. share in [1,
+ *             Q4_MAX_TOP_K] (else Q4_ERR_SHAPE): a token's slots are consecutive,
+ *             as the grouped products write them.
+ *   weights   [M, share] f32, as q4_route writes them, or NULL: all 1. A row whose
+ *             weight is 0 adds nothing, whatever it holds (its slot may be in no
+ *             group).
+ *   residual  [M, K] f32, or NULL: none.
+ *   sum       [M, K] f32: h, the next residual; or NULL. May be `residual` itself
+ *             (the only array that may be an input and an output).
+ *   gamma     [K] f32.
+ *   eps       finite, >= 0 (else Q4_ERR_SHAPE). A row of zeros with eps 0 gives 0.
+ *   y         [M, K]: f32 (y_bf16 zero) or bfloat16 patterns (non-zero).
+ *   M >= 0, M share <= Q4_MAX_SLOTS, K a positive multiple of 32, K <=
+ *   Q4_NORM_MAX_K (else Q4_ERR_SHAPE).
+ * Numerics: h is summed in f64 (share 1 without weights: one f32 addition) and
+ * rounded to f32 once; the mean of its squares and rstd are f64, rstd rounded to
+ * f32 once; y = (h rstd) gamma is two f32 products, then rounded to bfloat16 if
+ * asked. So |y - exact| <= 2^-21.6 |exact| (and 2^-8 |y| more in bfloat16) + 2^-126
+ * where h does not cancel (h itself is within half a step). Deterministic.
+ * Errors in the order shape, size, empty (M == 0), NULL, alignment, overlap.
+ */
+int q4_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+            const float *gamma, float eps, void *y, int y_bf16, int M, int K, void *stream);
+
+/* q4_norm_bf16 — q4_norm with x, residual and sum in bfloat16 (raw patterns). h
+ * is normed as summed; sum gets it rounded to bfloat16. */
+int q4_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                 uint16_t *sum, const float *gamma, float eps, void *y, int y_bf16, int M, int K,
+                 void *stream);
+
+/*
+ * q8_norm — q4_norm with y as Q8_0 blocks, for the products over Q8_0
+ * activations: what q8_quantize makes of q4_norm's f32 y, bit for bit.
+ *   out_q, out_bytes  the [M, K/32] blocks, out_bytes == M * (K/32) * 34 (else
+ *             Q4_ERR_SIZE).
+ *   y         [M, K] f32 as well, or NULL (for a router, say).
+ */
+int q8_norm(const float *x, const float *weights, int share, const float *residual, float *sum,
+            const float *gamma, float eps, float *y, void *out_q, size_t out_bytes, int M, int K,
+            void *stream);
+
+/* q8_norm_bf16 — q8_norm with x, residual, sum and y in bfloat16; the blocks are
+ * made from y before it is rounded to bfloat16. */
+int q8_norm_bf16(const uint16_t *x, const float *weights, int share, const uint16_t *residual,
+                 uint16_t *sum, const float *gamma, float eps, uint16_t *y, void *out_q,
+                 size_t out_bytes, int M, int K, void *stream);
+
+/*
+ * q4_act — the gated activation between two products: y = f(gate) up.
+ *   gate, up  [M, K] f32, rows ld elements apart: the halves of one product's
+ *             [M, 2 K] rows (ld = 2 K, up = gate + K), or two products' (ld = K).
+ *             up may be NULL: y = f(gate).
+ *   ld        >= K, a multiple of 4 (bfloat16: 8), so that every row is 16-byte
+ *             aligned (else Q4_ERR_SHAPE).
+ *   act       Q4_ACT_SILU: f(g) = g / (1 + exp(-g)); Q4_ACT_GELU: f(g) = g / (1 +
+ *             exp(-2 u)) = g (1 + tanh u) / 2, u = sqrt(2 / pi) (g + 0.044715 g^3).
+ *             Else Q4_ERR_SHAPE.
+ *   y         [M, K]: f32 (y_bf16 zero) or bfloat16 patterns (non-zero); overlaps
+ *             nothing between the first and the last element of gate or of up.
+ *   M >= 0, K a positive multiple of 32, K <= 2^22 (else Q4_ERR_SHAPE).
+ * Numerics, in f32: |y - exact| <= 2^-20 |exact| (GELU: (2^-20 + |u| 2^-21) |exact|)
+ * + |up| 2^-119 + 2^-149, and 2^-8 |y| more in bfloat16. Deterministic.
+ */
+int q4_act(const float *gate, const float *up, int ld, int act, void *y, int y_bf16, int M, int K,
+           void *stream);
+
+/* q4_act_bf16 — q4_act with gate and up in bfloat16 (raw patterns). */
+int q4_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *y, int y_bf16,
+                int M, int K, void *stream);
+
+/* q8_act, q8_act_bf16 — the same with y as Q8_0 blocks: what q8_quantize makes of
+ * q4_act's (q4_act_bf16's) f32 y, bit for bit. out_bytes == M * (K/32) * 34. */
+int q8_act(const float *gate, const float *up, int ld, int act, void *out_q, size_t out_bytes,
+           int M, int K, void *stream);
+int q8_act_bf16(const uint16_t *gate, const uint16_t *up, int ld, int act, void *out_q,
+                size_t out_bytes, int M, int K, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,154 @@
+"""GPU tests of the gated activations (q4_act, q8_act, f8_act and their bfloat16
+forms) against plain_rows.py in 64 bits, within include/q4.h's bound; the 8-bit
+forms: the bytes that the quantizers make of the f32 result."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import plain_rows as plain  # noqa: E402
+from block_quantized_weight_dequant_amd import binding as q4  # noqa: E402
+from gpu_helpers import DEV, Guarded, to_dev  # noqa: E402
+from plain_experts import bf16_bits  # noqa: E402
+
+
+def dev_of(a):
+    if a is None:
+        return None
+    return to_dev(a.view(np.int16)).view(torch.bfloat16) if a.dtype == np.uint16 else to_dev(a)
+
+
+def check_act(gate, up, gelu, layout="halves"):
+    """gate, up [M, K] numpy, f32 or bfloat16 patterns; layout of the calls."""
+    bf16 = gate.dtype == np.uint16
+    M, K = gate.shape
+    tail, fn = "_bf16" if bf16 else "", q4.Q4_ACT_GELU if gelu else q4.Q4_ACT_SILU
+    what = "M %d K %d %s gelu %s %s" % (M, K, tail, gelu, layout)
+    if layout == "halves":
+        both = dev_of(np.concatenate([gate, gate if up is None else up], 1))
+        g, u = both[:, :K], None if up is None else both[:, K:]
+    elif layout == "wide":          # rows with more behind them
+        both = dev_of(np.concatenate([gate, gate if up is None else up, gate[:, :8]], 1))
+        g, u = both[:, :K], None if up is None else both[:, K:2 * K]
+    else:
+        g, u = dev_of(gate), dev_of(up)
+    nb, ns = M * (K // 32) * 34, M * -(-K // 128)
+    y32, y16, q8 = Guarded(M * K, torch.float32), Guarded(M * K, torch.bfloat16), Guarded(nb, torch.uint8)
+    f8, fs = Guarded(M * K, torch.uint8), Guarded(ns, torch.float32)
+    getattr(q4, "q4_act" + tail)(g, u, y32.view, M, K, fn)
+    getattr(q4, "q4_act" + tail)(g, u, y16.view, M, K, fn)
+    getattr(q4, "q8_act" + tail)(g, u, q8.view, M, K, fn)
+    getattr(q4, "f8_act" + tail)(g, u, f8.view, fs.view, M, K, fn)
+    torch.cuda.synchronize()
+    for b in (y32, y16, q8, f8, fs):
+        assert b.guards_intact(), what
+    ref = plain.act(gate, up, gelu)
+    fine = np.abs(ref) < 3e38
+    for b, half in ((y32, False), (y16, True)):
+        got = b.view.float().cpu().numpy().astype(np.float64).reshape(M, K)
+        tol = plain.act_tolerance(gate, up, gelu, half)
+        with np.errstate(invalid="ignore"):
+            bad = np.argwhere((np.abs(got - ref) > tol) & fine | np.isnan(got))
+        assert bad.size == 0, "%s: %d off, first %s: %r for gate %r up %r, exact %r" % (
+            what, len(bad), bad[0], got[tuple(bad[0])], plain.widen(gate)[tuple(bad[0])],
+            None if up is None else plain.widen(up)[tuple(bad[0])], ref[tuple(bad[0])])
+    assert torch.equal(y16.view, y32.view.to(torch.bfloat16)), what
+    if not fine.all():
+        return
+    want, ws = torch.empty(nb, dtype=torch.uint8, device=DEV), torch.empty(ns, device=DEV)
+    q4.q8_quantize(y32.view.contiguous(), want)
+    assert torch.equal(q8.view, want), what
+    want = torch.empty(M * K, dtype=torch.uint8, device=DEV)
+    q4.f8_quantize(y32.view.contiguous(), want, ws, M, K, 1)
+    assert torch.equal(f8.view, want) and torch.equal(fs.view, ws), what
+
+
+def make(M, K, bf16, seed):
+    g = np.random.default_rng(seed)
+    gate = (3 * g.normal(0, 1, (M, K))).astype(np.float32)
+    up = (g.normal(0, 1, (M, K)) * np.exp(g.normal(0, 1, (M, 1)))).astype(np.float32)
+    return (bf16_bits(gate), bf16_bits(up)) if bf16 else (gate, up)
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (5, 160), (1, 256), (7, 288), (2, 512), (9, 544), (4, 1024), (37, 1056),
+                                 (1, 2048), (130, 2080), (6, 4096), (2, 14336), (1, 14368), (1001, 416)])
+def test_shapes(M, K, bf16, gelu):
+    gate, up = make(M, K, bf16, 7 * M + K)
+    check_act(gate, up, gelu)
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("layout", ["halves", "wide", "apart"])
+def test_layouts_and_no_up(layout, bf16, gelu):
+    gate, up = make(19, 672, bf16, 5)
+    check_act(gate, up, gelu, layout)
+    check_act(gate, None, gelu, layout)
+    check_act(gate[:1], up[:1], gelu, layout)
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_every_size_of_gate(bf16, gelu):
+    # Both signs, from the smallest to the largest values, and +-0.
+    g = np.random.default_rng(9)
+    mag = np.exp2(g.uniform(-140, 127, 4096)).astype(np.float32)
+    near = g.uniform(80, 140, 2048).astype(np.float32)     # where exp leaves f32
+    gate = np.concatenate([mag, -mag, near, -near, g.uniform(-12, 12, 4096).astype(np.float32), np.zeros(32, np.float32),
+                           -np.zeros(32, np.float32), np.full(32, 3.3e38, np.float32), np.full(32, -3.3e38, np.float32)])
+    gate = gate.reshape(-1, 32)
+    up = g.normal(0, 1, gate.shape).astype(np.float32)
+    up[:, ::5] *= np.float32(2.0 ** 100)
+    up[:, ::7] *= np.float32(2.0 ** -120)
+    check_act(bf16_bits(gate) if bf16 else gate, bf16_bits(up) if bf16 else up, gelu)
+    check_act(bf16_bits(gate) if bf16 else gate, None, gelu)
+
+
+def test_offsets_past_32_bits():
+    K, ld = 4096, 2 ** 20
+    M = 2 ** 32 // ld + 2
+    both = torch.empty(M, ld, dtype=torch.bfloat16, device=DEV)
+    both[:, :2 * K] = 1.0
+    g = torch.Generator(device=DEV).manual_seed(8)
+    both[-1, :2 * K] = torch.randn(2 * K, generator=g, device=DEV).to(torch.bfloat16)
+    y = torch.empty(M, K, device=DEV)
+    q4.q4_act_bf16(both[:, :K], both[:, K:2 * K], y, M, K)
+    torch.cuda.synchronize()
+    bits = both[-1:, :2 * K].contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+    ref = plain.act(bits[:, :K], bits[:, K:], False)
+    assert (np.abs(y[-1:].cpu().numpy() - ref) <= plain.act_tolerance(bits[:, :K], bits[:, K:], False, False)).all()
+    assert bool((y[:-1] == y[0, 0]).all())
+
+
+def test_rows_past_a_grid_dimension():
+    # More rows than a grid's second dimension holds, of the narrowest width.
+    M, K = 70001, 32
+    gate, up = make(M, K, True, 3)
+    check_act(gate, up, False)
+
+
+def test_binding_refuses():
+    M, K = 4, 64
+    x, y = torch.zeros(M, 2 * K, device=DEV), torch.zeros(M, K, device=DEV)
+    g, u = x[:, :K], x[:, K:]
+    for a, b, c in [(g.cpu(), u, y), (g, u.contiguous(), y), (g[:2], u, y), (g, x, y), (g.double(), u, y), (g, u, y.half()),
+                    (g, u, y[:3]), (x.t()[:K], u, y), (x[:, ::2], x[:, 1::2], y)]:
+        with pytest.raises(ValueError):
+            q4.q4_act(a, b, c, M, K)
+    with pytest.raises(q4.Q4Error) as e:
+        q4.q4_act(g, u, y, M, K, 2)
+    assert e.value.status == q4.Q4_ERR_SHAPE
+    with pytest.raises(q4.Q4Error) as e:
+        q4.q4_act(x[:, 1:K + 1], u, y, M, K)
+    assert e.value.status == q4.Q4_ERR_ALIGN
+    with pytest.raises(ValueError):
+        q4.q8_act(g, u, torch.zeros(M * 2 * 34 + 1, dtype=torch.uint8, device=DEV), M, K)
+    q4.q4_act(x[:0, :K], x[:0, K:], y[:0], 0, K)     # empty
+    torch.cuda.synchronize()
+    assert not y.any()

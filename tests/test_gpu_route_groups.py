@@ -1,0 +1,157 @@
+"""GPU tests of q4_route_groups against plain_rows.py in 64 bits: choices,
+offsets and order exact, weights within one rounding to f32 (2^-24) and 2^-45 for
+the f64 scores and their sum."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import plain_rows as plain  # noqa: E402
+from block_quantized_weight_dequant_amd import binding as q4  # noqa: E402
+from gpu_helpers import DEV, Guarded, to_dev  # noqa: E402
+
+
+def run(x, bias, k, sigmoid, G=1, top=1, best=1, renorm=True, scale=1.0, stream=None):
+    T, E = x.shape
+    out = [Guarded(T * k, torch.int32), Guarded(T * k, torch.float32), Guarded(E + 1, torch.int32), Guarded(T * k, torch.int32)]
+    q4.q4_route_groups(to_dev(x), None if bias is None else to_dev(bias), *(o.view for o in out), T, E, k,
+                       q4.Q4_SCORE_SIGMOID if sigmoid else q4.Q4_SCORE_SOFTMAX, G, top, best, renorm, scale, stream=stream)
+    torch.cuda.synchronize()
+    assert all(o.guards_intact() for o in out)
+    return [o.host() for o in out]
+
+
+def check(x, bias, k, sigmoid, G=1, top=1, best=1, renorm=True, scale=1.0):
+    T, E = x.shape
+    what = "T %d E %d k %d sigmoid %s groups %d %d %d renorm %s" % (T, E, k, sigmoid, G, top, best, renorm)
+    ids, w, off, order = run(x, bias, k, sigmoid, G, top, best, renorm, scale)
+    r_ids, r_w, r_off, r_order = plain.route(x, bias, k, sigmoid, G, top, best, renorm, scale)
+    bad = np.argwhere(ids.reshape(T, k) != r_ids)
+    assert bad.size == 0, "%s: %d choices differ, first at %s" % (what, len(bad), bad[0])
+    assert np.array_equal(off, r_off) and np.array_equal(order, r_order), what
+    r_w = r_w.reshape(-1)
+    assert (np.abs(w - r_w) <= (2.0 ** -24 + 2.0 ** -45) * np.abs(r_w) + 2.0 ** -149).all(), what
+
+
+def make(T, E, seed, biased=True):
+    g = np.random.default_rng(seed)
+    x = (g.normal(0, 1, (T, E)) + 0.5 * g.normal(0, 1, (1, E))).astype(np.float32)
+    return x, (0.1 * g.normal(0, 1, E)).astype(np.float32) if biased else None
+
+
+# One to sixteen experts a lane, group sizes that are and are not powers of two.
+SHAPES = [(1, 256, 8, 8, 4, 2), (2, 256, 8, 8, 4, 2), (33, 256, 8, 8, 4, 2), (64, 64, 6, 8, 3, 1), (65, 60, 4, 5, 2, 2),
+          (200, 128, 1, 4, 1, 2), (31, 160, 8, 8, 3, 1), (100, 640, 32, 64, 7, 2), (1, 1024, 16, 32, 5, 2), (40, 1000, 10, 10, 9, 2),
+          (300, 12, 3, 3, 2, 2), (17, 64, 8, 64, 8, 1), (5, 126, 9, 63, 60, 2), (90, 2, 1, 2, 1, 1), (2100, 256, 8, 8, 4, 2)]
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("T,E,k,G,top,best", SHAPES)
+def test_groups(T, E, k, G, top, best, sigmoid):
+    x, b = make(T, E, 3 * T + E)
+    check(x, b, k, sigmoid, G, top, best, True, 2.5)
+    check(x, None, k, sigmoid, G, top, best, False, 1.0)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (64, 8, 2), (77, 65, 7), (130, 256, 32), (9, 257, 8), (200, 1024, 32), (1000, 40, 6)])
+def test_no_groups(T, E, k, sigmoid):
+    x, b = make(T, E, T + E)
+    check(x, b, k, sigmoid, renorm=True, scale=0.5)
+    check(x, b, k, sigmoid, renorm=False)
+    if E % 2 == 0:
+        check(x, b, k, sigmoid, 2, 2, 1)          # all groups kept
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("E,G,top", [(64, 8, 3), (256, 8, 4), (1000, 10, 4)])
+def test_equal_keys(E, G, top, sigmoid):
+    # Few distinct logits and biases: the lowest group, then the lowest expert.
+    g = np.random.default_rng(E)
+    x = (g.integers(-2, 3, (70, E)) * 0.5).astype(np.float32)
+    b = (g.integers(0, 2, E) * 0.25).astype(np.float32)
+    check(x, b, 8, sigmoid, G, top, 2)
+    check(x, None, 8, sigmoid, G, top, 1)
+    check(np.zeros((66, E), dtype=np.float32), None, 8, sigmoid, G, top, 2)
+    z = np.zeros((3, E), dtype=np.float32)
+    z[:, ::3] = -0.0
+    check(z, np.where(np.arange(E) % 2, 0.0, -0.0).astype(np.float32), 8, sigmoid, G, top, 2)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_masks(sigmoid):
+    T, E, G = 67, 64, 8
+    x, b = make(T, E, 77)
+    g = np.random.default_rng(1)
+    x[g.random((T, E)) < 0.5] = -np.inf
+    x[3] = -np.inf                       # nothing left
+    x[4, 1:] = -np.inf                   # one expert
+    x[5, 8:] = -np.inf                   # one group
+    x[6, ::8] = np.nan
+    b[[9, 17, 63]] = -np.inf
+    for G, top, best in [(1, 1, 1), (8, 3, 2), (8, 3, 1), (8, 8, 1)]:
+        for renorm in (True, False):
+            check(x, b, 6, sigmoid, G, top, best, renorm)
+    ids, w, _, _ = run(x, b, 6, sigmoid)
+    assert (w.reshape(T, 6)[3] == 0).all() and ids.reshape(T, 6)[3].tolist() == [0, 1, 2, 3, 4, 5]
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_far_logits(sigmoid):
+    # Scores down to exp(-700) and saturated ones; beyond, they count as equal.
+    g = np.random.default_rng(2)
+    x = g.uniform(-690, 5, (130, 128)).astype(np.float32)
+    check(x, None, 8, sigmoid, 8, 4, 2)
+    x[::2] = g.uniform(-3e4, -1e3, (65, 128)).astype(np.float32)
+    check(x, None, 8, sigmoid, 8, 4, 2, renorm=False)
+    x = np.full((3, 64), 3.3e38, dtype=np.float32)
+    x[1] = -3.3e38
+    check(x, None, 4, sigmoid)
+
+
+def test_biases_decide():
+    # Large biases of both signs order the experts, the scores weigh them.
+    x, _ = make(90, 256, 4)
+    b = np.random.default_rng(5).normal(0, 50, 256).astype(np.float32)
+    for sigmoid in (True, False):
+        check(x, b, 8, sigmoid, 8, 4, 2, True, -1.5)
+        check(x, -np.abs(b), 8, sigmoid, 8, 4, 1, False, 0.0)
+
+
+def test_what_is_not_a_number_stays_a_grouping():
+    T, E, k = 100, 256, 8
+    x, b = make(T, E, 6)
+    x[::3, ::5] = np.nan
+    x[::4, 3] = np.inf
+    b[7], b[200] = np.nan, np.inf
+    ids, _, off, order = run(x, b, k, True, 8, 4, 2)
+    ids = ids.reshape(T, k)
+    assert ((ids >= 0) & (ids < E)).all() and all(len(set(r)) == k for r in ids.tolist())
+    flat = ids.reshape(-1)
+    assert np.array_equal(order, np.argsort(flat, kind="stable"))
+    assert np.array_equal(off, np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E))]))
+
+
+def test_streams_and_repeats():
+    x, b = make(3000, 256, 8)
+    first = run(x, b, 8, True, 8, 4, 2)
+    st = torch.cuda.Stream()
+    for s in (None, st, st):
+        assert all(np.array_equal(p, q) for p, q in zip(first, run(x, b, 8, True, 8, 4, 2, stream=s)))
+
+
+def test_binding_refuses():
+    T, E, k = 4, 16, 2
+    x, i = torch.zeros(T, E, device=DEV), lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
+    ok = [x, None, i(T * k), torch.zeros(T * k, device=DEV), i(E + 1), i(T * k)]
+    for at, bad in [(0, x.double()), (0, x[:2]), (0, x.t()), (0, x.cpu()), (1, torch.zeros(E + 1, device=DEV)), (2, i(T * k).long()),
+                    (3, i(T * k)), (4, i(E)), (5, i(3))]:
+        with pytest.raises(ValueError):
+            q4.q4_route_groups(*[bad if j == at else v for j, v in enumerate(ok)], T, E, k)
+    with pytest.raises(q4.Q4Error) as e:
+        q4.q4_route_groups(*ok, T, E, k, q4.Q4_SCORE_SIGMOID, 3, 1)
+    assert e.value.status == q4.Q4_ERR_SHAPE
