@@ -23,16 +23,17 @@ constexpr float kE4M3Max = 448.0f;
 template <class T>
 constexpr int kPiece = 16 / (int)sizeof(T);
 
+// Rows are read once: their loads are non-temporal.
 __device__ __forceinline__ void load_piece(const float *p, float (&v)[4])
 {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+    const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         v[i] = a[i];
 }
 __device__ __forceinline__ void load_piece(const uint16_t *p, float (&v)[8])
 {
-    const u32x4 a = *reinterpret_cast<const u32x4 *>(p);
+    const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(a[i] << 16);
@@ -42,12 +43,17 @@ __device__ __forceinline__ void load_piece(const uint16_t *p, float (&v)[8])
 
 // P values of f32, or rounded to bfloat16, at p (aligned to 16 bytes, to 8
 // for four bfloat16 values).
+template <class T>
+__device__ __forceinline__ void store(void *p, T v)
+{
+    __builtin_nontemporal_store(v, static_cast<T *>(p));
+}
 template <int P>
 __device__ __forceinline__ void store_piece(float *p, const float (&v)[P])
 {
 #pragma unroll
     for (int h = 0; h < P / 4; ++h)
-        reinterpret_cast<f32x4 *>(p)[h] = (f32x4){v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        store(p + 4 * h, (f32x4){v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
 }
 template <int P>
 __device__ __forceinline__ void store_piece(uint16_t *p, const float (&v)[P])
@@ -57,20 +63,24 @@ __device__ __forceinline__ void store_piece(uint16_t *p, const float (&v)[P])
     for (int h = 0; h < P / 2; ++h)
         w[h] = bitcast<uint32_t>((bf16x2){(__bf16)v[2 * h], (__bf16)v[2 * h + 1]});
     if constexpr (P == 8)
-        *reinterpret_cast<u32x4 *>(p) = (u32x4){w[0], w[1], w[2], w[3]};
+        store(p, (u32x4){w[0], w[1], w[2], w[3]});
     else
-        *reinterpret_cast<u32x2 *>(p) = (u32x2){w[0], w[1]};
+        store(p, (u32x2){w[0], w[1]});
 }
 
-// x / s, correctly rounded to f32, for a scale s >= 0 that no |x| exceeds `limit`
-// times by more than a rounding. s in [2^-90, 2^90]: from the correctly rounded
-// reciprocal; each step takes the exact remainder (an FMA), the first to within
-// a unit in the last place, the second to the nearest (Markstein's theorem). No
-// intermediate leaves the normal range here but where the quotient is far below
-// the smallest code. The remainder of -0 is +0, which would lose its sign: the
-// quotient takes x's. Six operations an element; a division takes about twice
-// that. Other scales divide; s == 0 gives 0. clamp: to +-limit there (in the range
-// above the quotient is at most a rounding past it, which the codes absorb).
+// x / s for a scale s >= 0 that no |x| exceeds `limit` times by more than a
+// rounding, to be rounded to a code. s in [2^-90, 2^90]: from the correctly
+// rounded reciprocal and one step with the exact remainder (an FMA), which leaves
+// the quotient on the side of every midpoint between two E4M3 values, and of
+// every k + 1/2 up to 128, on which the correctly rounded one is, or on it: checked
+// for all significands of s, all midpoints (5 and 8 bits) and the five x nearest
+// to each product, the only ones whose quotients come within 2 units in the last
+// place. No intermediate leaves the normal range here but where the quotient is
+// far below the smallest code. The remainder of -0 is +0, which would lose its
+// sign: the quotient takes x's. Four operations an element; a division takes
+// about twelve. Other scales divide; s == 0 gives 0. clamp: to +-limit there (in
+// the range above the quotient is at most a rounding past it, which the codes
+// absorb).
 template <int P>
 __device__ __forceinline__ void quotients(const float (&x)[P], float s, bool clamp, float limit, float (&q)[P])
 {
@@ -79,8 +89,7 @@ __device__ __forceinline__ void quotients(const float (&x)[P], float s, bool cla
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const float q0 = x[i] * r;
-            const float q1 = fmaf(fmaf(-q0, s, x[i]), r, q0);
-            q[i] = __builtin_copysignf(fmaf(fmaf(-q1, s, x[i]), r, q1), x[i]);
+            q[i] = __builtin_copysignf(fmaf(fmaf(-q0, s, x[i]), r, q0), x[i]);
         }
     } else {
 #pragma unroll
@@ -133,9 +142,19 @@ __device__ __forceinline__ float lanes_max(float v)
     return v;
 }
 
+// max / c, correctly rounded, for c = 448 or 127: the quotient by the reciprocal
+// and one step with the exact remainder, checked for every significand.
+__device__ __forceinline__ float scale_of(float max, float c)
+{
+    if (!(max >= 0x1p-90f && max <= 0x1p120f))
+        return max / c;
+    const float r = 1.0f / c, q = max * r;
+    return fmaf(fmaf(-q, c, max), r, q);
+}
+
 // One piece of row `row` at column col, in the form O. Every lane of the
-// wavefront calls it; lanes that are not `in` (past the row's end) hold zeros
-// and write nothing.
+// wavefront calls it; lanes that are not `in` (past the row's end) count for no
+// maximum and write nothing.
 template <RowForm O, int P>
 __device__ __forceinline__ void put_piece(const RowOut &o, int K, const float (&v)[P], bool in, size_t row, int col)
 {
@@ -147,21 +166,21 @@ __device__ __forceinline__ void put_piece(const RowOut &o, int K, const float (&
         if (in)
             store_piece(static_cast<uint16_t *>(o.y) + at, v);
     } else if constexpr (O == RowForm::kE4M3) {
-        const float s = lanes_max<128 / P>(abs_max(v)) / kE4M3Max;
+        const float s = scale_of(lanes_max<128 / P>(in ? abs_max(v) : 0.0f), kE4M3Max);
         uint32_t w[P / 4];
         e4m3_codes(v, s, w);
         if (in) {
             uint8_t *p = static_cast<uint8_t *>(o.y) + at;
             if constexpr (P == 8)
-                *reinterpret_cast<u32x2 *>(p) = (u32x2){w[0], w[1]};
+                store(p, (u32x2){w[0], w[1]});
             else
-                *reinterpret_cast<uint32_t *>(p) = w[0];
+                store(p, w[0]);
             if ((col & 127) == 0)
                 o.s[row * (size_t)(((unsigned)K + 127) / 128) + (size_t)((unsigned)col >> 7)] = s;
         }
     } else {
         // Q8_0: a block's 34 bytes are 2-byte aligned, and so are these stores.
-        const float d = lanes_max<32 / P>(abs_max(v)) / 127.0f;
+        const float d = scale_of(lanes_max<32 / P>(in ? abs_max(v) : 0.0f), 127.0f);
         float q[P];
         quotients(v, d, false, 0.0f, q);
         uint32_t w[P / 4];

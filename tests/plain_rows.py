@@ -58,10 +58,15 @@ def act(gate, up, gelu):
 
 
 def act_tolerance(gate, up, gelu, bf16):
-    """include/q4.h, q4_act."""
+    """include/q4.h, q4_act. By its operations, u = 2^-24 the half step of f32: the
+    exponent z log2 e is a product with a rounded constant, off by 1.25 u of itself
+    (the constant log2 e is off by 2^-26.2) for SiLU and by 4 u for GELU (g^2, the
+    constants, the sum, the product), so exp(-z) by |z| times that (z = g, or 2 u);
+    the exponential by 2 u, 1 + e by u, the quotient by u and a little, the product
+    with up by u. 2^-20 is 16 u, |g| 2^-23 twice and |u| 2^-20 twice the shares of z."""
     y = np.abs(act(gate, up, gelu))
     g = widen(gate)
-    rel = 2.0 ** -20 + (2.0 ** -21 * np.abs(gelu_u(g)) if gelu else 0.0)
+    rel = 2.0 ** -20 + (2.0 ** -20 * np.abs(gelu_u(g)) if gelu else 2.0 ** -23 * np.abs(g))
     u = 1.0 if up is None else np.abs(widen(up))
     # In bfloat16 the f32 result is rounded once more, by half a step at most.
     half = 2.0 ** -8 * (y * (1 + rel)) if bf16 else 0.0
