@@ -657,19 +657,21 @@ def q4_route_groups(logits, bias, ids, weights, offsets, order, T: int, E: int, 
 _F32, _I32 = (torch.float32,), (torch.int32,)
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _array(x, n: int, dtypes) -> int:
     """Address of a dense device tensor of n elements of one of ``dtypes`` (or of
-    None, or of a plain address): the kernels go by the sizes given beside it."""
+    None, or of a plain address): the kernels go by the sizes given beside it.
+    These checks cost 0.2 us a tensor."""
     if x is None:
         return 0
-    if isinstance(x, int):
+    if type(x) is int:
         return x
-    if not x.is_cuda or x.dtype not in dtypes or x.numel() != n or not x.is_contiguous():
-        raise ValueError("expected a dense device tensor of %d elements of %s, got %s" % (
-            n, " or ".join(map(str, dtypes)), _what(x)))
-    return x.data_ptr()
+    if x.is_cuda and x.dtype in dtypes and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError("expected a dense device tensor of %d elements of %s, got %s" % (
+        n, " or ".join(map(str, dtypes)), _what(x)))
 
 
 def _what(x) -> str:
@@ -679,63 +681,72 @@ def _what(x) -> str:
 def _stream_for(stream, x) -> int:
     """_stream, where the work is x's: without a ``stream`` its device has to be
     the current one, whose stream is taken."""
-    if stream is None and getattr(x, "is_cuda", False) and x.get_device() != torch._C._cuda_getDevice():
+    if stream is not None or type(x) is int:
+        return _stream(stream)
+    device = x.get_device()
+    if device != _current_device():
         raise ValueError("the tensors are on %s, which is not the current device: make it current, or "
                          "pass a stream" % x.device)
-    return _stream(stream)
+    return _current_stream(device)
 
 
-def _values(y, n: int):
-    """Address of f32 or bfloat16 values, and whether they are bfloat16."""
-    bf16 = not isinstance(y, int) and y is not None and y.dtype in _BF16
+def _norm(entry, dtypes, x, gamma, M, K, eps, residual, sum, weights, share, tail, stream) -> None:
+    n = M * K
+    _check(getattr(lib, entry)(
+        _array(x, n * share, dtypes), _array(weights, M * share, _F32), share,
+        _array(residual, n, dtypes), _array(sum, n, dtypes), _array(gamma, K, _F32), eps, *tail, M, K,
+        _stream_for(stream, x)), entry)
+
+
+def _values_out(y, n: int, y_bf16):
+    """Where f32 or bfloat16 values go, and which of the two: by y's type, or by
+    ``y_bf16`` where y is an address."""
+    bf16 = bool(y_bf16) if type(y) is int or y is None else y.dtype in _BF16
     return _array(y, n, _BF16 if bf16 else _F32), bf16
 
 
-def _norm_inputs(x, gamma, M, K, dtypes, residual, sum, weights, share, eps):
-    n = M * K
-    return (_array(x, n * share, dtypes), _array(weights, M * share, _F32), share,
-            _array(residual, n, dtypes), _array(sum, n, dtypes), _array(gamma, K, _F32), eps)
+def _q8_out(out_q, M, K):
+    n = M * (K // 32) * 34
+    return _array(out_q, n, _BYTES), n
+
+
+def _f8_out(q, s, M, K):
+    n, ns = M * K, M * -(-K // 128)
+    return _array(q, n, _BYTES), n, _array(s, ns, _F32), ns
 
 
 def q4_norm(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
-            share: int = 1, y_bf16=None, stream=None) -> None:
+            share: int = 1, y_bf16=False, stream=None) -> None:
     """The residual's addition and the root-mean-square norm: h = ``residual`` +
     sum_j weights[m, j] x[m share + j], written to ``sum`` (which may be
     ``residual``), and ``y`` = h / sqrt(mean(h^2) + eps) * gamma in f32 or
     bfloat16, by y's type (of an address: ``y_bf16``). ``x`` [M * share, K],
     ``residual`` and ``sum`` [M, K] f32; ``weights`` [M, share] as q4_route writes
     them, a weight of 0 leaving its row out; ``gamma`` [K] f32."""
-    at, bf16 = _values(y, M * K)
-    _check(lib.q4_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps), at,
-                       bf16 if y_bf16 is None else bool(y_bf16), M, K, _stream_for(stream, x)), "q4_norm")
+    _norm("q4_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
+          _values_out(y, M * K, y_bf16), stream)
 
 
 def q4_norm_bf16(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
-                 share: int = 1, y_bf16=None, stream=None) -> None:
+                 share: int = 1, y_bf16=False, stream=None) -> None:
     """As q4_norm with ``x``, ``residual`` and ``sum`` in bfloat16."""
-    at, bf16 = _values(y, M * K)
-    _check(lib.q4_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps), at,
-                            bf16 if y_bf16 is None else bool(y_bf16), M, K, _stream_for(stream, x)),
-           "q4_norm_bf16")
+    _norm("q4_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
+          _values_out(y, M * K, y_bf16), stream)
 
 
 def q8_norm(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
             share: int = 1, y=None, stream=None) -> None:
     """q4_norm with the result as Q8_0 blocks in the uint8 tensor ``out_q``, and in
     f32 in ``y`` as well where that is given."""
-    nb = M * (K // 32) * 34
-    _check(lib.q8_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps),
-                       _array(y, M * K, _F32), _array(out_q, nb, _BYTES), nb, M, K,
-                       _stream_for(stream, x)), "q8_norm")
+    _norm("q8_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _F32), *_q8_out(out_q, M, K)), stream)
 
 
 def q8_norm_bf16(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
                  share: int = 1, y=None, stream=None) -> None:
     """As q8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
-    nb = M * (K // 32) * 34
-    _check(lib.q8_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps),
-                            _array(y, M * K, _BF16), _array(out_q, nb, _BYTES), nb, M, K,
-                            _stream_for(stream, x)), "q8_norm_bf16")
+    _norm("q8_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _BF16), *_q8_out(out_q, M, K)), stream)
 
 
 def f8_norm(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
@@ -743,87 +754,70 @@ def f8_norm(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None,
     """q4_norm with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
     columns, ``s`` [M, ceil(K / 128)], and in f32 in ``y`` as well where that is
     given."""
-    ns = M * -(-K // 128)
-    _check(lib.f8_norm(*_norm_inputs(x, gamma, M, K, _F32, residual, sum, weights, share, eps),
-                       _array(y, M * K, _F32), _array(q, M * K, _BYTES), M * K, _array(s, ns, _F32), ns,
-                       M, K, _stream_for(stream, x)), "f8_norm")
+    _norm("f8_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _F32), *_f8_out(q, s, M, K)), stream)
 
 
 def f8_norm_bf16(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
                  share: int = 1, y=None, stream=None) -> None:
     """As f8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
-    ns = M * -(-K // 128)
-    _check(lib.f8_norm_bf16(*_norm_inputs(x, gamma, M, K, _BF16, residual, sum, weights, share, eps),
-                            _array(y, M * K, _BF16), _array(q, M * K, _BYTES), M * K,
-                            _array(s, ns, _F32), ns, M, K, _stream_for(stream, x)), "f8_norm_bf16")
+    _norm("f8_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _BF16), *_f8_out(q, s, M, K)), stream)
 
 
-def _halves(gate, up, M, K, dtypes, ld):
-    """Addresses and row distance of [M, K] views whose rows are dense."""
-    if isinstance(gate, int):
-        return gate, 0 if up is None else up, K if ld is None else ld
-    for t in (gate, up):
-        if t is not None and (not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != M
-                              or t.shape[1] != K or t.stride(1) != 1
-                              or (M > 1 and t.stride(0) != gate.stride(0))):
-            raise ValueError("expected [%d, %d] device tensors of %s with dense rows at the same distance, "
-                             "got %s" % (M, K, " or ".join(map(str, dtypes)), _what(t)))
-    return gate.data_ptr(), 0 if up is None else up.data_ptr(), gate.stride(0) if M > 1 else K
+def _half(x, M, K, dtypes) -> int:
+    """Address of an [M, K] view whose rows are dense."""
+    if x is None:
+        return 0
+    if x.is_cuda and x.dtype in dtypes and x.dim() == 2 and x.shape == (M, K) and x.stride(1) == 1:
+        return x.data_ptr()
+    raise ValueError("expected an [%d, %d] device tensor of %s with dense rows, got %s" % (
+        M, K, " or ".join(map(str, dtypes)), _what(x)))
 
 
-def q4_act(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=None, ld=None, stream=None) -> None:
+def _act(entry, dtypes, gate, up, M, K, act, tail, ld, stream) -> None:
+    if type(gate) is int:
+        g, u, ld = gate, up, K if ld is None else ld
+    else:
+        g, u, ld = _half(gate, M, K, dtypes), _half(up, M, K, dtypes), gate.stride(0) if M > 1 else K
+        if up is not None and M > 1 and up.stride(0) != ld:
+            raise ValueError("gate's and up's rows are at different distances: %s, %s" % (_what(gate), _what(up)))
+    _check(getattr(lib, entry)(g, u, ld, act, *tail, M, K, _stream_for(stream, gate)), entry)
+
+
+def q4_act(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=False, ld=None, stream=None) -> None:
     """The gated activation y = f(gate) * up, f SiLU or GELU (tanh form), in f32 or
     bfloat16 by y's type. ``gate`` and ``up`` are f32 [M, K] views with dense
     rows, the halves of one product's rows or two products' results (of
     addresses: ``ld`` elements a row); ``up`` may be None."""
-    at, bf16 = _values(y, M * K)
-    g, u, ld = _halves(gate, up, M, K, _F32, ld)
-    _check(lib.q4_act(g, u, ld, act, at, bf16 if y_bf16 is None else bool(y_bf16), M, K,
-                      _stream_for(stream, gate)), "q4_act")
+    _act("q4_act", _F32, gate, up, M, K, act, _values_out(y, M * K, y_bf16), ld, stream)
 
 
-def q4_act_bf16(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=None, ld=None,
+def q4_act_bf16(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=False, ld=None,
                 stream=None) -> None:
     """As q4_act with ``gate`` and ``up`` in bfloat16."""
-    at, bf16 = _values(y, M * K)
-    g, u, ld = _halves(gate, up, M, K, _BF16, ld)
-    _check(lib.q4_act_bf16(g, u, ld, act, at, bf16 if y_bf16 is None else bool(y_bf16), M, K,
-                           _stream_for(stream, gate)), "q4_act_bf16")
-
-
-def _q8_act(entry, gate, up, out_q, M, K, act, dtypes, ld, stream) -> None:
-    nb = M * (K // 32) * 34
-    g, u, ld = _halves(gate, up, M, K, dtypes, ld)
-    _check(getattr(lib, entry)(g, u, ld, act, _array(out_q, nb, _BYTES), nb, M, K,
-                               _stream_for(stream, gate)), entry)
+    _act("q4_act_bf16", _BF16, gate, up, M, K, act, _values_out(y, M * K, y_bf16), ld, stream)
 
 
 def q8_act(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """q4_act with the result as Q8_0 blocks in the uint8 tensor ``out_q``."""
-    _q8_act("q8_act", gate, up, out_q, M, K, act, _F32, ld, stream)
+    _act("q8_act", _F32, gate, up, M, K, act, _q8_out(out_q, M, K), ld, stream)
 
 
 def q8_act_bf16(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """As q8_act with ``gate`` and ``up`` in bfloat16."""
-    _q8_act("q8_act_bf16", gate, up, out_q, M, K, act, _BF16, ld, stream)
-
-
-def _f8_act(entry, gate, up, q, s, M, K, act, dtypes, ld, stream) -> None:
-    ns = M * -(-K // 128)
-    g, u, ld = _halves(gate, up, M, K, dtypes, ld)
-    _check(getattr(lib, entry)(g, u, ld, act, _array(q, M * K, _BYTES), M * K, _array(s, ns, _F32), ns,
-                               M, K, _stream_for(stream, gate)), entry)
+    _act("q8_act_bf16", _BF16, gate, up, M, K, act, _q8_out(out_q, M, K), ld, stream)
 
 
 def f8_act(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """q4_act with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
     columns, ``s`` [M, ceil(K / 128)]."""
-    _f8_act("f8_act", gate, up, q, s, M, K, act, _F32, ld, stream)
+    _act("f8_act", _F32, gate, up, M, K, act, _f8_out(q, s, M, K), ld, stream)
 
 
 def f8_act_bf16(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """As f8_act with ``gate`` and ``up`` in bfloat16."""
-    _f8_act("f8_act_bf16", gate, up, q, s, M, K, act, _BF16, ld, stream)
+    _act("f8_act_bf16", _BF16, gate, up, M, K, act, _f8_out(q, s, M, K), ld, stream)
 
 
 def raw_status(entry: str, *args) -> int:

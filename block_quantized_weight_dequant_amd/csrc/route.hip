@@ -24,6 +24,8 @@
 // in either order, and two f64 roundings almost never. s takes some 25 f64
 // operations an expert. A step of the selection then compares the keys' upper
 // halves, and the lower ones only where several experts share the largest.
+#include <algorithm>
+
 #include "f64.h"
 #include "launch.h"
 #include "validate.h"
@@ -32,7 +34,6 @@ namespace q4k {
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 constexpr int kMaxExperts = Q4_MAX_EXPERTS, kMaxTopK = Q4_MAX_TOP_K;
-static_assert(kMaxExperts == kRouteThreads, "one thread per expert in the scans");
 
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -126,34 +127,51 @@ __device__ __forceinline__ void route_tokens(const float *__restrict__ logits, i
     }
 }
 
-// W: keys of a wavefront's token in expert order, where groups are ranked.
-template <int W = 1>
+// NT threads, at most MAX_E experts; W: 8-byte keys of a wavefront's token in
+// expert order, where it needs them.
+template <int W = 1, int NT = kRouteThreads, int MAX_E = kMaxExperts>
 struct RouteLds {
-    int cursor[kMaxExperts];                          // next position of each expert
-    int part[kRouteWaves];
+    static constexpr int kThreads = NT;
+    static_assert(MAX_E <= NT, "one thread per expert in the scans");
+    int cursor[MAX_E];                              // next position of each expert
+    int part[NT / 64];
     union {
-        uint16_t waves[kRouteWaves][kMaxExperts];     // slots of a batch, by wavefront and expert
-        double vals[kRouteWaves][W];                  // not needed any more when slots are placed
+        uint16_t waves[NT / 64][MAX_E];             // slots of a batch, by wavefront and expert
+        double vals[NT / 64][W];                    // not needed any more when slots are placed
+        uint64_t keys[NT / 64][W];
     };
 };
 
-// Exclusive prefix sum over the workgroup's threads.
-__device__ __forceinline__ int exclusive_scan(int v, int *part)
+// Inclusive prefix sum over the wavefront: DPP within rows of 16, then each row's
+// last lane into the next row, and lane 31 into the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_from(int v)
+{
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v = add_from<0x111, 0xF>(v);   // row_shr 1
+    v = add_from<0x112, 0xF>(v);   // row_shr 2
+    v = add_from<0x114, 0xF>(v);   // row_shr 4
+    v = add_from<0x118, 0xF>(v);   // row_shr 8
+    v = add_from<0x142, 0xA>(v);   // row_bcast 15 into rows 1 and 3
+    return add_from<0x143, 0xC>(v);   // row_bcast 31 into rows 2 and 3
+}
+
+// Exclusive prefix sum over the workgroup's NW wavefronts.
+template <int NW>
+__device__ __forceinline__ int exclusive_scan(int v, int (&part)[NW])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(s, d);
-        if (lane >= d)
-            s += u;
-    }
+    const int s = wave_scan(v);
     if (lane == 63)
         part[wave] = s;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < wave; ++w)
-        before += part[w];
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        before += w < wave ? part[w] : 0;
     __syncthreads();
     return before + s - v;
 }
@@ -166,8 +184,8 @@ __device__ __forceinline__ void place(Lds &l, Fn expert, int s0, int n, int E, i
                                       int *__restrict__ order)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int b = 0; b < n; b += kRouteThreads) {
-        const int used = (min(n - b, kRouteThreads) + 63) / 64;   // wavefronts with slots
+    for (int b = 0; b < n; b += Lds::kThreads) {
+        const int used = (min(n - b, Lds::kThreads) + 63) / 64;   // wavefronts with slots
         if (tid < E)
             for (int w = 0; w < used; ++w)
                 l.waves[w][tid] = 0;
@@ -186,6 +204,7 @@ __device__ __forceinline__ void place(Lds &l, Fn expert, int s0, int n, int E, i
         __syncthreads();
         if (tid < E) {      // counts -> slots of the batch before each wavefront's
             int before = 0;
+#pragma unroll 4
             for (int w = 0; w < used; ++w) {
                 const int c = l.waves[w][tid];
                 l.waves[w][tid] = (uint16_t)before;
@@ -201,9 +220,42 @@ __device__ __forceinline__ void place(Lds &l, Fn expert, int s0, int n, int E, i
     }
 }
 
+// The counts of a chunk: 16 bits each where they fit (and their padded rows fit the
+// workspace), in rows of whole 16 bytes, so that the second launch, in which every
+// workgroup adds up the whole table, reads half the bytes in wide loads.
+__host__ __device__ inline bool route_narrow(int E, int chunk, int top_k) { return E >= 8 && chunk <= 65535 / top_k; }
+__host__ __device__ inline size_t route_pitch(int E) { return ((size_t)E + 7) / 8 * 8; }
+
 using q4v::route_chunk;
 using q4v::route_chunks;
 constexpr int kOneChunk = q4v::kRouteOneChunk;
+
+// What follows when the chunk's experts are counted in l.cursor: the counts, or,
+// where one workgroup does all of it, the sort.
+template <class Lds>
+__device__ __forceinline__ void route_sort(Lds &l, const uint16_t *s_ids, int *__restrict__ offsets,
+                                           int *__restrict__ order, int *__restrict__ counts, int T, int E,
+                                           int top_k, int chunk, int bits)
+{
+    const int tid = threadIdx.x;
+    __syncthreads();
+    const int count = tid < E ? l.cursor[tid] : 0;
+    if (counts) {
+        if (route_narrow(E, chunk, top_k)) {
+            if (tid < (int)route_pitch(E))
+                reinterpret_cast<uint16_t *>(counts)[(size_t)blockIdx.x * route_pitch(E) + tid] = (uint16_t)count;
+        } else if (tid < E) {
+            counts[(size_t)blockIdx.x * E + tid] = count;
+        }
+        return;
+    }
+    const int at = exclusive_scan(count, l.part);
+    if (tid < E)
+        offsets[tid] = at;
+    if (tid == 0)
+        offsets[E] = T * top_k;
+    place(l, [&](int i) { return (int)s_ids[i]; }, 0, T * top_k, E, bits, at, order);
+}
 
 // One workgroup's chunk: tokens(tok, n, to) chooses the experts of n tokens (the
 // second tok repeats another if n is 1) and leaves the choices of the u-th at
@@ -231,19 +283,7 @@ __device__ __forceinline__ void route_workgroup(Lds &l, uint16_t *s_ids, Tokens 
             if ((tid & 63) < top_k)
                 atomicAdd(&l.cursor[to(u)[tid & 63]], 1);
     }
-    __syncthreads();
-    const int count = tid < E ? l.cursor[tid] : 0;
-    if (counts) {
-        if (tid < E)
-            counts[(size_t)blockIdx.x * E + tid] = count;
-        return;
-    }
-    const int at = exclusive_scan(count, l.part);
-    if (tid < E)
-        offsets[tid] = at;
-    if (tid == 0)
-        offsets[E] = T * top_k;
-    place(l, [&](int i) { return (int)s_ids[i]; }, 0, T * top_k, E, bits, at, order);
+    route_sort(l, s_ids, offsets, order, counts, T, E, top_k, chunk, bits);
 }
 
 template <int V>
@@ -275,6 +315,8 @@ __device__ __forceinline__ Key f64_key(double v)
     return {b.y ^ (flip | 0x80000000u), b.x ^ flip};
 }
 
+__device__ const float kNoBias = 0.0f;
+
 // What a wavefront keeps of its V experts lane + 64 i for all its tokens.
 template <int V>
 struct Experts {
@@ -288,10 +330,11 @@ __device__ __forceinline__ Experts<V> load_experts(const RouteGroups &g, int E, 
 {
     Experts<V> x;
     const int size = E / g.n_groups;
+    const float *bias = g.bias ? g.bias : &kNoBias;   // loads that need no branch stay in flight together
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = min((int)(threadIdx.x & 63) + 64 * i, E - 1);
-        x.bias[i] = g.bias ? g.bias[e] : 0.0f;
+        x.bias[i] = bias[g.bias ? e : 0];
         x.bit[i] = GROUPED ? (e / size) << lanes : 0;
     }
     return x;
@@ -450,6 +493,481 @@ __device__ __forceinline__ void choose_tokens(const float *__restrict__ logits, 
     }
 }
 
+// How four tokens share a wavefront, 16 lanes (a DPP row) each: 2^lanes lanes
+// hold a group's experts, `per` neighbours each; without a choice of groups the
+// row is one group.
+struct RouteRows {
+    int groups, lanes, size, per;
+};
+
+// Largest, and sum, over the 16 lanes of a row, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float v) { return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v))); }
+template <int CTRL>
+__device__ __forceinline__ double dpp_of(double v) { return dpp_f64<CTRL>(v); }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+// The middle one of a >= b and c.
+__device__ __forceinline__ float middle(float a, float b, float c) { return __builtin_amdgcn_fmed3f(a, b, c); }
+__device__ __forceinline__ double middle(double a, double b, double c) { return fmax(b, fmin(a, c)); }
+template <class K>
+__device__ __forceinline__ K row_max(K v)
+{
+    v = larger(v, dpp_of<0xB1>(v));
+    v = larger(v, dpp_of<0x4E>(v));
+    v = larger(v, dpp_of<0x141>(v));
+    return larger(v, dpp_of<0x140>(v));
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max(v, dpp_u32<0xB1>(v));
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    return max(v, dpp_u32<0x140>(v));
+}
+__device__ __forceinline__ double row_sum(double v)
+{
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x141>(v);
+    return v + dpp_f64<0x140>(v);
+}
+
+// Falling order, by Batcher's merge exchange (63 exchanges of 16).
+template <int N>
+__device__ __forceinline__ void sort_falling(uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = v[i + j], b = v[i + j + k];
+                        v[i + j] = max(a, b);
+                        v[i + j + k] = min(a, b);
+                    }
+}
+
+// The value itself, which the compiler then computes where it stands: sunk under the
+// condition of a later choice, each score would be a chain of dependent operations by
+// itself instead of one among sixteen.
+template <class K>
+__device__ __forceinline__ K at_once(K v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Score of one logit that is not masked. Softmax: top is the row's largest logit,
+// share the reciprocal of its sum.
+template <bool SIGMOID>
+__device__ __forceinline__ double score_of(float v, double top, double share)
+{
+    if constexpr (SIGMOID)
+        return rcp_f64(1.0 + exp_f64(fmin(fmax(-(double)v, -700.0), 700.0)));
+    else
+        return exp_f64(fmax((double)v - top, -700.0)) * share;
+}
+
+// A lane's experts e0 .. e0 + n - 1 and what they share for all tokens: `unit`
+// steps of a key's code to 1, and keys whose codes are up to `blur` steps apart may
+// come in either order.
+template <int CAP, class K>
+struct RowExperts {
+    float bias[CAP];   // of places without an expert: -inf
+    int e0, n, group;
+    K unit, margin;    // groups' sums up to `margin` apart may be in either order
+    uint32_t blur;
+};
+constexpr uint32_t kMostSteps = (1u << 24) - 1024, kMaskedCode = 1;
+
+// CAP floats from byte `at` on, zeros past the buffer: whole 16-byte loads at any
+// 4-byte alignment, without a branch, so that all stay in flight together.
+template <int CAP>
+__device__ __forceinline__ void load_row(float (&v)[CAP], __amdgpu_buffer_rsrc_t b, uint32_t at)
+{
+#pragma unroll
+    for (int i = 0; i < CAP; i += 4) {
+        const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(b, at + 4 * i, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[i + k] = __uint_as_float(q[k]);
+    }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const float *p, size_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(p), 0, (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000);
+}
+
+template <int CAP, class K>
+__device__ __forceinline__ void place_row_experts(RowExperts<CAP, K> &x, const float *logits, const RouteGroups &g,
+                                                  const RouteRows &r, int E)
+{
+    const int p = threadIdx.x & 15, part = p & ((1 << r.lanes) - 1);
+    x.group = p >> r.lanes;
+    x.n = x.group < r.groups ? min(max(r.size - part * r.per, 0), r.per) : 0;
+    x.e0 = x.n ? x.group * r.size + part * r.per : 0;
+    load_row(x.bias, row_buffer(g.bias ? g.bias : logits, g.bias ? (size_t)E * 4 : 0), (uint32_t)x.e0 * 4);
+}
+
+// Scores lie in [0, 1], so keys span at most 1 more than the finite biases and 0
+// (hi + lo). Errors of a key: f64 (softmax): far below a step, which two roundings
+// to steps can turn into two. f32 (sigmoid): the exponent's rounding moves the score
+// by s (1 - s) |l| 2^-23.7 <= 2^-25.8, the exponential by s (1 - s) 2^-23 <= 2^-25,
+// 1 + e and the reciprocal by s 1.5 2^-23, all together 2^-22, the sum with the bias by 2^-24 (1 + |bias|); the distance and its
+// product with `unit` are within 2^-24 of the range each. Twice all that is below
+// 2^-20 + 2^-22 (1 + the largest |bias|), and so is a sum of two keys' error.
+template <int CAP, class K>
+__device__ __forceinline__ void scale_row_experts(RowExperts<CAP, K> &x)
+{
+    float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) {
+        const float b = fabsf(x.bias[i]) < __builtin_inff() ? x.bias[i] : 0.0f;   // 0 of NaN too
+        hi = larger(hi, b);   // places past the lane's experts only widen the range
+        lo = smaller(lo, b);
+        x.bias[i] = i < x.n ? x.bias[i] : -__builtin_inff();
+    }
+    hi = row_max(hi);
+    lo = row_max(-lo);
+    const float range = 1.0f + (hi + lo), unit = (float)kMostSteps * 0.999999f * __builtin_amdgcn_rcpf(range);
+    x.unit = (K)unit;
+    if constexpr (sizeof(K) == 4) {
+        const float err = 0x1p-20f + 0x1p-22f * (1.0f + larger(hi, lo));
+        // Four keys' errors, and the roundings of two sums and of the comparison.
+        x.margin = 0x1p-20f + 12 * 0x1p-24f * (1.0f + larger(hi, lo));
+        // Beyond 500 steps all is uncertain (the masked code is 1000 away).
+        x.blur = err * unit < 500.0f ? (uint32_t)(err * unit) + 4u : ~0u;
+    } else {
+        x.margin = 0x1p-48 * (double)range;
+        x.blur = 2u;
+    }
+}
+
+// LDS of a wavefront of rows: the tokens' logits by lane and place (a lane's at a
+// pitch that spreads them over the banks), and the keys of a token that is chosen
+// exactly.
+constexpr int kRowThreads = 512, kRowWaves = kRowThreads / 64, kRowExperts = 256, kRowTopK = 15;
+struct RowLds {
+    float logits[64 * 17];
+    union {
+        double vals[kRowExperts];
+        uint64_t keys[kRowExperts];
+    };
+};
+
+// One token by the whole wavefront, with keys in f64: into l.vals, masked ones
+// -inf; returns the groups that can be chosen (bits as best_groups').
+template <bool GROUPED, bool SIGMOID>
+__device__ __forceinline__ uint64_t exact_keys(const float *__restrict__ row, const RouteGroups &g, int lanes,
+                                               RowLds &l, int E)
+{
+    const int lane = threadIdx.x & 63;
+    const float ninf = -__builtin_inff();
+    double top = 0.0, share = 1.0;
+    if constexpr (!SIGMOID) {
+        uint32_t m = logit_key(ninf);
+        for (int e = lane; e < E; e += 64)
+            m = max(m, row[e] > ninf ? logit_key(row[e]) : 0u);
+        const float t = key_logit(wave_max_u32(m));
+        top = t > ninf ? (double)t : 0.0;
+        double sum = 0.0;
+        for (int e = lane; e < E; e += 64)
+            sum += row[e] > ninf ? score_of<SIGMOID>(row[e], top, 1.0) : 0.0;
+        share = rcp_f64(fmax(wave_sum_f64(sum), 0x1p-1000));
+    }
+    const float *bias = g.bias ? g.bias : row;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+    for (int e = lane; e < E; e += 64) {
+        const float v = row[e], b = g.bias ? bias[e] : 0.0f;
+        l.vals[e] = (v > ninf) & (b > ninf) ? score_of<SIGMOID>(v, top, share) + (double)b : -__builtin_inf();
+    }
+    __builtin_amdgcn_wave_barrier();
+    return GROUPED ? best_groups(l.vals, g, E, lanes) : 0;
+}
+
+// One token's choices by the whole wavefront, the lowest expert among equals.
+// Small and slow: hardly a token needs it.
+template <bool GROUPED, bool SIGMOID>
+__device__ __forceinline__ void choose_exactly(const float *__restrict__ row, const RouteGroups &g, int lanes,
+                                               RowLds &l, int E, int top_k, uint16_t *out)
+{
+    const int lane = threadIdx.x & 63, size = E / g.n_groups;
+    const uint64_t kept = exact_keys<GROUPED, SIGMOID>(row, g, lanes, l, E);
+    __builtin_amdgcn_wave_barrier();
+    for (int e = lane; e < E; e += 64) {
+        const double v = l.vals[e];
+        const Key k = f64_key(v);
+        const uint64_t key = v > -__builtin_inf() ? (uint64_t)k.hi << 32 | k.lo : 1u;
+        l.keys[e] = !GROUPED || (kept >> (e / size << lanes) & 1) ? key : 0u;
+    }
+    for (int j = 0; j < top_k; ++j) {
+        __builtin_amdgcn_wave_barrier();
+        uint64_t mine = 0;
+        int at = lane;
+        for (int e = lane; e < E; e += 64)
+            if (l.keys[e] > mine)
+                mine = l.keys[e], at = e;
+        const uint32_t hi = wave_max_u32((uint32_t)(mine >> 32));
+        const uint32_t lo = wave_max_u32((uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+        const bool best = mine == ((uint64_t)hi << 32 | lo);
+        const int id = 2 * kMaxExperts - (int)wave_max_u32(best ? (uint32_t)(2 * kMaxExperts - at) : 0u);
+        __builtin_amdgcn_wave_barrier();
+        if (lane == 0) {
+            out[j] = (uint16_t)id;
+            l.keys[id] = 0;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Tokens by four rows of a wavefront: tok is uniform within a row, v its logits,
+// `in` where it is not a repetition. Choice j goes to out[j], and with its weight to
+// ids and weights.
+//
+// A key (s + bias: sigmoid scores in f32 here, softmax scores in f64) becomes a
+// code of 24 bits, its distance from the row's largest in steps of the range that
+// keys can have, with the expert's lane and its place in the lane in the eight bits
+// below, so that equal codes are in the order of their experts. A lane sorts its
+// codes once, and a step of the selection is a maximum over the row's heads (four DPP
+// moves) for four tokens at a time, and one head taken off. Codes near enough to be
+// in the wrong order are taken along, and ordered by f64 keys, which the weights need
+// of each candidate anyway. Where that does not settle it (more than 16 candidates)
+// the token is chosen again, exactly.
+template <int CAP, bool GROUPED, bool SIGMOID, class K>
+__device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__restrict__ logits, const RouteGroups &g,
+                                            const RouteRows &r, const RowExperts<CAP, K> &x, RowLds &l, int lanes,
+                                            int E, int top_k, int *__restrict__ ids, float *__restrict__ weights,
+                                            int tok, bool in, uint16_t *out)
+{
+    const int lane = threadIdx.x & 63, p = lane & 15;
+    const float ninf = -__builtin_inff();
+    const K none = -(K)__builtin_inf();
+#pragma unroll
+    for (int i = 0; i < CAP; ++i)
+        l.logits[lane * 17 + i] = v[i];
+    double top = 0.0, share = 1.0;
+    K key[CAP];
+    if constexpr (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < CAP; ++i)
+            key[i] = at_once(__builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v[i] * -1.44269504f)) + x.bias[i]);
+    } else {
+        float m = ninf;
+#pragma unroll
+        for (int i = 0; i < CAP; ++i)
+            m = fmaxf(m, i < x.n ? v[i] : ninf);   // of NaN the other
+        m = row_max(m);
+        top = m > ninf ? (double)m : 0.0;
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < CAP; ++i) {
+            key[i] = at_once(score_of<SIGMOID>(v[i], top, 1.0));
+            sum += (i < x.n) & (v[i] > ninf) ? key[i] : 0.0;
+        }
+        share = rcp_f64(fmax(row_sum(sum), 0x1p-1000));
+#pragma unroll
+        for (int i = 0; i < CAP; ++i)
+            key[i] = key[i] * share + (double)x.bias[i];
+    }
+    K first = none, second = none;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) {
+        // Masked by the logit (-inf or NaN) or the bias, or absent. (The minimum of
+        // NaN and a number is NaN here.)
+        key[i] = __builtin_elementwise_minimum(v[i], x.bias[i]) > ninf ? key[i] : none;
+        if (GROUPED)
+            second = middle(first, second, key[i]);
+        first = larger(first, key[i]);
+    }
+    bool open = x.n > 0;   // the lane's experts can be chosen
+    const K mine = first;
+    if constexpr (GROUPED) {
+        const auto merge = [&](K f, K s) __attribute__((always_inline)) {
+            second = larger(smaller(first, f), larger(second, s));
+            first = larger(first, f);
+        };
+        if (r.lanes > 0)
+            merge(dpp_of<0xB1>(first), dpp_of<0xB1>(second));
+        if (r.lanes > 1)
+            merge(dpp_of<0x4E>(first), dpp_of<0x4E>(second));
+        if (r.lanes > 2)
+            merge(dpp_of<0x141>(first), dpp_of<0x141>(second));
+        const K score = g.group_best == 2 ? first + second : first;
+        // Lanes of the row (whole groups, by turning it) whose sum is better for
+        // certain, and those that may be, the lane's own group among them.
+        int ahead = 0, maybe = 1;
+        const K above = score + x.margin, below = score - x.margin;
+        unroll<15>([&](auto turn) __attribute__((always_inline)) {
+            const K other = dpp_of<0x121 + turn.value>(score);   // row_ror 1 .. 15
+            ahead += other > above;
+            maybe += !(other < below);
+        });
+        ahead >>= r.lanes;
+        maybe >>= r.lanes;
+        const bool sure = (maybe <= g.top_groups) | (ahead >= g.top_groups);
+        open = open & (maybe <= g.top_groups);
+        // Sums too near to tell, once in some ten thousand tokens: by f64 keys.
+        uint64_t unsure = __ballot((x.n > 0) & !sure);
+        while (unsure) {
+            const int u = __builtin_ctzll(unsure) & 48;
+            unsure &= ~(0xFFFFull << u);
+            const size_t t = (size_t)__builtin_amdgcn_readlane(tok, u);
+            const uint64_t kept = exact_keys<GROUPED, SIGMOID>(logits + t * (size_t)E, g, lanes, l, E);
+            if ((lane & 48) == u)
+                open = (x.n > 0) & (kept >> (x.group << lanes) & 1) != 0;
+        }
+    }
+    const K most = row_max(open ? mine : none);
+    uint32_t code[CAP];
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) {
+        const K far = smaller(larger((most - key[i]) * x.unit, (K)0), (K)kMostSteps);
+        const uint32_t steps = key[i] > none ? 0x00FFFFFFu - (uint32_t)far : kMaskedCode;
+        code[i] = open & (i < x.n) ? steps << 8 | (uint32_t)((15 - p) << 4 | (15 - i)) : 0u;
+    }
+    sort_falling(code);
+    // Codes are taken until what is left is certain to be smaller than the top_k-th. A
+    // lane offers its eight largest: a row that would take more of one is not certain.
+    constexpr int LIST = CAP < 8 ? CAP : 8;
+    uint32_t taken = 0, best = 0;   // lane j's: the j-th code
+    int offered = 0;
+    const auto take = [&](int j) __attribute__((always_inline)) {
+        taken = p == j ? best : taken;
+        if (code[0] == best) {
+            ++offered;
+#pragma unroll
+            for (int i = 0; i + 1 < LIST; ++i)
+                code[i] = code[i + 1];
+            code[LIST - 1] = 0;
+        }
+    };
+#pragma unroll 1
+    for (int j = 0; j < top_k; ++j) {
+        best = row_max(code[0]);
+        take(j);
+    }
+    const uint32_t last = best;
+    bool more = true;
+#pragma unroll 1
+    for (int j = top_k; j < 16; ++j) {
+        best = row_max(code[0]);
+        more = ((last >> 8) - (best >> 8) <= x.blur) & (best >> 8 > kMaskedCode);
+        if (!__ballot(more))
+            break;
+        take(j);
+    }
+    const bool doubt = more | ((CAP > LIST) & (offered >= LIST) & (x.n > LIST));
+
+    // Lane p: candidate p, its score in f64.
+    const int from = (lane & 48) + 15 - (int)(taken >> 4 & 15u), at = 15 - (int)(taken & 15u);
+    int id = __shfl(x.e0, from) + at;
+    float logit = l.logits[from * 17 + (at < CAP ? at : 0)];
+    bool masked = taken >> 8 <= kMaskedCode;
+    double s = at_once(score_of<SIGMOID>(logit, top, share));
+    s = masked ? 0.0 : s;
+    const uint32_t next = dpp_u32<0x101>(taken);   // row_shl 1: the lane after
+    const bool near = (next >> 8 > kMaskedCode) & ((taken >> 8) - (next >> 8) <= x.blur);
+    if (__ballot(near)) {
+        // Some neighbours may be in the wrong order: by their f64 keys, then, the lowest
+        // expert among equals.
+        const float b = (g.bias ? g.bias : logits)[masked ? 0 : id];
+        const double k = masked ? -__builtin_inf() : s + (double)(g.bias ? b : 0.0f);
+        int rank = 0;
+        unroll<15>([&](auto turn) __attribute__((always_inline)) {
+            constexpr int C = 0x121 + turn.value;
+            const double other = dpp_of<C>(k);
+            rank += (other > k) | ((other == k) & ((int)dpp_u32<C>((uint32_t)(masked ? 4096 + p : id)) < (masked ? 4096 + p : id)));
+        });
+        const int to = ((lane & 48) + rank) * 4;   // a permutation of the row
+        id = __builtin_amdgcn_ds_permute(to, id);
+        const u32x2 h = bitcast<u32x2>(s);
+        s = bitcast<double>((u32x2){(uint32_t)__builtin_amdgcn_ds_permute(to, (int)h.x), (uint32_t)__builtin_amdgcn_ds_permute(to, (int)h.y)});
+    }
+    if (p < top_k)
+        out[p] = (uint16_t)id;
+    uint64_t unsure = __ballot(doubt);
+    while (unsure) {
+        const int u = __builtin_ctzll(unsure) & 48;
+        unsure &= ~(0xFFFFull << u);
+        __builtin_amdgcn_wave_barrier();
+        const int t = __builtin_amdgcn_readlane(tok, u);
+        const uint64_t o = reinterpret_cast<uint64_t>(out);
+        uint16_t *to = reinterpret_cast<uint16_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(o >> 32), u) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((int)o, u));
+        choose_exactly<GROUPED, SIGMOID>(logits + (size_t)t * (size_t)E, g, lanes, l, E, top_k, to);
+        if ((lane & 48) == u && p < top_k) {
+            id = out[p];
+            logit = logits[(size_t)tok * (size_t)E + id];
+            s = at_once(score_of<SIGMOID>(logit, top, share));
+            s = (logit > ninf) & ((g.bias ? g.bias[id] : 0.0f) > ninf) ? s : 0.0;
+        }
+    }
+
+    s = p < top_k ? s : 0.0;
+    const double total = row_sum(s);
+    const double w = g.renorm ? (total > 0.0 ? s * rcp_f64(total) : 0.0) : s;
+    if (in && p < top_k) {
+        const size_t to = (size_t)tok * (size_t)top_k + p;
+        ids[to] = id;
+        weights[to] = (float)(w * (double)g.scale);
+    }
+}
+
+// Up to 256 experts in rows of lanes, four tokens a wavefront at a time.
+template <int CAP, bool GROUPED, bool SIGMOID>
+__global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restrict__ logits, RouteGroups g,
+                                                           RouteRows r, int lanes, int *__restrict__ ids,
+                                                           float *__restrict__ weights, int *__restrict__ offsets,
+                                                           int *__restrict__ order, int *__restrict__ counts, int T,
+                                                           int E, int top_k, int chunk, int bits)
+{
+    using K = std::conditional_t<SIGMOID, float, double>;
+    __shared__ RouteLds<1, kRowThreads, kRowExperts> l;
+    __shared__ RowLds rows[kRowWaves];
+    __shared__ uint16_t s_ids[kOneChunk * kRowTopK];   // the choices of a chunk that is alone, or of a pass
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, T);
+    // The chunk's logits span less than 2^31 bytes: 256 of them all are on the card.
+    const __amdgpu_buffer_rsrc_t all = row_buffer(logits + (size_t)t0 * (size_t)E, (size_t)(T - t0) * (size_t)E * 4);
+    RowExperts<CAP, K> x;
+    float v[CAP];
+    place_row_experts(x, logits, g, r, E);
+    const auto fetch = [&](int t) __attribute__((always_inline)) {
+        load_row(v, all, ((uint32_t)min(t + (lane >> 4), t1 - 1) - (uint32_t)t0) * (uint32_t)E * 4u + (uint32_t)x.e0 * 4u);
+    };
+    fetch(t0 + 4 * wave);
+    if (tid < E)
+        l.cursor[tid] = 0;
+    __syncthreads();
+    scale_row_experts(x);
+    for (int t = t0 + 4 * wave; t < t1; t += 4 * kRowWaves) {
+        const int mine = t + (lane >> 4), tok = min(mine, t1 - 1);
+        uint16_t *out = s_ids + (mine - t0) % kOneChunk * top_k;
+        choose_rows<CAP, GROUPED, SIGMOID>(v, logits, g, r, x, rows[wave], lanes, E, top_k, ids, weights, tok, mine < t1, out);
+        if (t + 4 * kRowWaves < t1)
+            fetch(t + 4 * kRowWaves);
+        if (mine < t1 && (lane & 15) < top_k)
+            atomicAdd(&l.cursor[out[lane & 15]], 1);
+        __builtin_amdgcn_wave_barrier();
+    }
+    route_sort(l, s_ids, offsets, order, counts, T, E, top_k, chunk, bits);
+}
+
+// Every size: one token a wavefront at a time.
 template <int V, bool GROUPED>
 __global__ __launch_bounds__(kRouteThreads) void k_route_groups(const float *__restrict__ logits,
                                                                RouteGroups g, int lanes,
@@ -477,48 +995,64 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_groups(const float *__r
     route_workgroup(l, s_ids, tokens, offsets, order, counts, T, E, top_k, chunk, bits);
 }
 
-// Chunk c's slots to their places: thread (p, e) sums expert e's counts over
-// the chunks c' = p mod parts, all of them and those before c.
+// The slots of chunks c0 = blockIdx.x run .. c0 + run - 1 to their places, after the
+// sums of the experts' counts over all chunks and over those before c0. NARROW:
+// 16-bit counts, eight experts a thread.
+template <bool NARROW>
 __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__restrict__ ids,
                                                               const int *__restrict__ counts,
                                                               int *__restrict__ offsets,
                                                               int *__restrict__ order, int T, int E,
-                                                              int top_k, int chunk, int chunks,
+                                                              int top_k, int chunk, int chunks, int run,
                                                               int bits)
 {
+    constexpr int W = NARROW ? 8 : 1;   // experts a thread
     __shared__ RouteLds<> l;
-    __shared__ int sums[2][kRouteThreads];
-    const int tid = threadIdx.x, c = blockIdx.x;
-    const int width = 1 << bits, parts = kRouteThreads / width;   // E <= width <= 1024
-    const int e = tid & (width - 1), p = tid >> bits;
-    int all = 0, before = 0;
-    if (e < E) {
+    __shared__ int sums[2][W * kRouteThreads];
+    const int tid = threadIdx.x, c0 = blockIdx.x * run;
+    const int width = max(1, (1 << bits) / W), parts = kRouteThreads / width;   // threads a row of the table, rows at a time
+    const int q = tid % width, p = tid / width;
+    int all[W] = {}, before[W] = {};
+    if (q * W < E) {
+        const auto add = [&](int k, int i, int v) __attribute__((always_inline)) {
+            all[i] += v;
+            before[i] += k < c0 ? v : 0;
+        };
 #pragma unroll 8
         for (int k = p; k < chunks; k += parts) {
-            const int v = counts[(size_t)k * E + e];
-            all += v;
-            before += k < c ? v : 0;
+            if constexpr (NARROW) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(counts) +
+                                                                 (size_t)k * route_pitch(E) + q * 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    add(k, i, (int)(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xFFFFu));
+            } else {
+                add(k, 0, counts[(size_t)k * E + q]);
+            }
         }
     }
-    sums[0][tid] = all;
-    sums[1][tid] = before;
+    // Part p's sums at p's row of `width` W experts.
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        sums[0][tid * W + i] = all[i];
+        sums[1][tid * W + i] = before[i];
+    }
     __syncthreads();
-    all = before = 0;
-    if (tid < E) {
-        for (int q = 0; q < parts; ++q) {
-            all += sums[0][(q << bits) + tid];
-            before += sums[1][(q << bits) + tid];
+    int total = 0, ahead = 0;
+    if (tid < E)
+        for (int k = 0; k < parts; ++k) {
+            total += sums[0][k * width * W + tid];
+            ahead += sums[1][k * width * W + tid];
         }
-    }
-    const int first = exclusive_scan(all, l.part);
-    if (c == 0) {
+    const int first = exclusive_scan(total, l.part);
+    if (c0 == 0) {
         if (tid < E)
             offsets[tid] = first;
         if (tid == 0)
             offsets[E] = T * top_k;
     }
-    const int s0 = c * chunk * top_k, n = (min((c + 1) * chunk, T) - c * chunk) * top_k;
-    place(l, [&](int i) { return ids[s0 + i]; }, s0, n, E, bits, first + before, order);
+    const int s0 = c0 * chunk * top_k, n = ((int)min((long long)(c0 + run) * chunk, (long long)T) - c0 * chunk) * top_k;
+    place(l, [&](int i) { return ids[s0 + i]; }, s0, n, E, bits, first + ahead, order);
 }
 
 static int expert_bits(int E)
@@ -534,8 +1068,11 @@ static hipError_t launch_place(const int *ids, const int *counts, int *offsets, 
                                int top_k, hipStream_t st)
 {
     const int chunk = route_chunk(T), chunks = route_chunks(T);
-    return launch_kernel(k_route_place, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, ids, counts,
-                         offsets, order, T, E, top_k, chunk, chunks, expert_bits(E));
+    // As many chunks a workgroup as give every thread a slot.
+    const int run = std::max(1, kRouteThreads / (chunk * top_k));
+    auto kernel = route_narrow(E, chunk, top_k) ? k_route_place<true> : k_route_place<false>;
+    return launch_kernel(kernel, dim3((unsigned)((chunks + run - 1) / run)), dim3(kRouteThreads), 0, st, ids,
+                         counts, offsets, order, T, E, top_k, chunk, chunks, run, expert_bits(E));
 }
 
 hipError_t launch_route(const float *logits, int *ids, float *weights, int *offsets, int *order,
@@ -559,17 +1096,39 @@ static auto groups_kernel(int E)
          : E <= 256 ? k_route_groups<4, GROUPED> : k_route_groups<16, GROUPED>;
 }
 
+template <bool GROUPED, bool SIGMOID>
+static auto rows_kernel(int per)
+{
+    return per <= 4 ? k_route_rows<4, GROUPED, SIGMOID> : per <= 8 ? k_route_rows<8, GROUPED, SIGMOID>
+                                                                   : k_route_rows<16, GROUPED, SIGMOID>;
+}
+
 hipError_t launch_route_groups(const float *logits, const RouteGroups &g, int *ids, float *weights,
                                int *offsets, int *order, void *workspace, int T, int E, int top_k,
                                hipStream_t st)
 {
     const int chunk = route_chunk(T), chunks = route_chunks(T);
     int *counts = chunks > 1 ? static_cast<int *>(workspace) : nullptr;
+    const bool grouped = g.top_groups < g.n_groups;
     int lanes = 6;
     while (g.n_groups << lanes > 64)
         --lanes;
-    auto kernel = g.top_groups < g.n_groups ? groups_kernel<true>(E) : groups_kernel<false>(E);
-    hipError_t e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, logits, g,
+    // Rows of 16 lanes hold up to 16 groups, 16 experts a lane, and 15 choices with the one after them.
+    RouteRows r = {grouped ? g.n_groups : 1, 4, 0, 0};
+    while (r.groups << r.lanes > 16 && r.lanes > 0)
+        --r.lanes;
+    r.size = E / r.groups;
+    r.per = (r.size + (1 << r.lanes) - 1) >> r.lanes;
+    hipError_t e;
+    if (r.groups <= 16 && r.per <= 16 && top_k <= kRowTopK) {
+        auto kernel = grouped ? (g.sigmoid ? rows_kernel<true, true>(r.per) : rows_kernel<true, false>(r.per))
+                              : (g.sigmoid ? rows_kernel<false, true>(r.per) : rows_kernel<false, false>(r.per));
+        e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRowThreads), 0, st, logits, g, r, lanes, ids, weights,
+                          offsets, order, counts, T, E, top_k, chunk, expert_bits(E));
+        return e != hipSuccess || !counts ? e : launch_place(ids, counts, offsets, order, T, E, top_k, st);
+    }
+    auto kernel = grouped ? groups_kernel<true>(E) : groups_kernel<false>(E);
+    e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRouteThreads), 0, st, logits, g,
                                  lanes, ids, weights, offsets, order, counts, T, E, top_k, chunk,
                                  expert_bits(E));
     if (e != hipSuccess || !counts)

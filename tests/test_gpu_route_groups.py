@@ -113,6 +113,47 @@ def test_far_logits(sigmoid):
     check(x, None, 4, sigmoid)
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,G,top", [(64, 1, 1), (128, 1, 1), (256, 1, 1), (256, 8, 4), (160, 8, 3), (240, 15, 4), (60, 5, 2)])
+def test_keys_an_f32_step_apart(E, G, top, biased):
+    # Logits some steps of f32 apart, in any order: scores that f32 cannot tell apart,
+    # from a few at the edge of the choice to all of them, and groups' sums with them.
+    g = np.random.default_rng(E + G)
+    T = 96
+    x = g.normal(0, 1, (T, E)).astype(np.float32)
+    for t in range(T):
+        n = [2, 3, 5, 12, 20, E][t % 6]
+        at = np.argsort(-x[t], kind="stable")[t % 9:][:n]
+        near = np.float32(x[t, at[0]]) + np.arange(len(at)) * np.float32(2.0 ** -23 * (1 + t % 3))
+        x[t, at] = g.permutation(near.astype(np.float32))
+    b = np.where(g.random(E) < 0.5, np.float32(0.125), np.float32(0.125 + 2.0 ** -24)).astype(np.float32) if biased else None
+    for k in (1, 6, 8, 15, 16):
+        if k <= top * (E // G):
+            check(x, b, k, True, G, top, 2)
+            check(x, b, k, False, G, top, 1)
+
+
+@pytest.mark.parametrize("E,G,top", [(256, 1, 1), (256, 8, 4), (128, 1, 1), (250, 10, 3)])
+def test_the_best_are_neighbours(E, G, top):
+    # The best sixteen experts side by side, from every start.
+    x = np.random.default_rng(3).normal(0, 1, (E - 15, E)).astype(np.float32)
+    for t in range(E - 15):
+        x[t, t:t + 16] += 6
+    for k in (8, 12, 15):
+        check(x, None, k, True, G, top, 2)
+
+
+def test_large_biases_blur_f32():
+    # Keys near 10^4 and 10^7, where f32 holds no score.
+    x, _ = make(70, 256, 12)
+    for size in (1e4, 1e7):
+        b = np.full(256, size, dtype=np.float32)
+        check(x, b, 8, True, 8, 4, 2)
+        b[::3] = -size
+        check(x, b, 8, True, 8, 4, 2)
+        check(x, b, 8, False, 1, 1, 1)
+
+
 def test_biases_decide():
     # Large biases of both signs order the experts, the scores weigh them.
     x, _ = make(90, 256, 4)
