@@ -388,9 +388,10 @@ def _scratch(nbytes: int, stream, like):
     """A uint8 device tensor of nbytes from PyTorch's caching allocator, marked
     as in use by ``stream`` so that it is not handed out again before the work
     queued there has finished."""
-    import torch
     dev = like.device if hasattr(like, "device") else torch.device("cuda", torch.cuda.current_device())
     t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is None:
+        return t
     if isinstance(stream, torch.cuda.Stream):
         t.record_stream(stream)
     elif isinstance(stream, int) and stream != 0:

@@ -32,6 +32,24 @@ __device__ __forceinline__ double wave_sum_f64(double v)
     return (readlane_f64(v, 0) + readlane_f64(v, 16)) + (readlane_f64(v, 32) + readlane_f64(v, 48));
 }
 
+// The same over each 16 or 32 neighbouring lanes.
+template <int L>
+__device__ __forceinline__ double lanes_sum_f64(double v)
+{
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x141>(v);
+    v += dpp_f64<0x140>(v);
+    if constexpr (L == 32) {
+        // Rows of 16 lanes 0 and 1, and 2 and 3, change places.
+        const u32x2 b = bitcast<u32x2>(v);
+        const auto lo = __builtin_amdgcn_permlane16_swap(b.x, b.x, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(b.y, b.y, false, false);
+        v = bitcast<double>((u32x2){lo[0], hi[0]}) + bitcast<double>((u32x2){lo[1], hi[1]});
+    }
+    return v;
+}
+
 // 1 / sqrt(v) for normal v > 0: each Newton step squares the estimate's error
 // (2^-14 at most at the start), to within 2^-51.
 __device__ __forceinline__ double rsqrt_f64(double v)

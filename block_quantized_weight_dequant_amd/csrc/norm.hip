@@ -11,22 +11,30 @@
 // is the exact sum rounded once but for sums that cancel past 2^-53), and so are
 // the squares: two full-rate f64 operations an element, a fortieth of the time
 // its bytes take, and the result does not depend on the order of the sums but in
-// one row of some 10^7.
+// one row of some 10^7. f32 sums instead are 1 to 4 % faster on every size measured.
+//
+// Measured, with cold rows: 2048 x 4096, two experts' f32 rows and a residual to
+// bfloat16, 27.0 us, 5.6 TB/s (a plain stream of the same bytes 25.9); 1001 x 4096
+// bfloat16 to E4M3 7.6 us (5.4); one row 3.0 us (2.2).
 #include "f64.h"
 #include "launch.h"
 #include "rows_out.h"
 
 namespace q4k {
 
-template <class T, RowForm O, bool COMBINE, int RW, int V>
+// SUB rows share a wavefront (then RW and V are 1): rows of up to 64 / SUB pieces,
+// the heads of an attention layer (65536 x 128 bfloat16: 7.8 us, 4.3 TB/s; a wavefront
+// a row 17.4).
+template <class T, RowForm O, bool COMBINE, int RW, int V, int SUB>
 __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, double inv_k, int first)
 {
-    constexpr int P = kPiece<T>, ROWS = RW < 4 ? 4 / RW : 1;
-    __shared__ double part[ROWS][RW];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    static_assert(SUB == 1 || (RW == 1 && V == 1), "whole rows in a piece a lane");
+    constexpr int P = kPiece<T>, WAVES = RW < 4 ? 4 / RW : 1, ROWS = WAVES * SUB, LANES = 64 / SUB;
+    __shared__ double part[WAVES][RW];
+    const int lane = threadIdx.x & (LANES - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int w = wave % RW, slot = wave / RW;
-    const long long want = ((long long)blockIdx.x + first) * ROWS + slot;
-    const size_t row = (size_t)(want < a.M ? want : a.M - 1);   // the last rows' spare wavefronts write nothing
+    const long long want = ((long long)blockIdx.x + first) * ROWS + (SUB > 1 ? (int)threadIdx.x / LANES : slot);
+    const size_t row = (size_t)(want < a.M ? want : a.M - 1);   // the last rows' spare lanes write nothing
     const bool live = want < a.M;
 
     const T *x = static_cast<const T *>(a.x) + row * (size_t)a.share * (size_t)a.K;
@@ -37,7 +45,7 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
     float h[V][P], gamma[V][P];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = ((i * RW + w) * 64 + lane) * P;
+        const int c = ((i * RW + w) * LANES + lane) * P;
         in[i] = c < a.K;
         col[i] = in[i] ? c : 0;
     }
@@ -122,7 +130,7 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
             piece = fma((double)h[i][k], (double)h[i][k], piece);
         sq += in[i] ? piece : 0.0;
     }
-    sq = wave_sum_f64(sq);
+    sq = SUB > 1 ? lanes_sum_f64<LANES>(sq) : wave_sum_f64(sq);
     if constexpr (RW > 1) {
         if (lane == 0)
             part[slot][w] = sq;
@@ -144,22 +152,36 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
             h[i][k] = h[i][k] * rstd * gamma[i][k];
         if (a.dense && live && in[i])
             store_piece(static_cast<T *>(a.dense) + row * (size_t)a.K + col[i], h[i]);
-        put_piece<O>(a.out, a.K, h[i], in[i] && live, row, col[i]);
+        put_piece<O, LANES>(a.out, a.K, h[i], in[i] && live, row, col[i]);
     }
 }
 
-template <class T, RowForm O, bool COMBINE, int RW, int V>
+template <class T, RowForm O, bool COMBINE, int RW, int V, int SUB = 1>
 static hipError_t launch_rows(const NormArgs &a, hipStream_t st)
 {
-    constexpr int ROWS = RW < 4 ? 4 / RW : 1;
-    return launch_parts(k_norm<T, O, COMBINE, RW, V>, ((long long)a.M + ROWS - 1) / ROWS, 1, RW < 4 ? 256 : 64 * RW,
+    constexpr int ROWS = (RW < 4 ? 4 / RW : 1) * SUB;
+    return launch_parts(k_norm<T, O, COMBINE, RW, V, SUB>, ((long long)a.M + ROWS - 1) / ROWS, 1, RW < 4 ? 256 : 64 * RW,
                         st, a, 1.0 / a.K);
 }
 
+// As many wavefronts a row as take it in one piece a lane: the shortest way for few
+// rows, and for many (1001 x 4096 bfloat16 to E4M3 7.6 us with 8 wavefronts a row,
+// 8.3 with 4 of two pieces). From 9 to 16 of them the workgroups get so large that
+// two are on a compute unit at a time; many rows of those take two pieces a lane
+// in 8 wavefronts, unless experts' rows are added (us, 16 x 1 and 8 x 2; f32):
+//                              M = 512     1024        2048
+//   4096 to f32                7.2  7.0  14.1 13.1   25.6 23.9
+//   4096 to Q8_0               6.7  7.5  12.7 12.0   22.7 21.2
+//   4096 to E4M3               7.1  7.3  12.9 11.8   22.6 20.9
+//   4096 to bfloat16, of 2                           27.0 29.1
 template <class T, RowForm O, bool COMBINE>
 static hipError_t launch_width(const NormArgs &a, hipStream_t st)
 {
-    const int waves = (a.K / kPiece<T> + 63) / 64;   // wavefronts of one piece a lane
+    const int pieces = a.K / kPiece<T>, waves = (pieces + 63) / 64;   // wavefronts of one piece a lane
+    if (pieces <= 16)
+        return launch_rows<T, O, COMBINE, 1, 1, 4>(a, st);
+    if (pieces <= 32)
+        return launch_rows<T, O, COMBINE, 1, 1, 2>(a, st);
     if (waves <= 1)
         return launch_rows<T, O, COMBINE, 1, 1>(a, st);
     if (waves <= 2)
@@ -168,15 +190,19 @@ static hipError_t launch_width(const NormArgs &a, hipStream_t st)
         return launch_rows<T, O, COMBINE, 4, 1>(a, st);
     if (waves <= 8)
         return launch_rows<T, O, COMBINE, 8, 1>(a, st);
-    if (waves <= 16)
+    if (waves <= 16) {
+        if constexpr (!COMBINE)
+            if (a.M >= 1024)
+                return launch_rows<T, O, COMBINE, 8, 2>(a, st);
         return launch_rows<T, O, COMBINE, 16, 1>(a, st);
+    }
     if (waves <= 32)
         return launch_rows<T, O, COMBINE, 16, 2>(a, st);
     if (waves <= 64)
         return launch_rows<T, O, COMBINE, 16, 4>(a, st);
     if constexpr (kPiece<T> == 4)
         return launch_rows<T, O, COMBINE, 16, 8>(a, st);
-    return hipErrorInvalidValue;
+    return hipErrorInvalidValue;   // K <= Q4_NORM_MAX_K ends above
 }
 
 template <class T, RowForm O>

@@ -154,8 +154,9 @@ __device__ __forceinline__ float scale_of(float max, float c)
 
 // One piece of row `row` at column col, in the form O. Every lane of the
 // wavefront calls it; lanes that are not `in` (past the row's end) count for no
-// maximum and write nothing.
-template <RowForm O, int P>
+// maximum and write nothing. LANES neighbouring lanes hold a row, where several rows
+// share the wavefront (a block is no longer than its row).
+template <RowForm O, int LANES = 64, int P>
 __device__ __forceinline__ void put_piece(const RowOut &o, int K, const float (&v)[P], bool in, size_t row, int col)
 {
     const size_t at = row * (size_t)K + (size_t)col;
@@ -166,7 +167,7 @@ __device__ __forceinline__ void put_piece(const RowOut &o, int K, const float (&
         if (in)
             store_piece(static_cast<uint16_t *>(o.y) + at, v);
     } else if constexpr (O == RowForm::kE4M3) {
-        const float s = scale_of(lanes_max<128 / P>(in ? abs_max(v) : 0.0f), kE4M3Max);
+        const float s = scale_of(lanes_max<(128 / P < LANES ? 128 / P : LANES)>(in ? abs_max(v) : 0.0f), kE4M3Max);
         uint32_t w[P / 4];
         e4m3_codes(v, s, w);
         if (in) {

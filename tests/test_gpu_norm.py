@@ -100,9 +100,9 @@ def check_norm(M, K, share, bf16, residual, weighted, seed, eps=EPS, data=None):
     assert torch.equal(f8.view, want) and torch.equal(fs.view, ws), what
 
 
-# One wavefront a row and less, 2, 4, 8 and 16 of them, several pieces a lane;
-# short last blocks of 32 and 128; the widest row.
-WIDTHS = [32, 128, 160, 256, 288, 512, 544, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8224, 14336, 16416, 32768]
+# Four, two and one row a wavefront, 2, 4, 8 and 16 wavefronts a row, several
+# pieces a lane; short last blocks of 32 and 128; the widest row.
+WIDTHS = [32, 64, 96, 128, 160, 192, 256, 288, 512, 544, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8224, 14336, 16416, 32768]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -110,13 +110,17 @@ WIDTHS = [32, 128, 160, 256, 288, 512, 544, 1024, 1056, 2048, 2080, 4096, 4128, 
 def test_widths(K, bf16):
     check_norm(3, K, 1, bf16, True, False, K)
     check_norm(5, K, 2, bf16, True, True, K + 1)
+    if K <= 512:
+        check_norm(1 + 16 * 5, K, 1, bf16, False, False, K + 2)
+        check_norm(2 + 16 * 5, K, 3, bf16, True, True, K + 3)
 
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("M,K,share,residual,weighted", [
     (1, 4096, 1, True, False), (1, 4096, 8, True, True), (1, 256, 1, False, False), (6, 96, 3, False, True),
     (257, 512, 1, True, False), (1001, 160, 1, True, False), (130, 1056, 32, True, True), (7, 2048, 5, True, False),
-    (64, 4096, 1, False, True), (513, 256, 2, False, False), (2050, 2048, 1, True, False)])
+    (64, 4096, 1, False, True), (513, 256, 2, False, False), (2050, 2048, 1, True, False),
+    (1024, 2336, 1, True, False), (1030, 4128, 1, True, False)])
 def test_rows_and_shares(M, K, share, residual, weighted, bf16):
     check_norm(M, K, share, bf16, residual, weighted, 31 * M + K)
 
