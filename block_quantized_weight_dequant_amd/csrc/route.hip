@@ -1008,38 +1008,63 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
 {
     constexpr int W = NARROW ? 8 : 1;   // experts a thread
     __shared__ RouteLds<> l;
-    __shared__ int sums[2][W * kRouteThreads];
+    __shared__ __align__(16) int sums[2][W * kRouteThreads];
     const int tid = threadIdx.x, c0 = blockIdx.x * run;
+    const int s0 = c0 * chunk * top_k, n = ((int)min((long long)(c0 + run) * chunk, (long long)T) - c0 * chunk) * top_k;
+    const int mine = ids[s0 + min(tid, n - 1)];   // the first batch's, on its way meanwhile
     const int width = max(1, (1 << bits) / W), parts = kRouteThreads / width;   // threads a row of the table, rows at a time
     const int q = tid % width, p = tid / width;
     int all[W] = {}, before[W] = {};
-    if (q * W < E) {
-        const auto add = [&](int k, int i, int v) __attribute__((always_inline)) {
-            all[i] += v;
-            before[i] += k < c0 ? v : 0;
-        };
-#pragma unroll 8
-        for (int k = p; k < chunks; k += parts) {
-            if constexpr (NARROW) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(counts) +
-                                                                 (size_t)k * route_pitch(E) + q * 8);
+    const auto add_rows = [&](auto in_flight) __attribute__((always_inline)) {
+        constexpr int N = in_flight.value;
+        for (int k0 = p; k0 < chunks; k0 += N * parts) {
+            std::conditional_t<NARROW, u32x4, int> v[N];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    add(k, i, (int)(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xFFFFu));
-            } else {
-                add(k, 0, counts[(size_t)k * E + q]);
+            for (int j = 0; j < N; ++j) {
+                const size_t k = (size_t)min(k0 + j * parts, chunks - 1);
+                if constexpr (NARROW)
+                    v[j] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(counts) + k * route_pitch(E) + q * 8);
+                else
+                    v[j] = counts[k * (size_t)E + q];
+            }
+            asm volatile("" ::: "memory");   // all of them before the first is used
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int k = k0 + j * parts;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    int c;
+                    if constexpr (NARROW)
+                        c = (int)(i & 1 ? v[j][i / 2] >> 16 : v[j][i / 2] & 0xFFFFu);
+                    else
+                        c = v[j];
+                    all[i] += k < chunks ? c : 0;
+                    before[i] += k < c0 ? c : 0;   // c0 < chunks
+                }
             }
         }
+    };
+    if (q * W < E) {
+        if (chunks > 2 * parts)
+            add_rows(std::integral_constant<int, 8>{});
+        else
+            add_rows(std::integral_constant<int, 2>{});
     }
     // Part p's sums at p's row of `width` W experts.
+    if constexpr (NARROW) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        sums[0][tid * W + i] = all[i];
-        sums[1][tid * W + i] = before[i];
+        for (int i = 0; i < W; i += 4) {
+            reinterpret_cast<i32x4 *>(sums[0])[(tid * W + i) / 4] = (i32x4){all[i], all[i + 1], all[i + 2], all[i + 3]};
+            reinterpret_cast<i32x4 *>(sums[1])[(tid * W + i) / 4] = (i32x4){before[i], before[i + 1], before[i + 2], before[i + 3]};
+        }
+    } else {
+        sums[0][tid] = all[0];
+        sums[1][tid] = before[0];
     }
     __syncthreads();
     int total = 0, ahead = 0;
     if (tid < E)
+#pragma unroll 8
         for (int k = 0; k < parts; ++k) {
             total += sums[0][k * width * W + tid];
             ahead += sums[1][k * width * W + tid];
@@ -1051,8 +1076,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
         if (tid == 0)
             offsets[E] = T * top_k;
     }
-    const int s0 = c0 * chunk * top_k, n = ((int)min((long long)(c0 + run) * chunk, (long long)T) - c0 * chunk) * top_k;
-    place(l, [&](int i) { return ids[s0 + i]; }, s0, n, E, bits, first + ahead, order);
+    place(l, [&](int i) { return i < kRouteThreads ? mine : ids[s0 + i]; }, s0, n, E, bits, first + ahead, order);
 }
 
 static int expert_bits(int E)
