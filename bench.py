@@ -26,8 +26,8 @@ Q8_0-quantized activations; one GPU's share of an 8-way row split; and
 streaming-read ceilings of the same byte counts. Each row is written to stderr
 as one ``row: {json}`` line (and to ``--rows-out``); stdout ends with ONE
 compact JSON line. ``--rows experts`` measures the operators of an expert layer
-in place of those rows: the E4M3 quantizers and products, the router, and the
-products grouped by expert.
+in place of those rows: the E4M3 quantizers and products, the routers, the norms
+and gated activations, and the products grouped by expert.
 
 ``roofline.traffic`` comes from the committed counter summary
 profiles/traffic.json (rocprofv3 FETCH_SIZE / WRITE_SIZE, scaled by a copy of
@@ -617,6 +617,17 @@ EXPERT_ROWS = [
     ("f8_gemm_2048x14336x4096", "f8", dict(M=2048, N=14336, K=4096)),
     ("route_32_2of8", "route", dict(T=32, E=8, k=2)),
     ("route_8192_6of64", "route", dict(T=8192, E=64, k=6)),
+    ("route_groups_32_8of256", "route_groups", dict(T=32, E=256, k=8)),
+    ("route_groups_8192_8of256", "route_groups", dict(T=8192, E=256, k=8)),
+    ("q8_norm_1x4096", "norm", dict(M=1, K=4096, act="f32", form="q8")),
+    ("f8_norm_bf16_37x4096_of_2", "norm", dict(M=37, K=4096, act="bf16", form="f8", k=2)),
+    ("f8_norm_bf16_1001x4096", "norm", dict(M=1001, K=4096, act="bf16", form="f8")),
+    ("q4_norm_2048x4096_of_2", "norm", dict(M=2048, K=4096, act="f32", form="bf16", k=2)),
+    ("q4_norm_bf16_65536x128", "norm", dict(M=65536, K=128, act="bf16", form="bf16")),
+    ("f8_act_bf16_2x14336", "act", dict(M=2, K=14336, act="bf16", form="f8")),
+    ("q8_act_37x14336", "act", dict(M=37, K=14336, act="f32", form="q8")),
+    ("q4_act_1001x14336", "act", dict(M=1001, K=14336, act="f32", form="bf16")),
+    ("f8_act_bf16_4096x14336", "act", dict(M=4096, K=14336, act="bf16", form="f8")),
     ("q4_grouped_f32_1_2of8_4096x4096", "grouped", dict(fmt="q4_0", act="f32", T=1, E=8, k=2, N=4096, K=4096)),
     ("q4_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q4_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
     ("q8_grouped_bf16_37_2of8_14336x4096", "grouped", dict(fmt="q8_0", act="bf16", T=37, E=8, k=2, N=14336, K=4096)),
@@ -636,7 +647,7 @@ EXPERT_ROWS = [
 
 
 def bench_expert(torch, q4, name, kind, steps, warmup, reps, profile, M=0, N=0, K=0, rows=1, act="f32",
-                 fmt="f8", T=0, E=1, k=1):
+                 fmt="f8", T=0, E=1, k=1, form="f8"):
     """One operator of the expert layer on inputs drawn on the device, R sets of
     them in turn (cold). Bytes: each input read once, each output written once;
     of the experts' weights only those that have rows."""
@@ -677,6 +688,30 @@ def bench_expert(torch, q4, name, kind, steps, warmup, reps, profile, M=0, N=0, 
             f = q4.f8_gemv if M <= 8 else q4.f8_gemm
             return ((lambda: f(a, a_s, w, w_s, y, M, N, K)),
                     (M + N) * K + (a_s.numel() + w_s.numel()) * 4 + M * N * 2, 2 * M * N * K)
+        if kind in ("norm", "act"):
+            dtype, e = (torch.bfloat16, 2) if act == "bf16" else (torch.float32, 4)
+            tail = "_bf16" if act == "bf16" else ""
+            if form == "f8":
+                dst = [torch.empty(M, K, dtype=torch.uint8, **dev), torch.empty(M, kb, **dev)]
+            else:
+                dst = [torch.empty(M * K // 32 * 34, dtype=torch.uint8, **dev) if form == "q8"
+                       else torch.empty(M, K, dtype=torch.bfloat16 if form == "bf16" else torch.float32, **dev)]
+            written = sum(t.numel() * t.element_size() for t in dst)
+            f = getattr(q4, ("q4" if form in ("f32", "bf16") else form) + "_" + kind + tail)
+            if kind == "act":
+                x = normal(M, 2 * K).to(dtype)
+                return (lambda: f(x[:, :K], x[:, K:], *dst, M, K)), 2 * M * K * e + written, 0
+            x, r, h, gamma = normal(M * k, K).to(dtype), normal(M, K).to(dtype), torch.empty(M, K, dtype=dtype, **dev), normal(K)
+            w = torch.rand(M, k, generator=g, **dev) if k > 1 else None
+            return ((lambda: f(x, gamma, *dst, M, K, 1e-5, residual=r, sum=h, weights=w, share=k)),
+                    M * K * e * (k + 2) + K * 4 + written, 0)
+        if kind == "route_groups":
+            ints = [torch.empty(n, dtype=torch.int32, **dev) for n in (S, E + 1, S)]
+            w, logits, bias = torch.empty(S, **dev), normal(T, E), 0.1 * normal(E)
+            ws = torch.empty(max(q4.q4_route_workspace_bytes(T, E, k), 16), dtype=torch.uint8, **dev)
+            return ((lambda: q4.q4_route_groups(logits, bias, ints[0], w, ints[1], ints[2], T, E, k,
+                                                q4.Q4_SCORE_SIGMOID, 8, 4, 2, True, 2.5, workspace=ws)),
+                    T * E * 4 + S * 12 + (2 * E + 1) * 4, 0)
         call, offsets, order = routed()
         if kind == "route":
             return call, T * E * 4 + S * 12 + (E + 1) * 4, 0

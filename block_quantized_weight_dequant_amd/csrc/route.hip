@@ -1012,7 +1012,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
     const int tid = threadIdx.x, c0 = blockIdx.x * run;
     const int s0 = c0 * chunk * top_k, n = ((int)min((long long)(c0 + run) * chunk, (long long)T) - c0 * chunk) * top_k;
     const int mine = ids[s0 + min(tid, n - 1)];   // the first batch's, on its way meanwhile
-    const int width = max(1, (1 << bits) / W), parts = kRouteThreads / width;   // threads a row of the table, rows at a time
+    // Threads a row of the table, and rows at a time: few, since their sums are added
+    // up below one after another.
+    const int width = max(1, (1 << bits) / W);
+    const int parts = min(min(kRouteThreads / width, chunks > 128 ? 32 : 16), chunks);
     const int q = tid % width, p = tid / width;
     int all[W] = {}, before[W] = {};
     const auto add_rows = [&](auto in_flight) __attribute__((always_inline)) {
@@ -1044,7 +1047,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const int *__rest
             }
         }
     };
-    if (q * W < E) {
+    if (q * W < E && p < parts) {
         if (chunks > 2 * parts)
             add_rows(std::integral_constant<int, 8>{});
         else
