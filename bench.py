@@ -1104,7 +1104,7 @@ def _read_csv(directory, suffix):
 def _short_kernel(name):
     """'void q4k::k_gemv_stream<q4k::FmtQ4_0, 1, 8, 16, false, 0>(...)' ->
     'k_gemv_stream<FmtQ4_0, 1, 8, 16, false, 0>'."""
-    n = name.replace("(anonymous namespace)::", "").split("(")[0]
+    n = name.replace("(anonymous namespace)::", "").replace("(q4k::RowForm)", "form ").split("(")[0]
     return n.replace("void ", "").replace("q4k::", "").replace("q4probe::", "").strip()
 
 
