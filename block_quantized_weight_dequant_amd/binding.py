@@ -647,12 +647,12 @@ def q4_route_groups(logits, bias, ids, weights, offsets, order, T: int, E: int, 
         wsb = int(workspace_bytes)
     else:
         wsb = _nbytes(ws) if ws is not None and not isinstance(ws, int) else 0
-    slots = T * top_k
-    _check(lib.q4_route_groups(_array(logits, T * E, _F32), _array(bias, E, _F32), T, E, top_k, score,
-                               n_groups, top_groups, group_best, bool(renorm), scale,
-                               _array(ids, slots, _I32), _array(weights, slots, _F32),
-                               _array(offsets, E + 1, _I32), _array(order, slots, _I32), _addr(ws),
-                               wsb, _stream_for(stream, logits)), "q4_route_groups")
+    slots, dev = T * top_k, _device_of(logits)
+    _check(lib.q4_route_groups(_array(logits, T * E, _F32, dev), _array(bias, E, _F32, dev), T, E, top_k,
+                               score, n_groups, top_groups, group_best, bool(renorm), scale,
+                               _array(ids, slots, _I32, dev), _array(weights, slots, _F32, dev),
+                               _array(offsets, E + 1, _I32, dev), _array(order, slots, _I32, dev),
+                               _addr(ws), wsb, _stream_for(stream, dev)), "q4_route_groups")
 
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
@@ -661,59 +661,65 @@ _BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _array(x, n: int, dtypes) -> int:
-    """Address of a dense device tensor of n elements of one of ``dtypes`` (or of
-    None, or of a plain address): the kernels go by the sizes given beside it.
+def _device_of(x) -> int:
+    """Index of the device that a call's arrays are on: its first input's (-1 of a
+    host tensor, which _array then refuses)."""
+    return _current_device() if type(x) is int or x is None else x.get_device()
+
+
+def _array(x, n: int, dtypes, device: int) -> int:
+    """Address of a dense tensor of n elements of one of ``dtypes`` on ``device`` (or
+    of None, or of a plain address): the kernels go by the sizes given beside it.
     These checks cost 0.2 us a tensor."""
     if x is None:
         return 0
     if type(x) is int:
         return x
-    if x.is_cuda and x.dtype in dtypes and x.numel() == n and x.is_contiguous():
+    if x.get_device() == device >= 0 and x.dtype in dtypes and x.numel() == n and x.is_contiguous():
         return x.data_ptr()
-    raise ValueError("expected a dense device tensor of %d elements of %s, got %s" % (
-        n, " or ".join(map(str, dtypes)), _what(x)))
+    raise ValueError("expected a dense tensor of %d elements of %s on %s, got %s" % (
+        n, " or ".join(map(str, dtypes)), "a GPU" if device < 0 else "cuda:%d" % device, _what(x)))
 
 
 def _what(x) -> str:
     return "%s of %s on %s, strides %s" % (tuple(x.shape), x.dtype, x.device, x.stride())
 
 
-def _stream_for(stream, x) -> int:
-    """_stream, where the work is x's: without a ``stream`` its device has to be
+def _stream_for(stream, device: int) -> int:
+    """_stream, where the work is on ``device``: without a ``stream`` that has to be
     the current one, whose stream is taken."""
-    if stream is not None or type(x) is int:
+    if stream is not None:
         return _stream(stream)
-    device = x.get_device()
     if device != _current_device():
-        raise ValueError("the tensors are on %s, which is not the current device: make it current, or "
-                         "pass a stream" % x.device)
+        raise ValueError("the tensors are on cuda:%d, which is not the current device: make it current, "
+                         "or pass a stream" % device)
     return _current_stream(device)
 
 
-def _norm(entry, dtypes, x, gamma, M, K, eps, residual, sum, weights, share, tail, stream) -> None:
+def _norm(entry, dtypes, dev, x, gamma, M, K, eps, residual, sum, weights, share, out, stream) -> None:
+    """out: the arguments between eps and M."""
     n = M * K
     _check(getattr(lib, entry)(
-        _array(x, n * share, dtypes), _array(weights, M * share, _F32), share,
-        _array(residual, n, dtypes), _array(sum, n, dtypes), _array(gamma, K, _F32), eps, *tail, M, K,
-        _stream_for(stream, x)), entry)
+        _array(x, n * share, dtypes, dev), _array(weights, M * share, _F32, dev), share,
+        _array(residual, n, dtypes, dev), _array(sum, n, dtypes, dev), _array(gamma, K, _F32, dev), eps,
+        *out, M, K, _stream_for(stream, dev)), entry)
 
 
-def _values_out(y, n: int, y_bf16):
+def _values_out(y, n: int, y_bf16, dev):
     """Where f32 or bfloat16 values go, and which of the two: by y's type, or by
     ``y_bf16`` where y is an address."""
     bf16 = bool(y_bf16) if type(y) is int or y is None else y.dtype in _BF16
-    return _array(y, n, _BF16 if bf16 else _F32), bf16
+    return _array(y, n, _BF16 if bf16 else _F32, dev), bf16
 
 
-def _q8_out(out_q, M, K):
+def _q8_out(out_q, M, K, dev):
     n = M * (K // 32) * 34
-    return _array(out_q, n, _BYTES), n
+    return _array(out_q, n, _BYTES, dev), n
 
 
-def _f8_out(q, s, M, K):
+def _f8_out(q, s, M, K, dev):
     n, ns = M * K, M * -(-K // 128)
-    return _array(q, n, _BYTES), n, _array(s, ns, _F32), ns
+    return _array(q, n, _BYTES, dev), n, _array(s, ns, _F32, dev), ns
 
 
 def q4_norm(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
@@ -724,30 +730,34 @@ def q4_norm(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, we
     bfloat16, by y's type (of an address: ``y_bf16``). ``x`` [M * share, K],
     ``residual`` and ``sum`` [M, K] f32; ``weights`` [M, share] as q4_route writes
     them, a weight of 0 leaving its row out; ``gamma`` [K] f32."""
-    _norm("q4_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
-          _values_out(y, M * K, y_bf16), stream)
+    dev = _device_of(x)
+    _norm("q4_norm", _F32, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          _values_out(y, M * K, y_bf16, dev), stream)
 
 
 def q4_norm_bf16(x, gamma, y, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
                  share: int = 1, y_bf16=False, stream=None) -> None:
     """As q4_norm with ``x``, ``residual`` and ``sum`` in bfloat16."""
-    _norm("q4_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
-          _values_out(y, M * K, y_bf16), stream)
+    dev = _device_of(x)
+    _norm("q4_norm_bf16", _BF16, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          _values_out(y, M * K, y_bf16, dev), stream)
 
 
 def q8_norm(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
             share: int = 1, y=None, stream=None) -> None:
     """q4_norm with the result as Q8_0 blocks in the uint8 tensor ``out_q``, and in
     f32 in ``y`` as well where that is given."""
-    _norm("q8_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
-          (_array(y, M * K, _F32), *_q8_out(out_q, M, K)), stream)
+    dev = _device_of(x)
+    _norm("q8_norm", _F32, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _F32, dev), *_q8_out(out_q, M, K, dev)), stream)
 
 
 def q8_norm_bf16(x, gamma, out_q, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
                  share: int = 1, y=None, stream=None) -> None:
     """As q8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
-    _norm("q8_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
-          (_array(y, M * K, _BF16), *_q8_out(out_q, M, K)), stream)
+    dev = _device_of(x)
+    _norm("q8_norm_bf16", _BF16, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _BF16, dev), *_q8_out(out_q, M, K, dev)), stream)
 
 
 def f8_norm(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
@@ -755,35 +765,38 @@ def f8_norm(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None,
     """q4_norm with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
     columns, ``s`` [M, ceil(K / 128)], and in f32 in ``y`` as well where that is
     given."""
-    _norm("f8_norm", _F32, x, gamma, M, K, eps, residual, sum, weights, share,
-          (_array(y, M * K, _F32), *_f8_out(q, s, M, K)), stream)
+    dev = _device_of(x)
+    _norm("f8_norm", _F32, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _F32, dev), *_f8_out(q, s, M, K, dev)), stream)
 
 
 def f8_norm_bf16(x, gamma, q, s, M: int, K: int, eps: float, residual=None, sum=None, weights=None,
                  share: int = 1, y=None, stream=None) -> None:
     """As f8_norm with ``x``, ``residual``, ``sum`` and ``y`` in bfloat16."""
-    _norm("f8_norm_bf16", _BF16, x, gamma, M, K, eps, residual, sum, weights, share,
-          (_array(y, M * K, _BF16), *_f8_out(q, s, M, K)), stream)
+    dev = _device_of(x)
+    _norm("f8_norm_bf16", _BF16, dev, x, gamma, M, K, eps, residual, sum, weights, share,
+          (_array(y, M * K, _BF16, dev), *_f8_out(q, s, M, K, dev)), stream)
 
 
-def _half(x, M, K, dtypes) -> int:
+def _half(x, M, K, dtypes, device: int) -> int:
     """Address of an [M, K] view whose rows are dense."""
     if x is None:
         return 0
-    if x.is_cuda and x.dtype in dtypes and x.dim() == 2 and x.shape == (M, K) and x.stride(1) == 1:
+    if type(x) is int:
+        return x
+    if (x.get_device() == device >= 0 and x.dtype in dtypes and x.shape == (M, K) and x.stride(1) == 1):
         return x.data_ptr()
-    raise ValueError("expected an [%d, %d] device tensor of %s with dense rows, got %s" % (
-        M, K, " or ".join(map(str, dtypes)), _what(x)))
+    raise ValueError("expected an [%d, %d] tensor of %s with dense rows on %s, got %s" % (
+        M, K, " or ".join(map(str, dtypes)), "a GPU" if device < 0 else "cuda:%d" % device, _what(x)))
 
 
-def _act(entry, dtypes, gate, up, M, K, act, tail, ld, stream) -> None:
-    if type(gate) is int:
-        g, u, ld = gate, up, K if ld is None else ld
-    else:
-        g, u, ld = _half(gate, M, K, dtypes), _half(up, M, K, dtypes), gate.stride(0) if M > 1 else K
-        if up is not None and M > 1 and up.stride(0) != ld:
+def _act(entry, dtypes, dev, gate, up, M, K, act, out, ld, stream) -> None:
+    g, u = _half(gate, M, K, dtypes, dev), _half(up, M, K, dtypes, dev)
+    if ld is None:
+        ld = gate.stride(0) if M > 1 and type(gate) is not int else K
+        if M > 1 and up is not None and type(up) is not int and up.stride(0) != ld:
             raise ValueError("gate's and up's rows are at different distances: %s, %s" % (_what(gate), _what(up)))
-    _check(getattr(lib, entry)(g, u, ld, act, *tail, M, K, _stream_for(stream, gate)), entry)
+    _check(getattr(lib, entry)(g, u, ld, act, *out, M, K, _stream_for(stream, dev)), entry)
 
 
 def q4_act(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=False, ld=None, stream=None) -> None:
@@ -791,34 +804,40 @@ def q4_act(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=False, ld
     bfloat16 by y's type. ``gate`` and ``up`` are f32 [M, K] views with dense
     rows, the halves of one product's rows or two products' results (of
     addresses: ``ld`` elements a row); ``up`` may be None."""
-    _act("q4_act", _F32, gate, up, M, K, act, _values_out(y, M * K, y_bf16), ld, stream)
+    dev = _device_of(gate)
+    _act("q4_act", _F32, dev, gate, up, M, K, act, _values_out(y, M * K, y_bf16, dev), ld, stream)
 
 
 def q4_act_bf16(gate, up, y, M: int, K: int, act: int = Q4_ACT_SILU, y_bf16=False, ld=None,
                 stream=None) -> None:
     """As q4_act with ``gate`` and ``up`` in bfloat16."""
-    _act("q4_act_bf16", _BF16, gate, up, M, K, act, _values_out(y, M * K, y_bf16), ld, stream)
+    dev = _device_of(gate)
+    _act("q4_act_bf16", _BF16, dev, gate, up, M, K, act, _values_out(y, M * K, y_bf16, dev), ld, stream)
 
 
 def q8_act(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """q4_act with the result as Q8_0 blocks in the uint8 tensor ``out_q``."""
-    _act("q8_act", _F32, gate, up, M, K, act, _q8_out(out_q, M, K), ld, stream)
+    dev = _device_of(gate)
+    _act("q8_act", _F32, dev, gate, up, M, K, act, _q8_out(out_q, M, K, dev), ld, stream)
 
 
 def q8_act_bf16(gate, up, out_q, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """As q8_act with ``gate`` and ``up`` in bfloat16."""
-    _act("q8_act_bf16", _BF16, gate, up, M, K, act, _q8_out(out_q, M, K), ld, stream)
+    dev = _device_of(gate)
+    _act("q8_act_bf16", _BF16, dev, gate, up, M, K, act, _q8_out(out_q, M, K, dev), ld, stream)
 
 
 def f8_act(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """q4_act with the result as E4M3 codes ``q`` [M, K] and a scale for each 128
     columns, ``s`` [M, ceil(K / 128)]."""
-    _act("f8_act", _F32, gate, up, M, K, act, _f8_out(q, s, M, K), ld, stream)
+    dev = _device_of(gate)
+    _act("f8_act", _F32, dev, gate, up, M, K, act, _f8_out(q, s, M, K, dev), ld, stream)
 
 
 def f8_act_bf16(gate, up, q, s, M: int, K: int, act: int = Q4_ACT_SILU, ld=None, stream=None) -> None:
     """As f8_act with ``gate`` and ``up`` in bfloat16."""
-    _act("f8_act_bf16", _BF16, gate, up, M, K, act, _f8_out(q, s, M, K), ld, stream)
+    dev = _device_of(gate)
+    _act("f8_act_bf16", _BF16, dev, gate, up, M, K, act, _f8_out(q, s, M, K, dev), ld, stream)
 
 
 def raw_status(entry: str, *args) -> int:

@@ -141,10 +141,20 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
             sq += part[slot][k];
     }
     const double ms = fma(sq, inv_k, (double)a.eps);
-    const float rstd = ms > 0.0 ? (float)rsqrt_f64(ms) : 0.0f;
+    // Rows below 2^-125, whose 1 / rms leaves f32 (eps is 0 or as small), are scaled
+    // up first.
+    const bool tiny = ms < 0x1p-250;
+    const float rstd = ms > 0.0 ? (float)(rsqrt_f64(ms) * (tiny ? 0x1p-64 : 1.0)) : 0.0f;
     if constexpr (!kEarly)
         put_sum();
 
+    if (__builtin_expect(tiny, 0)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                h[i][k] *= 0x1p64f;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll

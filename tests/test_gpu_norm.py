@@ -136,6 +136,11 @@ def test_scales_of_the_data(bf16):
     gamma[3] = 0
     for eps in (0.0, 1e-30, 1e-6):
         check_norm(M, K, 1, bf16, False, False, 0, eps=eps, data=(bf16_bits(x) if bf16 else x, None, None, gamma))
+    # Below 2^-125, where 1 / rms is past f32, down to the smallest f32.
+    x = np.ldexp(g.normal(0, 1, (25, 96)), -125 - np.arange(25)[:, None]).astype(np.float32)
+    x[24] = 0
+    x[24, 5] = 2.0 ** -133 if bf16 else 2.0 ** -149
+    check_norm(25, 96, 1, bf16, False, False, 0, eps=0.0, data=(bf16_bits(x) if bf16 else x, None, None, gamma[:96]))
     big = np.full((2, 64), 1.5e38, dtype=np.float32)
     check_norm(2, 64, 1, bf16, False, False, 0, data=(bf16_bits(big) if bf16 else big, None, None, gamma[:64]))
 

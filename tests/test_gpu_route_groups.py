@@ -93,6 +93,7 @@ def test_masks(sigmoid):
     x[5, 8:] = -np.inf                   # one group
     x[6, ::8] = np.nan
     b[[9, 17, 63]] = -np.inf
+    b[30] = np.nan
     for G, top, best in [(1, 1, 1), (8, 3, 2), (8, 3, 1), (8, 8, 1)]:
         for renorm in (True, False):
             check(x, b, 6, sigmoid, G, top, best, renorm)
