@@ -1,12 +1,13 @@
 // The gated activation between two products: y = f(gate) up, f SiLU or GELU (tanh
 // form), y in the form the next product reads (rows_out.h).
 //
-// Bound by bytes, with some 25 operations an element close behind. A wavefront
-// takes 64 pieces of one row (C wavefronts of a workgroup side by side, 4 / C
-// rows), so that its loads and stores are whole lines and a block's maximum stays
-// within it; two or four times the pieces a lane take 9 % longer (4096 x 14336
-// bfloat16 to E4M3: 50.2 us, 5.9 TB/s, 1001 x 14336 f32 to bfloat16 24.8 us, 5.8
-// TB/s; plain streams of the same bytes take 47.6 and 24.1).
+// Bound by bytes, with some 25 operations an element close behind. A lane takes one
+// 16-byte piece (two or four take 9 % longer), and the lanes of a block of the
+// output go to the blocks of all rows in turn, so that no lane idles at the end of
+// a row and a block's maximum stays within its lanes. With whole wavefronts, or
+// workgroups, in one row instead, 4096 x 2816 bfloat16 to E4M3 takes 13.4 us, or
+// 16.9, for 12.0. 4096 x 14336 bfloat16 to E4M3: 49.5 us, 6.0 TB/s; 1001 x 14336 f32
+// to bfloat16 24.8 us, 5.8 TB/s; plain streams of the same bytes take 47.6 and 24.1.
 //
 // f(g) = g / (1 + exp(-z)), z = g for SiLU and 2 sqrt(2 / pi) (g + 0.044715 g^3)
 // for GELU (where (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))): one exponential and one
@@ -32,17 +33,24 @@ __device__ __forceinline__ float gate_value(float g)
     return fmaf(fmaf(-d, q, g), r, q);
 }
 
-template <class T, RowForm O, int ACT, int C>
-__global__ __launch_bounds__(256) void k_act(ActArgs a, int first)
+// Columns of a block of the output; K is a multiple of 32.
+template <RowForm O>
+constexpr int kActBlock = O == RowForm::kE4M3 ? 128 : 32;
+
+// Block i of a launch lies in row first + i / blocks; the quotient is i times mul,
+// 2^shift / blocks rounded up, shifted: exact for i < 2^31, as mul is too large by
+// less than 1 and 2^shift >= 2^31 blocks.
+template <class T, RowForm O, int ACT>
+__global__ __launch_bounds__(256) void k_act(ActArgs a, uint32_t blocks, uint32_t mul, int shift, int first)
 {
-    constexpr int P = kPiece<T>, ROWS = 4 / C;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const long long row = ((long long)first + blockIdx.y) * ROWS + wave / C;
+    constexpr int P = kPiece<T>, LANES = kActBlock<O> / P;
+    const uint32_t i = blockIdx.x * (256u / LANES) + threadIdx.x / LANES, r = (uint32_t)(((uint64_t)i * mul) >> shift);
+    const long long row = (long long)first + r;
     if (row >= a.M)
         return;
     const T *gate = static_cast<const T *>(a.gate) + (size_t)row * (size_t)a.ld;
     const T *up = a.up ? static_cast<const T *>(a.up) + (size_t)row * (size_t)a.ld : gate;
-    const int c = (int)((blockIdx.x * C + wave % C) * 64 + lane) * P;   // K <= 2^22
+    const int c = (int)((i - r * blocks) * LANES + threadIdx.x % LANES) * P;   // K <= 2^22
     const bool in = c < a.K;
     const int col = in ? c : 0;
     float g[P], u[P];
@@ -62,19 +70,21 @@ __global__ __launch_bounds__(256) void k_act(ActArgs a, int first)
 template <class T, RowForm O, int ACT>
 static hipError_t launch_f(const ActArgs &a, hipStream_t st)
 {
-    // Columns fastest: the workgroups in flight read rows from end to end (rows
-    // fastest takes 4 to 10 % longer). At most 2^15 workgroups of rows a launch.
-    const int waves = (a.K / kPiece<T> + 63) / 64;
-    const auto go = [&](auto kernel, int c) {
-        const int rows = 4 / c, cols = (waves + c - 1) / c;
-        const long long groups = ((long long)a.M + rows - 1) / rows, part = 1 << 15;
-        hipError_t e = hipSuccess;
-        for (long long first = 0; first < groups && e == hipSuccess; first += part)
-            e = launch_kernel(kernel, dim3((unsigned)cols, (unsigned)(groups - first < part ? groups - first : part)),
-                              dim3(256), 0, st, a, (int)first);
-        return e;
-    };
-    return waves <= 1 ? go(k_act<T, O, ACT, 1>, 1) : waves <= 2 ? go(k_act<T, O, ACT, 2>, 2) : go(k_act<T, O, ACT, 4>, 4);
+    constexpr int LANES = kActBlock<O> / kPiece<T>;
+    const int blocks = (a.K + kActBlock<O> - 1) / kActBlock<O>;
+    int shift = 31;
+    while ((1ll << (shift - 31)) < blocks)
+        ++shift;
+    const uint32_t mul = (uint32_t)(((1ull << shift) + (uint64_t)blocks - 1) / (uint64_t)blocks);
+    // At most 2^28 lanes a launch, 256 rows of the longest.
+    const long long part = (1 << 28) / (blocks * LANES);
+    hipError_t e = hipSuccess;
+    for (long long first = 0; first < a.M && e == hipSuccess; first += part) {
+        const long long rows = a.M - first < part ? a.M - first : part;
+        e = launch_kernel(k_act<T, O, ACT>, dim3((unsigned)((rows * blocks * LANES + 255) / 256)), dim3(256), 0, st, a,
+                          (uint32_t)blocks, mul, shift, (int)first);
+    }
+    return e;
 }
 
 template <class T, RowForm O>

@@ -152,8 +152,8 @@ __device__ __forceinline__ float scale_of(float max, float c)
     return fmaf(fmaf(-q, c, max), r, q);
 }
 
-// One piece of row `row` at column col, in the form O. Every lane of the
-// wavefront calls it; lanes that are not `in` (past the row's end) count for no
+// One piece of row `row` at column col, in the form O. Every lane of a
+// block calls it; lanes that are not `in` (past the row's end) count for no
 // maximum and write nothing. LANES neighbouring lanes hold a row, where several rows
 // share the wavefront (a block is no longer than its row).
 template <RowForm O, int LANES = 64, int P>

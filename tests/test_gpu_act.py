@@ -152,3 +152,26 @@ def test_binding_refuses():
     q4.q4_act(x[:0, :K], x[:0, K:], y[:0], 0, K)     # empty
     torch.cuda.synchronize()
     assert not y.any()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_every_number_of_blocks(bf16):
+    # Rows end at every place of a wavefront and of a workgroup.
+    for b in range(1, 41):
+        gate, up = make(2 + b % 7, 32 * b, bf16, b)
+        check_act(gate, up, False)
+
+
+def test_rows_past_a_launch():
+    # 2^28 pieces are 2^24 rows of 128 columns; the rows next to the boundary and
+    # the last ones are what calls of their own give.
+    M, K = 2 ** 24 + 9, 128
+    both = torch.empty(M, 2 * K, dtype=torch.bfloat16, device=DEV).normal_()
+    q, s = torch.zeros(M, K, dtype=torch.uint8, device=DEV), torch.zeros(M, device=DEV)
+    q4.f8_act_bf16(both[:, :K], both[:, K:], q, s, M, K)
+    for first, n in ((0, 5), (2 ** 24 - 7, 16), (2 ** 23, 64)):
+        want, ws = torch.empty(n, K, dtype=torch.uint8, device=DEV), torch.empty(n, device=DEV)
+        rows = both[first:first + n]
+        q4.f8_act_bf16(rows[:, :K], rows[:, K:], want, ws, n, K)
+        assert torch.equal(q[first:first + n], want) and torch.equal(s[first:first + n], ws), first
+    assert bool((s > 0).all())
