@@ -176,9 +176,13 @@ static hipError_t launch_rows(const NormArgs &a, hipStream_t st)
 
 // As many wavefronts a row as take it in one piece a lane: the shortest way for few
 // rows, and for many (1001 x 4096 bfloat16 to E4M3 7.6 us with 8 wavefronts a row,
-// 8.3 with 4 of two pieces). From 9 to 16 of them the workgroups get so large that
-// two are on a compute unit at a time; many rows of those take two pieces a lane
-// in 8 wavefronts, unless experts' rows are added (us, 16 x 1 and 8 x 2; f32):
+// 8.3 with 4 of two pieces). The widths with 5, 10 and 12 wavefronts beside the
+// powers of two leave fewer lanes idle (us, with the next power of two and with
+// them): 512 x 2560 bfloat16 to E4M3 4.5 4.2, 512 x 5120 6.7 6.2, 900 x 10240 of 2 to
+// Q8_0 27.8 22.4, 512 x 12288 12.2 11.6; at worst 1024 x 5120 f32 of 2 21.4 22.5.
+// From 9 to 16 of them the workgroups get so large that two are on a compute unit
+// at a time; many rows of those take two pieces a lane in 5 or 8 wavefronts, unless
+// experts' rows are added (us, 16 x 1 and 8 x 2; f32):
 //                              M = 512     1024        2048
 //   4096 to f32                7.2  7.0  14.1 13.1   25.6 23.9
 //   4096 to Q8_0               6.7  7.5  12.7 12.0   22.7 21.2
@@ -198,14 +202,22 @@ static hipError_t launch_width(const NormArgs &a, hipStream_t st)
         return launch_rows<T, O, COMBINE, 2, 1>(a, st);
     if (waves <= 4)
         return launch_rows<T, O, COMBINE, 4, 1>(a, st);
+    if (waves <= 5)
+        return launch_rows<T, O, COMBINE, 5, 1>(a, st);
     if (waves <= 8)
         return launch_rows<T, O, COMBINE, 8, 1>(a, st);
     if (waves <= 16) {
         if constexpr (!COMBINE)
             if (a.M >= 1024)
-                return launch_rows<T, O, COMBINE, 8, 2>(a, st);
-        return launch_rows<T, O, COMBINE, 16, 1>(a, st);
+                return waves <= 10 ? launch_rows<T, O, COMBINE, 5, 2>(a, st) : launch_rows<T, O, COMBINE, 8, 2>(a, st);
+        return waves <= 10   ? launch_rows<T, O, COMBINE, 10, 1>(a, st)
+               : waves <= 12 ? launch_rows<T, O, COMBINE, 12, 1>(a, st)
+                             : launch_rows<T, O, COMBINE, 16, 1>(a, st);
     }
+    if (waves <= 20)
+        return launch_rows<T, O, COMBINE, 10, 2>(a, st);
+    if (waves <= 24)
+        return launch_rows<T, O, COMBINE, 12, 2>(a, st);
     if (waves <= 32)
         return launch_rows<T, O, COMBINE, 16, 2>(a, st);
     if (waves <= 64)

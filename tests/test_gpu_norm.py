@@ -126,6 +126,21 @@ def test_rows_and_shares(M, K, share, residual, weighted, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("waves", [3, 5, 7, 9, 10, 11, 12, 13, 17, 20, 21, 24, 25])
+def test_every_number_of_wavefronts(waves, bf16):
+    # A row that ends near the last wavefront's end, and the narrowest.
+    lanes = 512 if bf16 else 256
+    for K in (waves * lanes - 32, (waves - 1) * lanes + 32):
+        check_norm(3, K, 1, bf16, True, False, K)
+        check_norm(2, K, 3, bf16, True, True, K + 1)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_rows_of_nine_wavefronts(bf16):
+    check_norm(1025, (512 if bf16 else 256) * 9 - 32, 1, bf16, True, False, 77)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 def test_scales_of_the_data(bf16):
     # Rows of sizes from 2^-60 to 2^60, whose squares leave f32; rows of zeros.
     g = np.random.default_rng(5)
