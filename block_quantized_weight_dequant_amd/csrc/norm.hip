@@ -20,6 +20,8 @@
 #include "launch.h"
 #include "rows_out.h"
 
+#include <type_traits>
+
 namespace q4k {
 
 // SUB rows share a wavefront (then RW and V are 1): rows of up to 64 / SUB pieces,
@@ -49,35 +51,65 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
         in[i] = c < a.K;
         col[i] = in[i] ? c : 0;
     }
-    if constexpr (COMBINE) {
-        // Row j + 1 is fetched while row j is added; the residual is added last.
-        float r[V][P], next[V][P];
+    // gamma is fetched after the rows, or before them where their sum is a loop and the
+    // registers allow it.
+    const auto get_gamma = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            load_piece(x + col[i], next[i]);
+#pragma unroll
+            for (int q = 0; q < P / 4; ++q) {
+                const f32x4 g = *reinterpret_cast<const f32x4 *>(a.gamma + col[i] + 4 * q);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    gamma[i][4 * q + k] = g[k];
+            }
+    };
+    constexpr bool kGammaFirst = COMBINE && V == 1;
+    if constexpr (kGammaFirst)
+        get_gamma();
+    if constexpr (COMBINE) {
+        float r[V][P];
 #pragma unroll
         for (int i = 0; i < V; ++i)
             load_piece(res + col[i], r[i]);
         const float *weights = a.weights ? a.weights + row * (size_t)a.share : nullptr;
         double acc[V][P] = {};
-        for (int j = 0; j < a.share; ++j) {
-            const float wj = weights ? weights[j] : 1.0f;
-            float v[V][P];
+        // Rows j to j + N - 1.
+        const auto add = [&](auto count, int j) __attribute__((always_inline)) {
+            constexpr int N = decltype(count)::value;
+            float v[N][V][P], w[N];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int k = 0; k < P; ++k)
-                    v[i][k] = next[i][k];
-            const T *xn = x + (size_t)min(j + 1, a.share - 1) * (size_t)a.K;
+                for (int i = 0; i < V; ++i)
+                    load_piece(x + (size_t)(j + n) * (size_t)a.K + col[i], v[n][i]);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                load_piece(xn + col[i], next[i]);
+            for (int n = 0; n < N; ++n)
+                w[n] = weights ? weights[j + n] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int k = 0; k < P; ++k)
-                    acc[i][k] = fma((double)wj, (double)(wj == 0.0f ? 0.0f : v[i][k]), acc[i][k]);
-        }
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        acc[i][k] = fma((double)w[n], (double)(w[n] == 0.0f ? 0.0f : v[n][i][k]), acc[i][k]);
+        };
+        // N rows are in flight together, as many as leave the registers to two workgroups
+        // or more. Against one row fetched ahead of the one that is added (us, to E4M3):
+        // 976 x 512 bfloat16 of 8 4.8, 7.4; 3906 x 2048 f32 of 2 23.1, 25.1; 558 x 7168
+        // bfloat16 of 4 13.8, 15.2; at worst 279 x 7168 of 8 13.9, 12.3.
+        constexpr int N = V == 1 ? (P == 4 ? 8 : RW < 10 ? 4 : 2) : V == 2 ? 2 : 1;
+        int j = 0;
+        for (; j + N <= a.share; j += N)
+            add(std::integral_constant<int, N>{}, j);
+        if constexpr (N > 4)
+            for (; j + 4 <= a.share; j += 4)
+                add(std::integral_constant<int, 4>{}, j);
+        if constexpr (N > 2)
+            for (; j + 2 <= a.share; j += 2)
+                add(std::integral_constant<int, 2>{}, j);
+        for (; j < a.share; ++j)
+            add(std::integral_constant<int, 1>{}, j);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -96,15 +128,8 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
             for (int k = 0; k < P; ++k)
                 h[i][k] = a.residual ? h[i][k] + r[i][k] : h[i][k];
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int q = 0; q < P / 4; ++q) {
-            const f32x4 g = *reinterpret_cast<const f32x4 *>(a.gamma + col[i] + 4 * q);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                gamma[i][4 * q + k] = g[k];
-        }
+    if constexpr (!kGammaFirst)
+        get_gamma();
 
     // Rows of bfloat16 in one piece a lane write h before they are reduced (1001 x
     // 4096 to E4M3 7.9 us, 8.2 after), the others after (512 x 4096 f32 to Q8_0 6.6
