@@ -14,7 +14,7 @@
 // one row of some 10^7. f32 sums instead are 1 to 4 % faster on every size measured.
 //
 // Measured, with cold rows: 2048 x 4096, two experts' f32 rows and a residual to
-// bfloat16, 27.0 us, 5.6 TB/s (a plain stream of the same bytes 25.9); 1001 x 4096
+// bfloat16, 25.8 us, 5.9 TB/s (a plain stream of the same bytes 25.9); 1001 x 4096
 // bfloat16 to E4M3 7.6 us (5.4); one row 3.0 us (2.2).
 #include "f64.h"
 #include "launch.h"
@@ -207,12 +207,13 @@ static hipError_t launch_rows(const NormArgs &a, hipStream_t st)
 // Q8_0 27.8 22.4, 512 x 12288 12.2 11.6; at worst 1024 x 5120 f32 of 2 21.4 22.5.
 // From 9 to 16 of them the workgroups get so large that two are on a compute unit
 // at a time; many rows of those take two pieces a lane in 5 or 8 wavefronts, unless
-// experts' rows are added (us, 16 x 1 and 8 x 2; f32):
+// experts' rows of bfloat16 are added (1116 x 7168 of 2 to E4M3 16.9, 17.7 us)
+// (us, 16 x 1 and 8 x 2; f32):
 //                              M = 512     1024        2048
 //   4096 to f32                7.2  7.0  14.1 13.1   25.6 23.9
 //   4096 to Q8_0               6.7  7.5  12.7 12.0   22.7 21.2
 //   4096 to E4M3               7.1  7.3  12.9 11.8   22.6 20.9
-//   4096 to bfloat16, of 2                           27.0 29.1
+//   4096 to bfloat16, of 2                           26.9 25.8
 template <class T, RowForm O, bool COMBINE>
 static hipError_t launch_width(const NormArgs &a, hipStream_t st)
 {
@@ -232,7 +233,7 @@ static hipError_t launch_width(const NormArgs &a, hipStream_t st)
     if (waves <= 8)
         return launch_rows<T, O, COMBINE, 8, 1>(a, st);
     if (waves <= 16) {
-        if constexpr (!COMBINE)
+        if constexpr (!COMBINE || kPiece<T> == 4)
             if (a.M >= 1024)
                 return waves <= 10 ? launch_rows<T, O, COMBINE, 5, 2>(a, st) : launch_rows<T, O, COMBINE, 8, 2>(a, st);
         return waves <= 10   ? launch_rows<T, O, COMBINE, 10, 1>(a, st)
