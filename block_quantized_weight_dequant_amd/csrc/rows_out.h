@@ -4,10 +4,10 @@
 // columns).
 //
 // A lane holds P consecutive elements of a row, 16 bytes of input (P = 4 of f32,
-// 8 of bfloat16), and consecutive lanes hold consecutive pieces, the first lane
-// of a wavefront a piece whose column is a multiple of 128: a Q8_0 block is 32 / P
-// neighbouring lanes, a block of 128 columns 128 / P, and no block leaves its
-// wavefront or straddles the DPP rows that its maximum crosses.
+// 8 of bfloat16), and a block's lanes its pieces in order: a Q8_0 block is 32 / P
+// neighbouring lanes, a block of 128 columns 128 / P, the first of them at a multiple
+// of their number, so that no block leaves its wavefront or straddles the DPP rows
+// that its maximum crosses.
 #pragma once
 
 #include "device_common.h"
