@@ -793,9 +793,11 @@ def _half(x, M, K, dtypes, device: int) -> int:
 def _act(entry, dtypes, dev, gate, up, M, K, act, out, ld, stream) -> None:
     g, u = _half(gate, M, K, dtypes, dev), _half(up, M, K, dtypes, dev)
     if ld is None:
-        ld = gate.stride(0) if M > 1 and type(gate) is not int else K
-        if M > 1 and up is not None and type(up) is not int and up.stride(0) != ld:
-            raise ValueError("gate's and up's rows are at different distances: %s, %s" % (_what(gate), _what(up)))
+        ld = K if M <= 1 or gate is None or type(gate) is int else gate.stride(0)
+    if M > 1:
+        for x in (gate, up):
+            if x is not None and type(x) is not int and x.stride(0) != ld:
+                raise ValueError("expected rows %d elements apart, got %s" % (ld, _what(x)))
     _check(getattr(lib, entry)(g, u, ld, act, *out, M, K, _stream_for(stream, dev)), entry)
 
 

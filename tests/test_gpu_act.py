@@ -175,3 +175,22 @@ def test_rows_past_a_launch():
         q4.f8_act_bf16(rows[:, :K], rows[:, K:], want, ws, n, K)
         assert torch.equal(q[first:first + n], want) and torch.equal(s[first:first + n], ws), first
     assert bool((s > 0).all())
+
+
+def test_binding_holds_tensors_to_their_strides():
+    M, K = 4, 64
+    x, y = torch.ones(M, 2 * K, device=DEV), torch.zeros(M, K, device=DEV)
+    g, u = x[:, :K], x[:, K:]
+    for a, b, ld in [(g, u, 3 * K), (g, None, K), (g.data_ptr(), u, K), (g, u.contiguous(), None)]:
+        with pytest.raises(ValueError):
+            q4.q4_act(a, b, y, M, K, ld=ld)
+    with pytest.raises(q4.Q4Error) as e:
+        q4.q4_act(None, None, y, M, K)
+    assert e.value.status == q4.Q4_ERR_NULL
+    torch.cuda.synchronize()
+    assert not y.any()
+    q4.q4_act(g, u, y, M, K, ld=2 * K)
+    z = torch.zeros(M, K, device=DEV)
+    q4.q4_act(g.data_ptr(), u.data_ptr(), z, M, K, ld=2 * K)
+    q4.q4_act(g[:1], u[:1], y[:1], 1, K, ld=7 * K)   # one row: its distance counts for nothing
+    assert torch.equal(y, z) and bool((y > 0).all())
