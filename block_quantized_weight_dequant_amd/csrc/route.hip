@@ -540,7 +540,7 @@ __device__ __forceinline__ double row_sum(double v)
     return v + dpp_f64<0x140>(v);
 }
 
-// Falling order, by Batcher's merge exchange (63 exchanges of 16).
+// Falling order, by Batcher's merge exchange (63 exchanges of 16, 191 of 32).
 template <int N>
 __device__ __forceinline__ void sort_falling(uint32_t (&v)[N])
 {
@@ -561,7 +561,7 @@ __device__ __forceinline__ void sort_falling(uint32_t (&v)[N])
 
 // The value itself, which the compiler then computes where it stands: sunk under the
 // condition of a later choice, each score would be a chain of dependent operations by
-// itself instead of one among sixteen.
+// itself instead of one among many.
 template <class K>
 __device__ __forceinline__ K at_once(K v)
 {
@@ -590,7 +590,14 @@ struct RowExperts {
     K unit, margin;    // groups' sums up to `margin` apart may be in either order
     uint32_t blur;
 };
-constexpr uint32_t kMostSteps = (1u << 24) - 1024, kMaskedCode = 1;
+// A code's low bits: the lane (4) and the place in it.
+template <int CAP>
+constexpr int kPlaceBits = CAP <= 16 ? 4 : 5;
+template <int CAP>
+constexpr int kTagBits = 4 + kPlaceBits<CAP>;
+template <int CAP>
+constexpr uint32_t kMostSteps = (1u << (32 - kTagBits<CAP>)) - 1024;
+constexpr uint32_t kMaskedCode = 1;
 
 // CAP floats from byte `at` on, zeros past the buffer: whole 16-byte loads at any
 // 4-byte alignment, without a branch, so that all stay in flight together.
@@ -642,7 +649,7 @@ __device__ __forceinline__ void scale_row_experts(RowExperts<CAP, K> &x)
     }
     hi = row_max(hi);
     lo = row_max(-lo);
-    const float range = 1.0f + (hi + lo), unit = (float)kMostSteps * 0.999999f * __builtin_amdgcn_rcpf(range);
+    const float range = 1.0f + (hi + lo), unit = (float)kMostSteps<CAP> * 0.999999f * __builtin_amdgcn_rcpf(range);
     x.unit = (K)unit;
     if constexpr (sizeof(K) == 4) {
         const float err = 0x1p-20f + 0x1p-22f * (1.0f + larger(hi, lo));
@@ -659,20 +666,24 @@ __device__ __forceinline__ void scale_row_experts(RowExperts<CAP, K> &x)
 // LDS of a wavefront of rows: the tokens' logits by lane and place (a lane's at a
 // pitch that spreads them over the banks), and the keys of a token that is chosen
 // exactly.
-constexpr int kRowThreads = 512, kRowWaves = kRowThreads / 64, kRowExperts = 256, kRowTopK = 15;
+constexpr int kRowThreads = 512, kRowWaves = kRowThreads / 64, kRowTopK = 15;
+template <int CAP>
+constexpr int kRowExperts = CAP <= 16 ? 256 : 512;
+template <int CAP>
 struct RowLds {
-    float logits[64 * 17];
+    static constexpr int kPitch = kRowExperts<CAP> / 16 + 1;
+    float logits[64 * kPitch];
     union {
-        double vals[kRowExperts];
-        uint64_t keys[kRowExperts];
+        double vals[kRowExperts<CAP>];
+        uint64_t keys[kRowExperts<CAP>];
     };
 };
 
 // One token by the whole wavefront, with keys in f64: into l.vals, masked ones
 // -inf; returns the groups that can be chosen (bits as best_groups').
-template <bool GROUPED, bool SIGMOID>
+template <bool GROUPED, bool SIGMOID, class Lds>
 __device__ __forceinline__ uint64_t exact_keys(const float *__restrict__ row, const RouteGroups &g, int lanes,
-                                               RowLds &l, int E)
+                                               Lds &l, int E)
 {
     const int lane = threadIdx.x & 63;
     const float ninf = -__builtin_inff();
@@ -701,9 +712,9 @@ __device__ __forceinline__ uint64_t exact_keys(const float *__restrict__ row, co
 
 // One token's choices by the whole wavefront, the lowest expert among equals.
 // Small and slow: hardly a token needs it.
-template <bool GROUPED, bool SIGMOID>
+template <bool GROUPED, bool SIGMOID, class Lds>
 __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, const RouteGroups &g, int lanes,
-                                               RowLds &l, int E, int top_k, uint16_t *out)
+                                               Lds &l, int E, int top_k, uint16_t *out)
 {
     const int lane = threadIdx.x & 63, size = E / g.n_groups;
     const uint64_t kept = exact_keys<GROUPED, SIGMOID>(row, g, lanes, l, E);
@@ -739,9 +750,9 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
 // ids and weights.
 //
 // A key (s + bias: sigmoid scores in f32 here, softmax scores in f64) becomes a
-// code of 24 bits, its distance from the row's largest in steps of the range that
-// keys can have, with the expert's lane and its place in the lane in the eight bits
-// below, so that equal codes are in the order of their experts. A lane sorts its
+// code of 24 bits (23 with 17 to 32 experts a lane), its distance from the row's
+// largest in steps of the range that keys can have, with the expert's lane and its
+// place in the lane in the bits below, so that equal codes are in the order of their experts. A lane sorts its
 // codes once, and a step of the selection is a maximum over the row's heads (four DPP
 // moves) for four tokens at a time, and one head taken off. Codes near enough to be
 // in the wrong order are taken along, and ordered by f64 keys, which the weights need
@@ -749,7 +760,7 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
 // the token is chosen again, exactly.
 template <int CAP, bool GROUPED, bool SIGMOID, class K>
 __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__restrict__ logits, const RouteGroups &g,
-                                            const RouteRows &r, const RowExperts<CAP, K> &x, RowLds &l, int lanes,
+                                            const RouteRows &r, const RowExperts<CAP, K> &x, RowLds<CAP> &l, int lanes,
                                             int E, int top_k, int *__restrict__ ids, float *__restrict__ weights,
                                             int tok, bool in, uint16_t *out)
 {
@@ -758,7 +769,7 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
     const K none = -(K)__builtin_inf();
 #pragma unroll
     for (int i = 0; i < CAP; ++i)
-        l.logits[lane * 17 + i] = v[i];
+        l.logits[lane * l.kPitch + i] = v[i];
     double top = 0.0, share = 1.0;
     K key[CAP];
     if constexpr (SIGMOID) {
@@ -832,12 +843,13 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
         }
     }
     const K most = row_max(open ? mine : none);
+    constexpr int PLACE = kPlaceBits<CAP>, PLACES = (1 << PLACE) - 1, TAG = kTagBits<CAP>;
     uint32_t code[CAP];
 #pragma unroll
     for (int i = 0; i < CAP; ++i) {
-        const K far = smaller(larger((most - key[i]) * x.unit, (K)0), (K)kMostSteps);
-        const uint32_t steps = key[i] > none ? 0x00FFFFFFu - (uint32_t)far : kMaskedCode;
-        code[i] = open & (i < x.n) ? steps << 8 | (uint32_t)((15 - p) << 4 | (15 - i)) : 0u;
+        const K far = smaller(larger((most - key[i]) * x.unit, (K)0), (K)kMostSteps<CAP>);
+        const uint32_t steps = key[i] > none ? (1u << (32 - TAG)) - 1u - (uint32_t)far : kMaskedCode;
+        code[i] = open & (i < x.n) ? steps << TAG | (uint32_t)((15 - p) << PLACE | (PLACES - i)) : 0u;
     }
     sort_falling(code);
     // Codes are taken until what is left is certain to be smaller than the top_k-th. A
@@ -865,7 +877,7 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
 #pragma unroll 1
     for (int j = top_k; j < 16; ++j) {
         best = row_max(code[0]);
-        more = ((last >> 8) - (best >> 8) <= x.blur) & (best >> 8 > kMaskedCode);
+        more = ((last >> TAG) - (best >> TAG) <= x.blur) & (best >> TAG > kMaskedCode);
         if (!__ballot(more))
             break;
         take(j);
@@ -873,14 +885,14 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
     const bool doubt = more | ((CAP > LIST) & (offered >= LIST) & (x.n > LIST));
 
     // Lane p: candidate p, its score in f64.
-    const int from = (lane & 48) + 15 - (int)(taken >> 4 & 15u), at = 15 - (int)(taken & 15u);
+    const int from = (lane & 48) + 15 - (int)(taken >> PLACE & 15u), at = PLACES - (int)(taken & (uint32_t)PLACES);
     int id = __shfl(x.e0, from) + at;
-    float logit = l.logits[from * 17 + (at < CAP ? at : 0)];
-    bool masked = taken >> 8 <= kMaskedCode;
+    float logit = l.logits[from * l.kPitch + (at < CAP ? at : 0)];
+    bool masked = taken >> TAG <= kMaskedCode;
     double s = at_once(score_of<SIGMOID>(logit, top, share));
     s = masked ? 0.0 : s;
     const uint32_t next = dpp_u32<0x101>(taken);   // row_shl 1: the lane after
-    const bool near = (next >> 8 > kMaskedCode) & ((taken >> 8) - (next >> 8) <= x.blur);
+    const bool near = (next >> TAG > kMaskedCode) & ((taken >> TAG) - (next >> TAG) <= x.blur);
     if (__ballot(near)) {
         // Some neighbours may be in the wrong order: by their f64 keys, then, the lowest
         // expert among equals.
@@ -927,7 +939,9 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
     }
 }
 
-// Up to 256 experts in rows of lanes, four tokens a wavefront at a time.
+// Up to 512 experts in rows of lanes, CAP or fewer a lane, four tokens a wavefront at
+// a time: 32 / 2048 / 8192 tokens of 512 experts in 8 groups 12.9 / 19.9 / 24.0 us
+// (48.3 / 55.5 / 79.6 with a wavefront a token); 32 / 8192 of 256 8.8 / 16.4.
 template <int CAP, bool GROUPED, bool SIGMOID>
 __global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restrict__ logits, RouteGroups g,
                                                            RouteRows r, int lanes, int *__restrict__ ids,
@@ -936,8 +950,8 @@ __global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restr
                                                            int E, int top_k, int chunk, int bits)
 {
     using K = std::conditional_t<SIGMOID, float, double>;
-    __shared__ RouteLds<1, kRowThreads, kRowExperts> l;
-    __shared__ RowLds rows[kRowWaves];
+    __shared__ RouteLds<1, kRowThreads, kRowExperts<CAP>> l;
+    __shared__ RowLds<CAP> rows[kRowWaves];
     __shared__ uint16_t s_ids[kOneChunk * kRowTopK];   // the choices of a chunk that is alone, or of a pass
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, T);
@@ -1127,7 +1141,7 @@ template <bool GROUPED, bool SIGMOID>
 static auto rows_kernel(int per)
 {
     return per <= 4 ? k_route_rows<4, GROUPED, SIGMOID> : per <= 8 ? k_route_rows<8, GROUPED, SIGMOID>
-                                                                   : k_route_rows<16, GROUPED, SIGMOID>;
+         : per <= 16 ? k_route_rows<16, GROUPED, SIGMOID> : k_route_rows<32, GROUPED, SIGMOID>;
 }
 
 hipError_t launch_route_groups(const float *logits, const RouteGroups &g, int *ids, float *weights,
@@ -1140,14 +1154,14 @@ hipError_t launch_route_groups(const float *logits, const RouteGroups &g, int *i
     int lanes = 6;
     while (g.n_groups << lanes > 64)
         --lanes;
-    // Rows of 16 lanes hold up to 16 groups, 16 experts a lane, and 15 choices with the one after them.
+    // Rows of 16 lanes hold up to 16 groups, 32 experts a lane, and 15 choices with the one after them.
     RouteRows r = {grouped ? g.n_groups : 1, 4, 0, 0};
     while (r.groups << r.lanes > 16 && r.lanes > 0)
         --r.lanes;
     r.size = E / r.groups;
     r.per = (r.size + (1 << r.lanes) - 1) >> r.lanes;
     hipError_t e;
-    if (r.groups <= 16 && r.per <= 16 && top_k <= kRowTopK) {
+    if (r.groups <= 16 && r.per <= 32 && top_k <= kRowTopK) {
         auto kernel = grouped ? (g.sigmoid ? rows_kernel<true, true>(r.per) : rows_kernel<true, false>(r.per))
                               : (g.sigmoid ? rows_kernel<false, true>(r.per) : rows_kernel<false, false>(r.per));
         e = launch_kernel(kernel, dim3((unsigned)chunks), dim3(kRowThreads), 0, st, logits, g, r, lanes, ids, weights,

@@ -197,3 +197,34 @@ def test_binding_refuses():
     with pytest.raises(q4.Q4Error) as e:
         q4.q4_route_groups(*ok, T, E, k, q4.Q4_SCORE_SIGMOID, 3, 1)
     assert e.value.status == q4.Q4_ERR_SHAPE
+
+
+WIDE = [(512, 1, 1), (512, 8, 4), (320, 8, 3), (272, 16, 4), (257, 1, 1), (510, 15, 5), (320, 10, 2)]   # 17 to 32 experts a lane
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("E,G,top", WIDE)
+def test_wide_rows(E, G, top, sigmoid):
+    for T, k in ((1, 1), (33, 8), (66, 15), (300, 6)):
+        x, b = make(T, E, T + E)
+        check(x, b, k, sigmoid, G, top, 2, True, 2.5)
+        check(x, None, k, sigmoid, G, top, 1, False, 1.0)
+    test_equal_keys(E, G, top, sigmoid)
+    g = np.random.default_rng(E)
+    x, b = make(67, E, 77)
+    x[g.random((67, E)) < 0.9] = -np.inf
+    x[3] = -np.inf
+    x[4, 1:] = -np.inf
+    x[6, ::8] = np.nan
+    b[[9, 17, 63, E - 1]] = -np.inf
+    b[30] = np.nan
+    check(x, b, 8, sigmoid, G, top, 2)
+    check(x, None, 15, sigmoid, G, G, 1)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,G,top", WIDE)
+def test_wide_rows_of_near_keys(E, G, top, biased):
+    test_keys_an_f32_step_apart(E, G, top, biased)
+    if not biased:
+        test_the_best_are_neighbours(E, G, top)
