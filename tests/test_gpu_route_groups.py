@@ -228,3 +228,14 @@ def test_wide_rows_of_near_keys(E, G, top, biased):
     test_keys_an_f32_step_apart(E, G, top, biased)
     if not biased:
         test_the_best_are_neighbours(E, G, top)
+
+
+@pytest.mark.parametrize("size", [3.0, 50.0, 1e4, 1e7])
+def test_wide_rows_with_large_biases(size):
+    x, _ = make(70, 512, 12)
+    g = np.random.default_rng(5)
+    for b in (np.full(512, size, dtype=np.float32), (size * g.normal(0, 1, 512)).astype(np.float32),
+              np.where(np.arange(512) % 3, size, -size).astype(np.float32)):
+        check(x, b, 8, True, 8, 4, 2)
+        check(x, b, 15, True, 1, 1, 1)
+        check(x, b, 8, False, 8, 4, 1, False, -1.5)
