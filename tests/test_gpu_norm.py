@@ -190,6 +190,19 @@ def test_weight_zero_leaves_its_row_out(bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("K,share", [(64, 9), (1024, 7), (2528, 5), (4096, 3), (5120, 11), (8192, 6), (11616, 13), (32768, 2)])
+def test_weight_zero_at_every_width(K, share, bf16):
+    M = 2 * share + 1
+    x, res, w, gamma = make(M, K, share, bf16, True, True, K)
+    for m in range(M):                               # each slot alone, then all but it; the last row: none left
+        w[m, m % share if m < share else np.arange(share) != m % share] = 0
+    w[-1] = -0.0
+    rows = x.reshape(M, share, K)
+    rows[w == 0] = 0x7FC0 if bf16 else np.nan
+    check_norm(M, K, share, bf16, True, True, 0, data=(x, res, w, gamma))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("share", [1, 4])
 def test_sum_in_place(share, bf16):
     M, K = 33, 4128
