@@ -12,8 +12,9 @@
 // f(g) = g / (1 + exp(-z)), z = g for SiLU and 2 sqrt(2 / pi) (g + 0.044715 g^3)
 // for GELU (where (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))): one exponential and one
 // reciprocal, both from the hardware's f32 instructions (1 unit in the last
-// place, four times the time of another). The quotient takes its remainder once,
-// so that it is as good as a division.
+// place, four times the time of another). The reciprocal takes its remainder once
+// and is then within a little more than half a unit; it and not the quotient does,
+// whose remainder is NaN where g is infinite.
 #include "launch.h"
 #include "rows_out.h"
 
@@ -23,14 +24,14 @@ template <int ACT>
 __device__ __forceinline__ float gate_value(float g)
 {
     // Below these gates f is nearer to 0 than 2^-119 and counts as f there, so that
-    // the exponential stays finite.
-    g = __builtin_amdgcn_fmed3f(g, ACT == Q4_ACT_GELU ? -9.98f : -87.0f, 3.4028235e38f);
+    // the exponential stays finite. The maximum keeps NaN.
+    g = __builtin_elementwise_maximum(g, ACT == Q4_ACT_GELU ? -9.98f : -87.0f);
     constexpr double kLog2e = 1.4426950408889634, kTwice = 1.5957691216057308;   // 2 sqrt(2 / pi)
     const float hi = ACT == Q4_ACT_GELU ? g * fmaf(g * g, (float)(-kTwice * 0.044715 * kLog2e), (float)(-kTwice * kLog2e))
                                         : g * (float)-kLog2e;   // -z log2 e
     const float d = 1.0f + __builtin_amdgcn_exp2f(hi);
-    const float r = __builtin_amdgcn_rcpf(d), q = g * r;
-    return fmaf(fmaf(-d, q, g), r, q);
+    const float r = __builtin_amdgcn_rcpf(d);
+    return g * fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
 // Columns of a block of the output; K is a multiple of 32.

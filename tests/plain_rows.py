@@ -62,7 +62,7 @@ def act_tolerance(gate, up, gelu, bf16):
     exponent z log2 e is a product with a rounded constant, off by 1.25 u of itself
     (the constant log2 e is off by 2^-26.2) for SiLU and by 4 u for GELU (g^2, the
     constants, the sum, the product), so exp(-z) by |z| times that (z = g, or 2 u);
-    the exponential by 2 u, 1 + e by u, the quotient by u and a little, the product
+    the exponential by 2 u, 1 + e by u, the quotient by 2 u and a little, the product
     with up by u. 2^-20 is 16 u, |g| 2^-23 twice and |u| 2^-20 twice the shares of z."""
     y = np.abs(act(gate, up, gelu))
     g = widen(gate)

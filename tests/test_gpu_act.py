@@ -194,3 +194,40 @@ def test_binding_holds_tensors_to_their_strides():
     q4.q4_act(g.data_ptr(), u.data_ptr(), z, M, K, ld=2 * K)
     q4.q4_act(g[:1], u[:1], y[:1], 1, K, ld=7 * K)   # one row: its distance counts for nothing
     assert torch.equal(y, z) and bool((y > 0).all())
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_what_is_not_finite_is_passed_on(bf16, gelu):
+    # NaN stays NaN, an infinite gate gives f's limit (inf, or 0 within 2^-119); the
+    # elements beside them are what they are without.
+    M, K = 6, 96
+    gate, up = make(M, K, bf16, 17)
+    val = lambda v: bf16_bits(np.float32(v)) if bf16 else np.float32(v)
+    nan, inf, ninf = (0x7FC0, 0x7F80, 0xFF80) if bf16 else (np.nan, np.inf, -np.inf)
+    bad_g, bad_u = gate.copy(), up.copy()
+    bad_g[0, 3], bad_g[1, ::2], bad_u[2, 95], bad_u[3] = nan, nan, nan, nan
+    bad_g[4, 5], bad_u[4, 5] = inf, val(2.5)
+    bad_g[4, 6], bad_u[4, 6] = inf, val(-2.5)
+    bad_g[4, 7], bad_u[4, 7] = inf, val(0)
+    bad_g[4, 8], bad_u[4, 8] = ninf, val(2.5)
+    bad_g[4, 9], bad_u[4, 9] = val(1.5), ninf
+    y, want = torch.empty(M, K, device=DEV), torch.empty(M, K, device=DEV)
+    y16 = torch.empty(M, K, dtype=torch.bfloat16, device=DEV)
+    one = torch.empty(M, K, device=DEV)
+    fn, act = q4.Q4_ACT_GELU if gelu else q4.Q4_ACT_SILU, q4.q4_act_bf16 if bf16 else q4.q4_act
+    act(dev_of(gate), dev_of(up), want, M, K, fn)
+    for out in (y, y16):
+        act(dev_of(bad_g), dev_of(bad_u), out, M, K, fn)
+    act(dev_of(bad_g), None, one, M, K, fn)
+    y, y16, want, one = (t.float().cpu().numpy() for t in (y, y16, want, one))
+    gone = np.zeros((M, K), dtype=bool)
+    gone[0, 3] = gone[1, ::2] = gone[2, 95] = gone[3] = gone[4, 7] = True
+    for got in (y, y16):
+        assert np.array_equal(np.isnan(got), gone)
+        assert got[4, 5] == np.inf and got[4, 6] == -np.inf and got[4, 9] == -np.inf and abs(got[4, 8]) <= 2.5 * 2.0 ** -119
+    same = ~gone
+    same[4, 5:10] = False
+    assert np.array_equal(y[same], want[same])
+    gate_nan = np.isnan(plain.widen(bad_g))
+    assert np.array_equal(np.isnan(one), gate_nan) and (one[4, 5:8] == np.inf).all() and abs(one[4, 8]) <= 2.0 ** -119
