@@ -106,10 +106,12 @@ __global__ __launch_bounds__(256) void k_quantize_q8_0(const float *__restrict__
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const unsigned blk = bl + 32 * r;
-        float am = fmaxf(fmaxf(fabsf(v[r].x), fabsf(v[r].y)), fmaxf(fabsf(v[r].z), fabsf(v[r].w)));
-        am = fmaxf(am, dpp_xor1(am));
-        am = fmaxf(am, dpp_xor2(am));
-        am = fmaxf(am, dpp_mirror8(am));
+        // A maximum that keeps NaN: codes have none, so one in the block is the scale's.
+        const auto larger = [](float a, float b) __attribute__((always_inline)) { return __builtin_elementwise_maximum(a, b); };
+        float am = larger(larger(fabsf(v[r].x), fabsf(v[r].y)), larger(fabsf(v[r].z), fabsf(v[r].w)));
+        am = larger(am, dpp_xor1(am));
+        am = larger(am, dpp_xor2(am));
+        am = larger(am, dpp_mirror8(am));
 
         const float d = am / 127.0f;
         int q0 = 0, q1 = 0, q2 = 0, q3 = 0;

@@ -80,7 +80,7 @@ __device__ __forceinline__ void store_piece(uint16_t *p, const float (&v)[P])
 // sign: the quotient takes x's. Four operations an element; a division takes
 // about twelve. Other scales divide; s == 0 gives 0. clamp: to +-limit there (in
 // the range above the quotient is at most a rounding past it, which the codes
-// absorb).
+// absorb). NaN stays NaN under every scale.
 template <int P>
 __device__ __forceinline__ void quotients(const float (&x)[P], float s, bool clamp, float limit, float (&q)[P])
 {
@@ -95,7 +95,8 @@ __device__ __forceinline__ void quotients(const float (&x)[P], float s, bool cla
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const float v = x[i] / s;
-            q[i] = s == 0.0f ? 0.0f : clamp ? fminf(fmaxf(v, -limit), limit) : v;
+            q[i] = s == 0.0f ? fabsf(x[i]) * 0.0f
+                   : clamp ? __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -limit), limit) : v;
         }
     }
 }
@@ -114,30 +115,46 @@ __device__ __forceinline__ void e4m3_codes(const float (&x)[P], float s, uint32_
     }
 }
 
-template <int P>
+// The larger of two; of NaN and a number the number, or NaN (NAN_WINS).
+template <bool NAN_WINS>
+__device__ __forceinline__ float larger_of(float a, float b)
+{
+    if constexpr (NAN_WINS)
+        return __builtin_elementwise_maximum(a, b);
+    else
+        return fmaxf(a, b);
+}
+
+template <bool NAN_WINS = false, int P>
 __device__ __forceinline__ float abs_max(const float (&v)[P])
 {
     float m = fabsf(v[0]);
 #pragma unroll
     for (int i = 1; i < P; ++i)
-        m = fmaxf(m, fabsf(v[i]));
+        m = larger_of<NAN_WINS>(m, fabsf(v[i]));
     return m;
 }
 
+template <bool NAN_WINS, int CTRL>
+__device__ __forceinline__ float dpp_max(float v)
+{
+    return larger_of<NAN_WINS>(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false)));
+}
+
 // Largest over each L neighbouring lanes (4, 8, 16 or 32), in every one of them.
-template <int L>
+template <int L, bool NAN_WINS = false>
 __device__ __forceinline__ float lanes_max(float v)
 {
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));        // quad_perm 1,0,3,2
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));        // quad_perm 2,3,0,1
+    v = dpp_max<NAN_WINS, 0xB1>(v);        // quad_perm 1,0,3,2
+    v = dpp_max<NAN_WINS, 0x4E>(v);        // quad_perm 2,3,0,1
     if constexpr (L >= 8)
-        v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));   // row_half_mirror
+        v = dpp_max<NAN_WINS, 0x141>(v);   // row_half_mirror
     if constexpr (L >= 16)
-        v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));   // row_mirror
+        v = dpp_max<NAN_WINS, 0x140>(v);   // row_mirror
     if constexpr (L >= 32) {
         // Rows of 16 lanes 0 and 1, and 2 and 3, change places.
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        v = larger_of<NAN_WINS>(__uint_as_float(r[0]), __uint_as_float(r[1]));
     }
     return v;
 }
@@ -180,8 +197,9 @@ __device__ __forceinline__ void put_piece(const RowOut &o, int K, const float (&
                 o.s[row * (size_t)(((unsigned)K + 127) / 128) + (size_t)((unsigned)col >> 7)] = s;
         }
     } else {
-        // Q8_0: a block's 34 bytes are 2-byte aligned, and so are these stores.
-        const float d = scale_of(lanes_max<32 / P>(in ? abs_max(v) : 0.0f), 127.0f);
+        // Q8_0: a block's 34 bytes are 2-byte aligned, and so are these stores. Its codes
+        // have no NaN, so one in the block is the scale's.
+        const float d = scale_of(lanes_max<32 / P, true>(in ? abs_max<true>(v) : 0.0f), 127.0f);
         float q[P];
         quotients(v, d, false, 0.0f, q);
         uint32_t w[P / 4];

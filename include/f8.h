@@ -45,7 +45,8 @@ extern "C" {
  * f32 and clamped to [-448, 448] (the scale is rounded, so the largest quotient
  * can be a step of f32 past 448; farther only for a subnormal scale). -0 and
  * negative quotients that round to zero are 0x80. A block whose scale is 0
- * stores codes 0. Bit-exact.
+ * stores codes 0. Bit-exact. NaN elements get a NaN code (0x7F or 0xFF), the scale
+ * comes from the others; a block with an infinity has the scale inf.
  */
 int f8_quantize(const float *x, int M, int K, int block_rows, void *q, size_t q_bytes, float *s,
                 size_t s_elems, void *stream);

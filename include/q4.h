@@ -577,7 +577,8 @@ size_t q8_gemm_grouped_bf16_workspace_bytes(int G, int M, int N, int K);
  * nearest even) is stored little-endian, then 32 bytes q = round(x / d) in
  * two's complement, with round() half away from zero, the quotient formed from
  * the f32 d, and q = 0 (d = +0) for an all-zero block. Bit-exact and
- * deterministic.
+ * deterministic. A block with a NaN has a NaN d, one with an infinity an infinite
+ * d; their codes are unspecified.
  */
 int q8_quantize(const float *x, size_t n_elems, void *out_q, size_t out_bytes, void *stream);
 
