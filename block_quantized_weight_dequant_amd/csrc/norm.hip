@@ -177,7 +177,10 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
     // Rows below 2^-125, whose 1 / rms leaves f32 (eps is 0 or as small), are scaled
     // up first.
     const bool tiny = ms < 0x1p-250;
-    const float rstd = ms > 0.0 ? (float)(rsqrt_f64(ms) * (tiny ? 0x1p-64 : 1.0)) : 0.0f;
+    // 0 of a row of zeros and of one with an infinity, NaN of one with a NaN.
+    const float rstd = ms > 0.0 && ms < __builtin_inf() ? (float)(rsqrt_f64(ms) * (tiny ? 0x1p-64 : 1.0))
+                       : ms != ms                       ? __builtin_nanf("")
+                                                        : 0.0f;
     if constexpr (!kEarly)
         put_sum();
 

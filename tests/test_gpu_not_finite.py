@@ -113,3 +113,43 @@ def test_activations(bf16, gelu):
             vals.append((q8_values(blob, M, K), v))
         check(vals[0][0], vals[1][0], nan, inf, 32, False)
         check(vals[0][1], vals[1][1], nan, inf, 128, True)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("K,share", [(32, 1), (96, 3), (416, 1), (1056, 2), (4096, 1), (5120, 2), (11616, 1), (32768, 1)])
+def test_norms(K, share, bf16):
+    # Rows 1: a NaN in x; 2: in the residual; 3, 4: an infinity; 5: both signs of it in
+    # one sum. The rows beside them are what they are without.
+    M, tail = 7, "_bf16" if bf16 else ""
+    g = np.random.default_rng(K)
+    x, res = g.normal(0, 1, (M * share, K)).astype(np.float32), g.normal(0, 1, (M, K)).astype(np.float32)
+    w = g.uniform(0.5, 1, (M, share)).astype(np.float32)
+    bad_x, bad_r = x.copy(), res.copy()
+    at = K - 2
+    bad_x[1 * share, 3], bad_r[2, at] = np.nan, np.nan
+    bad_x[4 * share - 1, 5], bad_r[4, at] = np.inf, -np.inf
+    bad_x[5 * share, at], bad_r[5, at] = np.inf, -np.inf
+    outs = []
+    for xv, rv in ((bad_x, bad_r), (x, res)):
+        sm = torch.empty(M, K, dtype=torch.bfloat16 if bf16 else torch.float32, device=DEV)
+        y, y16 = torch.empty(M, K, device=DEV), torch.empty(M, K, dtype=torch.bfloat16, device=DEV)
+        blob = torch.empty(M * (K // 32) * 34, dtype=torch.uint8, device=DEV)
+        q, s = torch.empty(M * K, dtype=torch.uint8, device=DEV), torch.empty(M * -(-K // 128), device=DEV)
+        args, kw = (dev_of(xv, bf16), torch.ones(K, device=DEV)), dict(residual=dev_of(rv, bf16), weights=to_dev(w) if share > 1 else None, share=share)
+        getattr(q4, "q4_norm" + tail)(*args, y, M, K, 1e-5, sum=sm, **kw)
+        getattr(q4, "q4_norm" + tail)(*args, y16, M, K, 1e-5, **kw)
+        getattr(q4, "q8_norm" + tail)(*args, blob, M, K, 1e-5, **kw)
+        getattr(q4, "f8_norm" + tail)(*args, q, s, M, K, 1e-5, **kw)
+        outs.append([t.float().cpu().numpy().astype(np.float64) for t in (sm, y, y16)] + [q8_values(blob, M, K), f8_values(q, s, M, K)])
+    rest, other = [0, 6], np.arange(K)
+    for got, clean in zip(*outs):
+        assert np.array_equal(got[rest], clean[rest])
+    sm, y, y16, v8, vf = outs[0]
+    for v in (y, y16, v8, vf):
+        assert np.isnan(v[[1, 2, 5]]).all()
+        assert np.isnan(v[3, 5]) and np.isnan(v[4, at])
+    for v in (y, y16, vf):
+        assert (v[3, other != 5] == 0).all() and (v[4, other != at] == 0).all()
+    assert np.isnan(sm[1, 3]) and np.isnan(sm[2, at]) and sm[3, 5] == np.inf and sm[4, at] == -np.inf and np.isnan(sm[5, at])
+    for m, c in ((1, 3), (2, at), (3, 5), (4, at), (5, at)):
+        assert np.isfinite(sm[m, other != c]).all()
