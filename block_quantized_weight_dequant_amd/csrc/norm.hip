@@ -175,21 +175,21 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
     }
     const double ms = fma(sq, inv_k, (double)a.eps);
     // Rows below 2^-125, whose 1 / rms leaves f32 (eps is 0 or as small), are scaled
-    // up first.
-    const bool tiny = ms < 0x1p-250;
+    // up first, and those above 2^125, where it would lose bits below 2^-126, down.
+    const bool tiny = ms < 0x1p-250, huge = ms > 0x1p250;
     // 0 of a row of zeros and of one with an infinity, NaN of one with a NaN.
-    const float rstd = ms > 0.0 && ms < __builtin_inf() ? (float)(rsqrt_f64(ms) * (tiny ? 0x1p-64 : 1.0))
+    const float rstd = ms > 0.0 && ms < __builtin_inf() ? (float)(rsqrt_f64(ms) * (tiny ? 0x1p-64 : huge ? 0x1p64 : 1.0))
                        : ms != ms                       ? __builtin_nanf("")
                                                         : 0.0f;
     if constexpr (!kEarly)
         put_sum();
 
-    if (__builtin_expect(tiny, 0)) {
+    if (__builtin_expect(tiny || huge, 0)) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int k = 0; k < P; ++k)
-                h[i][k] *= 0x1p64f;
+                h[i][k] *= tiny ? 0x1p64f : 0x1p-64f;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {

@@ -618,7 +618,8 @@ int q4_quantize(const float *x, size_t n_elems, void *out_q, size_t out_bytes, v
  * rounded to f32 once; the mean of its squares and rstd are f64, rstd rounded to
  * f32 once; y = (h rstd) gamma is two f32 products, then rounded to bfloat16 if
  * asked. So |y - exact| <= 2^-21.6 |exact| (and 2^-8 |y| more in bfloat16) + 2^-126
- * where h does not cancel (h itself is within half a step). Deterministic.
+ * + |gamma| 2^-149 where h does not cancel (h itself is within half a step).
+ * Deterministic.
  * A NaN in a row of h makes its whole row of y NaN, an infinity gives NaN in its
  * own place and 0 in the others.
  * Errors in the order shape, size, empty (M == 0), NULL, alignment, overlap.

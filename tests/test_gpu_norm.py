@@ -271,3 +271,31 @@ def test_binding_refuses():
     q4.q4_norm(torch.zeros(0, K, device=DEV), gamma, torch.zeros(0, K, device=DEV), 0, K, EPS)   # empty
     torch.cuda.synchronize()
     assert not y.any()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("K", [96, 1056, 4096])
+def test_largest_rows(K, bf16):
+    # Up to the largest f32, where 1 / rms is below 2^-126: no bits are lost to that. The
+    # row in between, and its smallest elements, keep theirs too.
+    M = 48
+    g = np.random.default_rng(K)
+    x = (g.uniform(0.3, 1, (M, K)) * g.choice([-1, 1], (M, K)) * np.exp2(g.uniform(124, 127.95, (M, 1)))).astype(np.float32)
+    x[5] = np.float32(3.38e38)
+    x[6, ::3] = np.float32(2.0 ** -120)
+    x[7] = g.normal(0, 1, K).astype(np.float32)
+    gamma = (1 + 0.1 * g.normal(0, 1, K)).astype(np.float32)
+    check_norm(M, K, 1, bf16, False, False, 0, data=(bf16_bits(x) if bf16 else x, None, None, gamma))
+
+
+def test_large_gamma_on_small_elements():
+    # h rstd below 2^-126 is off by 2^-150 at most, and gamma times that.
+    M, K = 3, 128
+    g = np.random.default_rng(3)
+    x = g.normal(0, 1, (M, K)).astype(np.float32)
+    x[:, ::2] = np.ldexp(g.uniform(0.5, 1, (M, K // 2)), g.integers(-148, -120, (M, K // 2))).astype(np.float32)
+    gamma = np.where(np.arange(K) % 2, 1.0, g.uniform(0.5, 1, K) * 2.0 ** 100).astype(np.float32)
+    y = torch.empty(M, K, device=DEV)
+    q4.q4_norm(to_dev(x), to_dev(gamma), y, M, K, EPS)
+    ref = plain.norm(x.astype(np.float64), gamma, float(np.float32(EPS)))
+    assert (np.abs(host(y) - ref) <= 2.0 ** -21.6 * np.abs(ref) + 2.0 ** -126 + np.abs(gamma.astype(np.float64)) * 2.0 ** -149).all()
