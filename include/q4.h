@@ -664,10 +664,10 @@ int q8_norm_bf16(const uint16_t *x, const float *weights, int share, const uint1
  *             nothing between the first and the last element of gate or of up.
  *   M >= 0, K a positive multiple of 32, K <= 2^22 (else Q4_ERR_SHAPE).
  * Numerics, in f32: |y - exact| <= (2^-20 + |g| 2^-23) |exact| (GELU: (2^-20 + |u|
- * 2^-20) |exact|) + |up| 2^-119 + 2^-149, and 2^-8 |y| more in bfloat16. (The exponent
- * of the exponential is rounded to f32; where g is negative and large, f is small
- * and loses bits to that.) Deterministic. NaN and infinities are passed on: f(NaN) =
- * NaN, f(inf) = inf, f(-inf) = -0 as far as 2^-119.
+ * 2^-20) |exact|) + |up| 2^-119 + 2^-149, and 2^-8 |y| + 2^-134 more in bfloat16.
+ * (The exponent of the exponential is rounded to f32; where g is negative and large,
+ * f is small and loses bits to that.) Deterministic. NaN and infinities are passed
+ * on: f(NaN) = NaN, f(inf) = inf, f(-inf) = -0 as far as 2^-119.
  */
 int q4_act(const float *gate, const float *up, int ld, int act, void *y, int y_bf16, int M, int K,
            void *stream);

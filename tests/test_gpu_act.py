@@ -231,3 +231,28 @@ def test_what_is_not_finite_is_passed_on(bf16, gelu):
     assert np.array_equal(y[same], want[same])
     gate_nan = np.isnan(plain.widen(bad_g))
     assert np.array_equal(np.isnan(one), gate_nan) and (one[4, 5:8] == np.inf).all() and abs(one[4, 8]) <= 2.0 ** -119
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_the_stated_bound_of_small_results(bf16, gelu):
+    # Results around and below bfloat16's smallest normal value, 2^-126, where a
+    # rounding is off by half of its smallest step, 2^-134; the bound written out as in
+    # include/q4.h.
+    g = np.random.default_rng(12)
+    M, K = 40, 128
+    gate = (np.exp2(g.uniform(-75, -62, (M, K))) * g.choice([-1, 1], (M, K))).astype(np.float32)
+    up = (np.exp2(g.uniform(-64, -58, (M, K))) * g.choice([-1, 1], (M, K))).astype(np.float32)
+    if bf16:
+        gate, up = bf16_bits(gate), bf16_bits(up)
+    gv, uv = plain.widen(gate), plain.widen(up)
+    ref, z = plain.act(gate, up, gelu), np.abs(plain.gelu_u(gv)) * 2.0 ** -20 if gelu else np.abs(gv) * 2.0 ** -23
+    tol = (2.0 ** -20 + z) * np.abs(ref) + np.abs(uv) * 2.0 ** -119 + 2.0 ** -149
+    act, fn = q4.q4_act_bf16 if bf16 else q4.q4_act, q4.Q4_ACT_GELU if gelu else q4.Q4_ACT_SILU
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.empty(M, K, dtype=dtype, device=DEV)
+        act(dev_of(gate), dev_of(up), y, M, K, fn)
+        got = y.float().cpu().numpy().astype(np.float64)
+        more = 2.0 ** -8 * np.abs(got) + 2.0 ** -134 if dtype == torch.bfloat16 else 0.0
+        assert (np.abs(got - ref) <= tol + more).all()
+    assert (np.abs(got - ref) > tol + 2.0 ** -8 * np.abs(got)).any()     # 2^-134 is needed
