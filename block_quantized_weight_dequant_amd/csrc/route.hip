@@ -629,13 +629,15 @@ __device__ __forceinline__ void place_row_experts(RowExperts<CAP, K> &x, const f
     load_row(x.bias, row_buffer(g.bias ? g.bias : logits, g.bias ? (size_t)E * 4 : 0), (uint32_t)x.e0 * 4);
 }
 
-// Scores lie in [0, 1], so keys span at most 1 more than the finite biases and 0
+// Scores lie in [0, 1], so keys span at most R = 1 more than the finite biases and 0
 // (hi + lo). Errors of a key: f64 (softmax): far below a step, which two roundings
-// to steps can turn into two. f32 (sigmoid): the exponent's rounding moves the score
-// by s (1 - s) |l| 2^-23.7 <= 2^-25.8, the exponential by s (1 - s) 2^-23 <= 2^-25,
-// 1 + e and the reciprocal by s 1.5 2^-23, all together 2^-22, the sum with the bias by 2^-24 (1 + |bias|); the distance and its
-// product with `unit` are within 2^-24 of the range each. Twice all that is below
-// 2^-20 + 2^-22 (1 + the largest |bias|), and so is a sum of two keys' error.
+// to steps can turn into two. f32 (sigmoid), with u = 2^-24 and B the largest |bias|:
+// the exponent's rounding moves the score by s (1 - s) |l| 2^-23.7 <= 0.3 u, the
+// exponential by s (1 - s) 2 u <= 0.5 u, 1 + e and the reciprocal by s 3 u: 3.8 u;
+// the sum with the bias by (1 + B) u; the distance from the largest key and its
+// product with `unit` by R u each. So two keys whose codes are in the wrong order are
+// less than (10 + 2 B + 4 R) u apart in them, 16 steps at most, and one step more by
+// the roundings of both to steps.
 template <int CAP, class K>
 __device__ __forceinline__ void scale_row_experts(RowExperts<CAP, K> &x)
 {
@@ -652,11 +654,11 @@ __device__ __forceinline__ void scale_row_experts(RowExperts<CAP, K> &x)
     const float range = 1.0f + (hi + lo), unit = (float)kMostSteps<CAP> * 0.999999f * __builtin_amdgcn_rcpf(range);
     x.unit = (K)unit;
     if constexpr (sizeof(K) == 4) {
-        const float err = 0x1p-20f + 0x1p-22f * (1.0f + larger(hi, lo));
+        const float most = larger(hi, lo), err = 0x1p-24f * (10.0f + 2.0f * most + 4.0f * range);
         // Four keys' errors, and the roundings of two sums and of the comparison.
-        x.margin = 0x1p-20f + 12 * 0x1p-24f * (1.0f + larger(hi, lo));
-        // Beyond 500 steps all is uncertain (the masked code is 1000 away).
-        x.blur = err * unit < 500.0f ? (uint32_t)(err * unit) + 4u : ~0u;
+        x.margin = 0x1p-20f + 12 * 0x1p-24f * (1.0f + most);
+        // Where the biases' range leaves f32 all is uncertain (the masked code is 1000 away).
+        x.blur = err * unit < 500.0f ? (uint32_t)(err * unit) + 2u : ~0u;
     } else {
         x.margin = 0x1p-48 * (double)range;
         x.blur = 2u;

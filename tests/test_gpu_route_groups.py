@@ -239,3 +239,29 @@ def test_wide_rows_with_large_biases(size):
         check(x, b, 8, True, 8, 4, 2)
         check(x, b, 15, True, 1, 1, 1)
         check(x, b, 8, False, 8, 4, 1, False, -1.5)
+
+
+@pytest.mark.parametrize("B", [0.5, 2.0, 10.0, 100.0, 3000.0])
+@pytest.mark.parametrize("E,G,top", [(256, 1, 1), (256, 8, 4), (120, 1, 1), (60, 5, 3), (512, 1, 1), (512, 8, 4)])
+def test_near_keys_under_biases_of_both_signs(E, G, top, B):
+    # Four experts with the bias B, the others with -B, some of which have scores from a
+    # fraction of f32's step at 1 + 2 B to some ten of them apart, at the edge of the
+    # choice: the keys' rounding in f32 tells nothing there.
+    g = np.random.default_rng(int(10 * B) + E)
+    T = 160
+    b = np.full(E, -B, dtype=np.float32)
+    liked = g.permutation(E)[:4]
+    b[liked] = B
+    x = (g.normal(0, 1, (T, E)) - 9).astype(np.float32)
+    rest = np.setdiff1d(np.arange(E), liked)
+    for t in range(T):
+        n = int(g.integers(2, 13))
+        near = g.permutation(rest)[:n]
+        p = g.uniform(0.3, 0.7) + g.permutation(n) * g.uniform(0.02, 3) * (1 + 2 * B) * 2.0 ** -24
+        p = np.clip(p, 0.01, 0.99)
+        x[t, near] = np.log(p / (1 - p)).astype(np.float32)
+    for k in (5, 6, 8, 11, 15):
+        if k <= top * (E // G):
+            check(x, b, k, True, G, top, 2)
+            check(x, b, k, True, G, top, 1)
+            check(x, b, k, False, G, top, 2)
