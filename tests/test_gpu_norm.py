@@ -299,3 +299,73 @@ def test_large_gamma_on_small_elements():
     q4.q4_norm(to_dev(x), to_dev(gamma), y, M, K, EPS)
     ref = plain.norm(x.astype(np.float64), gamma, float(np.float32(EPS)))
     assert (np.abs(host(y) - ref) <= 2.0 ** -21.6 * np.abs(ref) + 2.0 ** -126 + np.abs(gamma.astype(np.float64)) * 2.0 ** -149).all()
+
+
+def sampled(M, seed):
+    """The rows that are looked at: the first and last ones, and some between."""
+    r = np.random.default_rng(seed)
+    return np.unique(np.concatenate([np.arange(5), np.arange(M - 5, M), r.integers(0, M, 24)]))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M", [1024, 1025])
+@pytest.mark.parametrize("waves", [9, 10, 11, 16])
+@pytest.mark.parametrize("share", [1, 2, 3])
+def test_many_rows_of_nine_to_sixteen_wavefronts(share, waves, M, bf16):
+    # Rows that end near a wavefront's end, and the narrowest, in every form; some
+    # weights are 0 over rows of NaN; the sum in place. A sample of the rows against 64
+    # bits, all of them against calls of fewer rows (which take other kernels).
+    lanes = 512 if bf16 else 256
+    dt, tail = dtype_of(bf16), "_bf16" if bf16 else ""
+    for K in (waves * lanes - 32, (waves - 1) * lanes + 32):
+        g = torch.Generator(device=DEV).manual_seed(M + K + share)
+        x = torch.randn(M * share, K, generator=g, device=DEV).to(dt)
+        res = (3 * torch.randn(M, K, generator=g, device=DEV)).to(dt)
+        gamma = 1 + 0.2 * torch.randn(K, generator=g, device=DEV)
+        w = None
+        if share > 1:
+            w = torch.rand(M, share, generator=g, device=DEV)
+            w[torch.rand(M, share, generator=g, device=DEV) < 0.2] = 0
+            x[(w == 0).reshape(-1)] = float("nan")
+        n, nb, nf = M * K, M * (K // 32) * 34, M * -(-K // 128)
+        y32, y16, q8 = Guarded(n, torch.float32), Guarded(n, torch.bfloat16), Guarded(nb, torch.uint8)
+        f8, fs, dense = Guarded(n, torch.uint8), Guarded(nf, torch.float32), Guarded(n, dt)
+        sm = Guarded(n, dt)
+        sm.view.copy_(res.reshape(-1))
+        kw = dict(weights=w, share=share)
+        getattr(q4, "q4_norm" + tail)(x, gamma, y32.view, M, K, EPS, residual=res, **kw)
+        getattr(q4, "q8_norm" + tail)(x, gamma, q8.view, M, K, EPS, residual=res, **kw)
+        getattr(q4, "f8_norm" + tail)(x, gamma, f8.view, fs.view, M, K, EPS, residual=res, y=dense.view, **kw)
+        getattr(q4, "q4_norm" + tail)(x, gamma, y16.view, M, K, EPS, residual=sm.view, sum=sm.view, **kw)   # in place
+        torch.cuda.synchronize()
+        what = "M %d K %d share %d %s" % (M, K, share, tail)
+        for b in (y32, y16, q8, f8, fs, dense, sm):
+            assert b.guards_intact(), what
+        at = sampled(M, K)
+        pick = lambda t: t.reshape(M, -1)[torch.from_numpy(at).to(DEV)].contiguous()
+        xs = pick(x.reshape(M, share * K)).reshape(-1, K)
+        bits = (lambda t: t.view(torch.int16).cpu().numpy().view(np.uint16)) if bf16 else (lambda t: t.cpu().numpy())
+        h, size = plain.norm_sum(bits(xs), None if w is None else pick(w).cpu().numpy(), share, bits(pick(res)))
+        step = 2.0 ** -8 if bf16 else 0.0
+        got = host(pick(sm.view))
+        assert (np.abs(got - h) <= (U + step * (1 + U)) * np.abs(h) + 2.0 ** -50 * size + 2.0 ** -134).all(), what
+        ref = plain.norm(h, gamma.cpu().numpy(), EPS)
+        rms = np.sqrt((h * h).mean(1, keepdims=True) + EPS)
+        loose = 5.02 * U * np.abs(ref) + 2.0 ** -49 * size / rms * np.abs(gamma.cpu().numpy())
+        assert (np.abs(host(pick(y32.view)) - ref) <= loose + 2.0 ** -126).all(), what
+        # Every row: the same bits as from calls of 300 rows.
+        few = torch.empty(n, device=DEV)
+        few_sum = torch.empty(M, K, dtype=dt, device=DEV)
+        for m0 in range(0, M, 300):
+            m1 = min(m0 + 300, M)
+            getattr(q4, "q4_norm" + tail)(x[m0 * share:m1 * share], gamma, few[m0 * K:m1 * K], m1 - m0, K, EPS, residual=res[m0:m1],
+                                          sum=few_sum[m0:m1], weights=None if w is None else w[m0:m1], share=share)
+        assert torch.equal(few_sum.reshape(-1), sm.view), what
+        assert torch.equal(few, y32.view), what
+        assert torch.equal(y16.view, y32.view.to(torch.bfloat16)) and torch.equal(dense.view, y32.view.to(dt)), what
+        want, ws = torch.empty(nb, dtype=torch.uint8, device=DEV), torch.empty(nf, device=DEV)
+        q4.q8_quantize(y32.view.contiguous(), want)
+        assert torch.equal(q8.view, want), what
+        want = torch.empty(n, dtype=torch.uint8, device=DEV)
+        q4.f8_quantize(y32.view.contiguous(), want, ws, M, K, 1)
+        assert torch.equal(f8.view, want) and torch.equal(fs.view, ws), what
