@@ -265,3 +265,54 @@ def test_near_keys_under_biases_of_both_signs(E, G, top, B):
             check(x, b, k, True, G, top, 2)
             check(x, b, k, True, G, top, 1)
             check(x, b, k, False, G, top, 2)
+
+
+def check_many(T, E, k, sigmoid, G=1, top=1, best=1, scale=2.5, seed=0):
+    """As check, for many tokens: the definition in torch's 64-bit operations over whole
+    arrays (finite logits, no masks)."""
+    g = torch.Generator(device=DEV).manual_seed(seed + T + E)
+    x = torch.randn(T, E, generator=g, device=DEV)
+    b = 0.1 * torch.randn(E, generator=g, device=DEV)
+    ids, w, off, order = [Guarded(T * k, torch.int32), Guarded(T * k, torch.float32), Guarded(E + 1, torch.int32), Guarded(T * k, torch.int32)]
+    q4.q4_route_groups(x, b, ids.view, w.view, off.view, order.view, T, E, k, q4.Q4_SCORE_SIGMOID if sigmoid else q4.Q4_SCORE_SOFTMAX,
+                       G, top, best, True, scale)
+    torch.cuda.synchronize()
+    assert all(o.guards_intact() for o in (ids, w, off, order))
+    s = torch.sigmoid(x.double()) if sigmoid else torch.softmax(x.double(), 1)
+    key = s + b.double()
+    if top < G:
+        sums = torch.sort(key.reshape(T, G, E // G), dim=2, descending=True)[0][:, :, :best].sum(2)
+        kept = torch.zeros(T, G, dtype=torch.bool, device=DEV)
+        kept.scatter_(1, torch.sort(sums, dim=1, descending=True, stable=True)[1][:, :top], True)
+        key = torch.where(kept.repeat_interleave(E // G, 1), key, -torch.inf)
+    want = torch.sort(key, dim=1, descending=True, stable=True)[1][:, :k]
+    what = "T %d E %d k %d" % (T, E, k)
+    assert torch.equal(ids.view.reshape(T, k).long(), want), what
+    ww = s.gather(1, want)
+    ww = scale * ww / ww.sum(1, keepdim=True)
+    assert bool(((w.view.reshape(T, k).double() - ww).abs() <= (2.0 ** -24 + 2.0 ** -45) * ww).all()), what
+    flat = want.reshape(-1)
+    assert torch.equal(order.view.long(), torch.sort(flat, stable=True)[1]), what
+    counts = torch.bincount(flat, minlength=E).cpu().numpy()
+    assert np.array_equal(off.host(), np.concatenate([[0], np.cumsum(counts)])), what
+
+
+# Chunks of 33 tokens and more: a second pass of a workgroup's wavefronts, a short one;
+# past 64 a third, whose slots start over; a last chunk that ends within a pass.
+MANY = [8193, 8200, 8192 + 256 * 5 + 3, 16385, 16700, 25003, 66000]
+
+
+@pytest.mark.parametrize("T", MANY)
+@pytest.mark.parametrize("E,k,G,top,best", [(256, 8, 8, 4, 2), (64, 6, 1, 1, 1), (60, 4, 5, 2, 2), (512, 8, 8, 4, 2), (320, 15, 1, 1, 1),   # rows of lanes
+                                            (5, 2, 1, 1, 1),                                                                            # 32-bit counts
+                                            (128, 16, 8, 4, 2), (96, 6, 32, 5, 2), (256, 20, 1, 1, 1), (640, 8, 10, 4, 1)])            # a token a wavefront
+def test_many_tokens(E, k, G, top, best, T):
+    check_many(T, E, k, True, G, top, best)
+    if T in (8200, 16700):
+        check_many(T, E, k, False, G, top, best)
+
+
+def test_chunks_whose_counts_may_pass_16_bits():
+    # More than 65535 slots a chunk: 32-bit counts of eight experts and more.
+    check_many(530000, 32, 32, True)
+    check_many(1048577, 16, 16, False)
