@@ -35,6 +35,15 @@ namespace q4k {
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 constexpr int kMaxExperts = Q4_MAX_EXPERTS, kMaxTopK = Q4_MAX_TOP_K;
 
+// Order LDS traffic between the lanes of one wavefront: its LDS operations
+// execute in issue order, so it is enough that the compiler keeps them there.
+__device__ __forceinline__ void wave_lds_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float wave_sum(float v)
 {
 #pragma unroll
@@ -278,7 +287,7 @@ __device__ __forceinline__ void route_workgroup(Lds &l, uint16_t *s_ids, Tokens 
             return s_ids + (counts ? (wave * 2 + u) * kMaxTopK : (tok[u] - t0) * top_k);
         };
         tokens(tok, n, to);
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
         for (int u = 0; u < n; ++u)
             if ((tid & 63) < top_k)
                 atomicAdd(&l.cursor[to(u)[tid & 63]], 1);
@@ -425,9 +434,9 @@ __device__ __forceinline__ void choose_tokens(const float *__restrict__ logits, 
                 vals[lane + 64 * i] = there[i] ? k : -__builtin_inf();
         }
         if constexpr (GROUPED) {
-            __builtin_amdgcn_wave_barrier();
+            wave_lds_sync();
             const uint64_t kept = best_groups(vals, g, E, lanes);
-            __builtin_amdgcn_wave_barrier();
+            wave_lds_sync();
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (!(kept >> x.bit[i] & 1))
@@ -702,13 +711,13 @@ __device__ __forceinline__ uint64_t exact_keys(const float *__restrict__ row, co
         share = rcp_f64(fmax(wave_sum_f64(sum), 0x1p-1000));
     }
     const float *bias = g.bias ? g.bias : row;
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
 #pragma unroll 4
     for (int e = lane; e < E; e += 64) {
         const float v = row[e], b = g.bias ? bias[e] : 0.0f;
         l.vals[e] = (v > ninf) & (b > ninf) ? score_of<SIGMOID>(v, top, share) + (double)b : -__builtin_inf();
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
     return GROUPED ? best_groups(l.vals, g, E, lanes) : 0;
 }
 
@@ -720,7 +729,7 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
 {
     const int lane = threadIdx.x & 63, size = E / g.n_groups;
     const uint64_t kept = exact_keys<GROUPED, SIGMOID>(row, g, lanes, l, E);
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
     for (int e = lane; e < E; e += 64) {
         const double v = l.vals[e];
         const Key k = f64_key(v);
@@ -728,7 +737,7 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
         l.keys[e] = !GROUPED || (kept >> (e / size << lanes) & 1) ? key : 0u;
     }
     for (int j = 0; j < top_k; ++j) {
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
         uint64_t mine = 0;
         int at = lane;
         for (int e = lane; e < E; e += 64)
@@ -738,13 +747,13 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
         const uint32_t lo = wave_max_u32((uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
         const bool best = mine == ((uint64_t)hi << 32 | lo);
         const int id = 2 * kMaxExperts - (int)wave_max_u32(best ? (uint32_t)(2 * kMaxExperts - at) : 0u);
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
         if (lane == 0) {
             out[j] = (uint16_t)id;
             l.keys[id] = 0;
         }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
 }
 
 // Tokens by four rows of a wavefront: tok is uniform within a row, v its logits,
@@ -887,6 +896,7 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
     const bool doubt = more | ((CAP > LIST) & (offered >= LIST) & (x.n > LIST));
 
     // Lane p: candidate p, its score in f64.
+    wave_lds_sync();
     const int from = (lane & 48) + 15 - (int)(taken >> PLACE & 15u), at = PLACES - (int)(taken & (uint32_t)PLACES);
     int id = __shfl(x.e0, from) + at;
     float logit = l.logits[from * l.kPitch + (at < CAP ? at : 0)];
@@ -917,7 +927,7 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
     while (unsure) {
         const int u = __builtin_ctzll(unsure) & 48;
         unsure &= ~(0xFFFFull << u);
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
         const int t = __builtin_amdgcn_readlane(tok, u);
         const uint64_t o = reinterpret_cast<uint64_t>(out);
         uint16_t *to = reinterpret_cast<uint16_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(o >> 32), u) << 32 |
@@ -978,7 +988,7 @@ __global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restr
             fetch(t + 4 * kRowWaves);
         if (mine < t1 && (lane & 15) < top_k)
             atomicAdd(&l.cursor[out[lane & 15]], 1);
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
     }
     route_sort(l, s_ids, offsets, order, counts, T, E, top_k, chunk, bits);
 }
