@@ -72,9 +72,9 @@ __device__ __forceinline__ void store_piece(uint16_t *p, const float (&v)[P])
 // rounding, to be rounded to a code. s in [2^-90, 2^90]: from the correctly
 // rounded reciprocal and one step with the exact remainder (an FMA), which leaves
 // the quotient on the side of every midpoint between two E4M3 values, and of
-// every k + 1/2 up to 128, on which the correctly rounded one is, or on it: checked
-// for all significands of s, all midpoints (5 and 8 bits) and the five x nearest
-// to each product, the only ones whose quotients come within 2 units in the last
+// every k + 1/2 up to 128, on which the correctly rounded one is, or on it if that
+// is: checked for all significands of s, all midpoints (of up to 8 bits) and the nine
+// x nearest to each product, beyond which no quotient comes within a unit in the last
 // place. No intermediate leaves the normal range here but where the quotient is
 // far below the smallest code. The remainder of -0 is +0, which would lose its
 // sign: the quotient takes x's. Four operations an element; a division takes
@@ -160,7 +160,8 @@ __device__ __forceinline__ float lanes_max(float v)
 }
 
 // max / c, correctly rounded, for c = 448 or 127: the quotient by the reciprocal
-// and one step with the exact remainder, checked for every significand.
+// and one step with the exact remainder, checked for every significand (both checks:
+// tests/test_quotients.py).
 __device__ __forceinline__ float scale_of(float max, float c)
 {
     if (!(max >= 0x1p-90f && max <= 0x1p120f))
