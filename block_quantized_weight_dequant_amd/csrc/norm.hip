@@ -25,8 +25,9 @@
 namespace q4k {
 
 // SUB rows share a wavefront (then RW and V are 1): rows of up to 64 / SUB pieces,
-// the heads of an attention layer (65536 x 128 bfloat16: 7.8 us, 4.3 TB/s; a wavefront
-// a row 17.4).
+// such as the heads of an attention layer in an array of their own (65536 x 128
+// bfloat16 without a residual: 7.8 us, 4.3 TB/s; a wavefront a row 17.4; with a
+// residual and the sum 13.4, 5.0 TB/s).
 template <class T, RowForm O, bool COMBINE, int RW, int V, int SUB>
 __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, double inv_k, int first)
 {
@@ -102,10 +103,15 @@ __global__ __launch_bounds__(RW < 4 ? 256 : 64 * RW) void k_norm(NormArgs a, dou
                         acc[i][k] = fma((double)w[n], (double)(!kSkip && w[n] == 0.0f ? 0.0f : v[n][i][k]), acc[i][k]);
             }
         };
-        // N rows are in flight together, as many as leave the registers to two workgroups
-        // or more. Against one row fetched ahead of the one that is added (us, to E4M3):
-        // 976 x 512 bfloat16 of 8 4.8, 7.4; 3906 x 2048 f32 of 2 23.1, 25.1; 558 x 7168
-        // bfloat16 of 4 13.8, 15.2; at worst 279 x 7168 of 8 13.9, 12.3.
+        // N rows are in flight together, by the row's width alone: as many as leave the
+        // registers to two workgroups a compute unit or more, also where there are fewer
+        // workgroups than compute units (64 x 7168 bfloat16 of 8, two in flight and 50 of
+        // 128 registers used, 7.5 us, some 4 for its bytes). Against one row fetched ahead
+        // of the one that is added (us, to E4M3): 976 x 512 bfloat16 of 8 4.8, 7.4; 3906 x
+        // 2048 f32 of 2 23.1, 25.1; 558 x 7168 bfloat16 of 4 13.8, 15.2; at worst 279 x
+        // 7168 of 8 13.4, 12.3. With eight f32 pieces a lane, or four of bfloat16 (K >
+        // 16384), the f64 sums alone fill the registers and some are spilled: 139 x 28672
+        // of 4 to E4M3 f32 32.8 us (21 to 39 registers), bfloat16 15.8 (1 to 5).
         constexpr int N = V == 1 ? (P == 4 ? 8 : RW < 10 ? 4 : 2) : V == 2 ? 2 : 1;
         int j = 0;
         for (; j + N <= a.share; j += N)

@@ -768,7 +768,9 @@ __device__ __forceinline__ void choose_exactly(const float *__restrict__ row, co
 // moves) for four tokens at a time, and one head taken off. Codes near enough to be
 // in the wrong order are taken along, and ordered by f64 keys, which the weights need
 // of each candidate anyway. Where that does not settle it (more than 16 candidates)
-// the token is chosen again, exactly.
+// the token is chosen again, exactly: so are all tokens whose scores agree in f32,
+// as saturated ones without a bias do (logits all above 14 or below -14: 32 tokens 8 of
+// 256 45.5 us for 8.6, 8192 tokens 52.8 for 15.7).
 template <int CAP, bool GROUPED, bool SIGMOID, class K>
 __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__restrict__ logits, const RouteGroups &g,
                                             const RouteRows &r, const RowExperts<CAP, K> &x, RowLds<CAP> &l, int lanes,
@@ -993,7 +995,8 @@ __global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restr
     route_sort(l, s_ids, offsets, order, counts, T, E, top_k, chunk, bits);
 }
 
-// Every size: one token a wavefront at a time.
+// Every size: one token a wavefront at a time. 16 experts a lane (above 256) spill 41
+// (GROUPED: 84) registers: 32 / 8192 tokens 8 of 1024 in 8 groups 54 / 93 us.
 template <int V, bool GROUPED>
 __global__ __launch_bounds__(kRouteThreads) void k_route_groups(const float *__restrict__ logits,
                                                                RouteGroups g, int lanes,

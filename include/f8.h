@@ -16,7 +16,7 @@
  * that overlap no input, asynchronous work on `stream`, nothing allocated, no
  * state kept, the same Q4_* status codes, empty problems Q4_OK. Every entry
  * point may be captured in a HIP graph, needs no workspace, and is
- * deterministic. Inputs are finite.
+ * deterministic. Inputs are finite, where an entry point states nothing else.
  */
 #ifndef Q4MI_F8_H
 #define Q4MI_F8_H

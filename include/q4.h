@@ -34,7 +34,8 @@
  *     nothing is written. Device faults surface at the caller's next
  *     synchronization. An empty problem (a zero dimension or element count)
  *     returns Q4_OK and launches nothing; its pointers may be NULL.
- *   - Inputs are finite; results for NaN or infinite inputs are unspecified.
+ *   - Inputs are finite; results for NaN or infinite inputs are unspecified where
+ *     an entry point does not state them.
  */
 #ifndef Q4MI_Q4_H
 #define Q4MI_Q4_H
