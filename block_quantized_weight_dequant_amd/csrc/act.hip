@@ -6,8 +6,8 @@
 // output go to the blocks of all rows in turn, so that no lane idles at the end of
 // a row and a block's maximum stays within its lanes. With whole wavefronts, or
 // workgroups, in one row instead, 4096 x 2816 bfloat16 to E4M3 takes 13.4 us, or
-// 16.9, for 12.0. 4096 x 14336 bfloat16 to E4M3: 49.2 us, 6.0 TB/s; 1001 x 14336 f32
-// to bfloat16 24.5 us, 5.9 TB/s; plain streams of the same bytes take 47.6 and 24.1.
+// 16.9, for 12.0. 4096 x 14336 bfloat16 to E4M3: 48.9 us, 6.0 TB/s; 1001 x 14336 f32
+// to bfloat16 24.1 us, 5.9 TB/s; plain streams of the same bytes take 47.6 and 24.1.
 //
 // f(g) = g / (1 + exp(-z)), z = g for SiLU and 2 sqrt(2 / pi) (g + 0.044715 g^3)
 // for GELU (where (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))): one exponential and one

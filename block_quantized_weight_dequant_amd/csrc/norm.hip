@@ -14,7 +14,7 @@
 // one row of some 10^7. f32 sums instead are 1 to 4 % faster on every size measured.
 //
 // Measured, with cold rows: 2048 x 4096, two experts' f32 rows and a residual to
-// bfloat16, 25.8 us, 5.9 TB/s (a plain stream of the same bytes 25.9); 1001 x 4096
+// bfloat16, 25.9 us, 5.9 TB/s (a plain stream of the same bytes 25.9); 1001 x 4096
 // bfloat16 to E4M3 7.6 us (5.4); one row 3.0 us (2.2).
 #include "f64.h"
 #include "launch.h"

@@ -954,8 +954,8 @@ __device__ __forceinline__ void choose_rows(float (&v)[CAP], const float *__rest
 }
 
 // Up to 512 experts in rows of lanes, CAP or fewer a lane, four tokens a wavefront at
-// a time: 32 / 2048 / 8192 tokens of 512 experts in 8 groups 12.9 / 19.9 / 24.0 us
-// (48.3 / 55.5 / 79.6 with a wavefront a token); 32 / 8192 of 256 8.8 / 16.4.
+// a time: 32 / 2048 / 8192 tokens of 512 experts in 8 groups 12.9 / 19.9 / 22.7 us
+// (48.3 / 55.5 / 79.6 with a wavefront a token); 32 / 8192 of 256 8.6 / 15.7.
 template <int CAP, bool GROUPED, bool SIGMOID>
 __global__ __launch_bounds__(kRowThreads) void k_route_rows(const float *__restrict__ logits, RouteGroups g,
                                                            RouteRows r, int lanes, int *__restrict__ ids,
