@@ -256,3 +256,30 @@ def test_the_stated_bound_of_small_results(bf16, gelu):
         more = 2.0 ** -8 * np.abs(got) + 2.0 ** -134 if dtype == torch.bfloat16 else 0.0
         assert (np.abs(got - ref) <= tol + more).all()
     assert (np.abs(got - ref) > tol + 2.0 ** -8 * np.abs(got)).any()     # 2^-134 is needed
+
+
+@pytest.mark.parametrize("K", [2 ** 22, 2 ** 22 - 32, 2 ** 21 + 160])
+def test_widest_rows(K):
+    # Past 256 rows of the widest a second launch; the blocks of a row are those of its
+    # pieces in calls of 128 (or 32) columns.
+    M = 259
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV).normal_()
+    up = torch.empty(M, K, dtype=torch.bfloat16, device=DEV).normal_()
+    q, s = torch.zeros(M, K, dtype=torch.uint8, device=DEV), torch.zeros(M, -(-K // 128), device=DEV)
+    q4.f8_act_bf16(x, up, q, s, M, K)
+    blob = torch.zeros(M, K // 32 * 34, dtype=torch.uint8, device=DEV)
+    q4.q8_act_bf16(x, up, blob, M, K)
+    for m in (0, 1, 127, 255, 256, 258):
+        n = K // 128
+        want, ws = torch.empty(n, 128, dtype=torch.uint8, device=DEV), torch.empty(n, device=DEV)
+        g, u = x[m, :128 * n].reshape(n, 128), up[m, :128 * n].reshape(n, 128)
+        q4.f8_act_bf16(g, u, want, ws, n, 128)
+        assert torch.equal(q[m, :128 * n].reshape(n, 128), want) and torch.equal(s[m, :n], ws), m
+        if K % 128:
+            g, u = x[m:m + 1, 128 * n:].contiguous(), up[m:m + 1, 128 * n:].contiguous()
+            want, ws = torch.empty(K % 128, dtype=torch.uint8, device=DEV), torch.empty(1, device=DEV)
+            q4.f8_act_bf16(g, u, want, ws, 1, K % 128)
+            assert torch.equal(q[m, 128 * n:], want) and torch.equal(s[m, n:], ws), m
+        w8 = torch.empty(K // 32 * 34, dtype=torch.uint8, device=DEV)
+        q4.q8_act_bf16(x[m].reshape(-1, 32), up[m].reshape(-1, 32), w8, K // 32, 32)
+        assert torch.equal(blob[m], w8), m

@@ -369,3 +369,21 @@ def test_many_rows_of_nine_to_sixteen_wavefronts(share, waves, M, bf16):
         want = torch.empty(n, dtype=torch.uint8, device=DEV)
         q4.f8_quantize(y32.view.contiguous(), want, ws, M, K, 1)
         assert torch.equal(f8.view, want) and torch.equal(fs.view, ws), what
+
+
+def test_rows_past_a_launch():
+    # 2^23 workgroups of 16 rows of 32 columns are 2^27 rows; the rows next to the
+    # boundary and the last ones are what calls of their own give, the sum in place.
+    M, K = 2 ** 27 + 21, 32
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV).normal_()
+    res = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    y, gamma = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV), torch.ones(K, device=DEV)
+    q4.q4_norm_bf16(x, gamma, y, M, K, EPS, residual=res, sum=res)
+    for first, n in ((0, 20), (2 ** 27 - 24, 45), (2 ** 26, 64)):
+        want, ws = torch.empty(n, K, dtype=torch.bfloat16, device=DEV), torch.empty(n, K, dtype=torch.bfloat16, device=DEV)
+        q4.q4_norm_bf16(x[first:first + n], gamma, want, n, K, EPS, residual=torch.ones_like(ws), sum=ws)
+        assert torch.equal(y[first:first + n], want) and torch.equal(res[first:first + n], ws), first
+    # No row was added twice, or not at all.
+    step = 2 ** 22
+    for m in range(0, M, step):
+        assert torch.equal(res[m:m + step], (x[m:m + step].float() + 1.0).to(torch.bfloat16)), m
